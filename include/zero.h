@@ -473,6 +473,135 @@ zero_status zero_memory_report(int64_t psi, int32_t n_ranks, int32_t align,
                                double formula_bytes[4], int64_t actual_bytes[4],
                                int64_t comm_elems[4]);
 
+/* ----------------------------------------------------------------------
+ * The head of a training step: what stands between a model's last layer and
+ * the flat gradients the calls above start from.  The pages take the gradients
+ * as given; these calls make them: the residual addition and RMS norm before
+ * the vocabulary matrix, the softmax cross entropy against that matrix, their
+ * gradients, and the global norm of a list of gradient tensors with the
+ * clipped gradients packed into the flat buffer.
+ *
+ * They need no plan and keep no state: scratch is a caller-owned workspace
+ * whose size a host call gives, contents undefined between calls.  Calls on
+ * different streams need workspaces of their own.  Matrices are row-major, rows
+ * `stride` elements apart; dim and every stride must be multiples of 8 and
+ * every pointer 16-byte aligned (ZERO_EALIGN), strides at least the row's
+ * length (ZERO_EINVAL), dim in [8, ZERO_HEAD_MAX_DIM].  Inputs and outputs must
+ * not overlap unless a call says so.  lp is the type of every matrix.  All
+ * asynchronous on `stream`, capturable into a CUDA graph, results the same
+ * bits from run to run.  Sums, statistics and products are held in float or
+ * wider; what is rounded to lp on the way is named below.
+ */
+#define ZERO_HEAD_MAX_DIM 32768
+
+/* Residual addition and root-mean-square norm of each of n_rows rows:
+ *   s[i] = x[i] + residual[i]  (residual NULL: s = x)
+ *   out[i] = lp(s[i] * rstd * weight[i]),  rstd = (mean(s^2) + eps)^(-1/2)
+ *   sum[i] = lp(s[i])          (sum NULL: not written)
+ * out is computed from the unrounded s.  weight: dim elements.  sum may be
+ * residual or x itself (in place).  eps >= 0 and finite. */
+zero_status zero_norm_forward(const void *x, int64_t x_stride, const void *residual,
+                              int64_t residual_stride, const void *weight, float eps,
+                              int64_t n_rows, int32_t dim, zero_lp lp, void *out,
+                              int64_t out_stride, void *sum, int64_t sum_stride, void *stream);
+
+/* The same with the normalised row in 8 bits, in the formats of the quantized
+ * gather: per block of ZERO_QUANT_BLOCK elements of a row (the last block of a
+ * row may be shorter) the codes and scale that zero_quantize_shard documents,
+ * taken from the unrounded values s[i] * rstd * weight[i].  format:
+ * ZERO_QUANT_INT8 or ZERO_QUANT_FP8_E4M3.  codes: n_rows * dim bytes, scales:
+ * n_rows * ceil(dim / ZERO_QUANT_BLOCK) floats, both without row padding. */
+zero_status zero_norm_forward_quantized(const void *x, int64_t x_stride, const void *residual,
+                                        int64_t residual_stride, const void *weight, float eps,
+                                        int64_t n_rows, int32_t dim, zero_lp lp, int32_t format,
+                                        int8_t *codes, float *scales, void *sum,
+                                        int64_t sum_stride, void *stream);
+
+/* out[i] = lp(code[i] * scale of its block), for codes and scales laid out as
+ * zero_norm_forward_quantized writes them. */
+zero_status zero_dequantize_rows(const int8_t *codes, const float *scales, int32_t format,
+                                 int64_t n_rows, int32_t dim, zero_lp lp, void *out,
+                                 int64_t out_stride, void *stream);
+
+/* Gradients of zero_norm_forward.  sum: its second output (the rounded s; rstd
+ * is computed again from it); grad_out: gradient of out; grad_sum (nullable):
+ * gradient that reaches s by its other uses.
+ *   grad_in[i]     = lp(rstd * (w[i] gy[i] - s[i] rstd^2 mean(w gy s)) + gs[i])
+ *   grad_weight[i] = lp(sum over rows of gy[i] s[i] rstd)
+ * grad_in is the gradient of x and of residual alike; it may be grad_out or
+ * grad_sum itself.  n_rows = 0 writes a zero grad_weight.  workspace: at least
+ * the bytes zero_norm_backward_workspace gives. */
+zero_status zero_norm_backward_workspace(int64_t n_rows, int32_t dim, int64_t *bytes);
+zero_status zero_norm_backward(const void *sum, int64_t sum_stride, const void *weight,
+                               const void *grad_out, int64_t grad_out_stride,
+                               const void *grad_sum, int64_t grad_sum_stride, float eps,
+                               int64_t n_rows, int32_t dim, zero_lp lp, void *grad_in,
+                               int64_t grad_in_stride, void *grad_weight, void *workspace,
+                               int64_t workspace_bytes, void *stream);
+
+/* Softmax cross entropy of hidden states against a vocabulary matrix, without
+ * keeping the logits z = hidden . weight^T (n_tokens x vocab):
+ *   lse[t]  = log(sum over v of exp(z[t][v]))
+ *   loss[t] = lse[t] - z[t][target[t]], or 0 where target[t] == ignore
+ * hidden: n_tokens rows, weight: vocab rows, of dim lp elements; target:
+ * n_tokens int64 (8-byte aligned); loss, lse: n_tokens floats.  The vocabulary
+ * is taken in pieces; only each piece's maximum and sum of exponentials are
+ * written.  A target outside [0, vocab) that is not `ignore` gives a NaN loss,
+ * no gradient, and sets bit ZERO_LOSS_BAD_TARGET of *status.
+ * status: one int32 of device memory, only ever OR-ed into: bit
+ * ZERO_LOSS_TIMEOUT is set by a kernel whose bounded wait for its copies or
+ * products gave up (its outputs are then not valid).  The caller clears it.
+ * n_tokens in [0, 2^31 - 2^16), vocab in [1, 2^31 - 2^16). */
+#define ZERO_LOSS_TIMEOUT 1
+#define ZERO_LOSS_BAD_TARGET 2
+zero_status zero_loss_workspace(int64_t n_tokens, int64_t vocab, int32_t dim,
+                                int64_t *forward_bytes, int64_t *backward_bytes);
+zero_status zero_loss_forward(const void *hidden, int64_t hidden_stride, const void *weight,
+                              int64_t weight_stride, const int64_t *target, int64_t ignore,
+                              int64_t n_tokens, int64_t vocab, int32_t dim, zero_lp lp,
+                              float *loss, float *lse, int32_t *status, void *workspace,
+                              int64_t workspace_bytes, void *stream);
+
+/* Gradients of sum over t of grad_loss[t] * loss[t] (grad_loss: n_tokens
+ * floats: the upstream gradient, e.g. loss scale / number of tokens):
+ *   q[t][v] = grad_loss[t] * (exp(z[t][v] - lse[t]) - [v == target[t]])
+ *   grad_hidden = lp(q . weight)        (n_tokens x dim)
+ *   grad_weight = lp(q^T . hidden)      (vocab x dim)
+ * lse: as zero_loss_forward wrote it.  An ignored token's grad_hidden is zero
+ * and it adds nothing to grad_weight, whatever its hidden state holds.  The
+ * logits are computed again, a piece of the vocabulary at a time; q is rounded
+ * to lp for the two products, relative to the largest finite |grad_loss| (so a
+ * gradient of any size fits fp16), whose sums are float. */
+zero_status zero_loss_backward(const void *hidden, int64_t hidden_stride, const void *weight,
+                               int64_t weight_stride, const int64_t *target, int64_t ignore,
+                               int64_t n_tokens, int64_t vocab, int32_t dim, zero_lp lp,
+                               const float *lse, const float *grad_loss, void *grad_hidden,
+                               int64_t grad_hidden_stride, void *grad_weight,
+                               int64_t grad_weight_stride, int32_t *status, void *workspace,
+                               int64_t workspace_bytes, void *stream);
+
+/* The global norm over a list of gradient tensors, and the clipped gradients:
+ *   norm = sqrt(sum over every element of g^2) / loss_scale
+ *   coef = max_norm / (norm + 1e-6) if max_norm > 0 and that is < 1, else 1
+ *          (the rule of zero_adam_step); 1 when an element is not finite
+ *   out[i][k] = round(grads[i][k] * coef)
+ * grads[i]: lens[i] contiguous elements of `dtype` (ZERO_FP16, ZERO_BF16 or
+ * ZERO_FP32); grads and out need only be aligned to their element, so out may
+ * point into a flat buffer whose tensors lie back to back (out[i] = flat +
+ * tensor_offsets[i] of zero_plan_query).  out[i] may be grads[i] (in place)
+ * but must not overlap any grads otherwise; out NULL: norm only.  lens[i] may
+ * be 0 (the pointers are then ignored).  The gradients keep their loss scale.
+ * norm, coef: one float each, nonfinite: one int32 (1 if any element is not
+ * finite), device memory, 4-byte aligned, any may be NULL.  The sum is exact
+ * to float rounding over the whole range of the type (partial sums in double).
+ * workspace: at least the bytes zero_clip_workspace gives. */
+#define ZERO_FP32 2
+zero_status zero_clip_workspace(int32_t n_tensors, const int64_t *lens, int64_t *bytes);
+zero_status zero_clip_gradients(int32_t n_tensors, const void *const *grads, const int64_t *lens,
+                                int32_t dtype, void *const *out, float loss_scale, float max_norm,
+                                float *norm, float *coef, int32_t *nonfinite, void *workspace,
+                                int64_t workspace_bytes, void *stream);
+
 /* Frees the plan and its device scratch, after waiting for the plan's own
  * device work (the whole device once one of its calls was captured into a
  * graph).  NULL is allowed. */

@@ -22,6 +22,9 @@ ZERO_FP16, ZERO_BF16 = 0, 1
 ZERO_MAX_RANKS = 1024
 ZERO_NORM_TILE = 4096
 ZERO_QUANT_INT8, ZERO_QUANT_FP8_E4M3 = 0, 1
+ZERO_FP32 = 2                     # an element type of zero_clip_gradients only
+ZERO_HEAD_MAX_DIM = 32768
+ZERO_LOSS_TIMEOUT, ZERO_LOSS_BAD_TARGET = 1, 2
 
 # every exported entry point of include/zero.h, with its ctypes signature
 _i32, _i64, _f32, _f64, _vp = C.c_int32, C.c_int64, C.c_float, C.c_double, C.c_void_p
@@ -55,6 +58,22 @@ SIGNATURES = {
     "zero_gather_layer_quantized": (_i32, [_vp, _i32, _vp, _vp, _vp, _vp]),
     "zero_reduce_partition_noalloc": (_i32, [_i32, _i32, _vp, _i64, _f32, _vp, _vp, _vp, _vp]),
     "zero_memory_report": (_i32, [_i64, _i32, _i32, _vp, _vp, _vp]),
+    "zero_norm_forward": (_i32, [_vp, _i64, _vp, _i64, _vp, _f32, _i64, _i32, _i32, _vp, _i64, _vp,
+                                 _i64, _vp]),
+    "zero_norm_forward_quantized": (_i32, [_vp, _i64, _vp, _i64, _vp, _f32, _i64, _i32, _i32, _i32,
+                                           _vp, _vp, _vp, _i64, _vp]),
+    "zero_dequantize_rows": (_i32, [_vp, _vp, _i32, _i64, _i32, _i32, _vp, _i64, _vp]),
+    "zero_norm_backward_workspace": (_i32, [_i64, _i32, _vp]),
+    "zero_norm_backward": (_i32, [_vp, _i64, _vp, _vp, _i64, _vp, _i64, _f32, _i64, _i32, _i32, _vp,
+                                  _i64, _vp, _vp, _i64, _vp]),
+    "zero_loss_workspace": (_i32, [_i64, _i64, _i32, _vp, _vp]),
+    "zero_loss_forward": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i32, _i32, _vp, _vp,
+                                 _vp, _vp, _i64, _vp]),
+    "zero_loss_backward": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i32, _i32, _vp, _vp,
+                                  _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp]),
+    "zero_clip_workspace": (_i32, [_i32, _vp, _vp]),
+    "zero_clip_gradients": (_i32, [_i32, _vp, _vp, _i32, _vp, _f32, _f32, _vp, _vp, _vp, _vp, _i64,
+                                   _vp]),
     "zero_plan_destroy": (None, [_vp]),
     "zero_last_error": (C.c_char_p, []),
 }
@@ -324,3 +343,98 @@ def zero_memory_report(psi: int, n_ranks: int, align: int = 1):
     _check(load().zero_memory_report(psi, n_ranks, align, _ptr(formula), _ptr(actual),
                                      _ptr(comm)), "zero_memory_report")
     return formula, actual, comm
+
+
+# ---- the head of a training step ---------------------------------------------
+
+def zero_norm_forward(x, x_stride: int, residual, residual_stride: int, weight, eps: float,
+                      n_rows: int, dim: int, lp: int, out, out_stride: int, sum_out,
+                      sum_stride: int, stream=None):
+    _check(load().zero_norm_forward(_ptr(x), x_stride, _ptr(residual), residual_stride, _ptr(weight),
+                                    eps, n_rows, dim, lp, _ptr(out), out_stride, _ptr(sum_out),
+                                    sum_stride, _stream(stream)), "zero_norm_forward")
+
+
+def zero_norm_forward_quantized(x, x_stride: int, residual, residual_stride: int, weight, eps: float,
+                                n_rows: int, dim: int, lp: int, fmt: int, codes, scales, sum_out,
+                                sum_stride: int, stream=None):
+    _check(load().zero_norm_forward_quantized(_ptr(x), x_stride, _ptr(residual), residual_stride,
+                                              _ptr(weight), eps, n_rows, dim, lp, fmt, _ptr(codes),
+                                              _ptr(scales), _ptr(sum_out), sum_stride,
+                                              _stream(stream)), "zero_norm_forward_quantized")
+
+
+def zero_dequantize_rows(codes, scales, fmt: int, n_rows: int, dim: int, lp: int, out,
+                         out_stride: int, stream=None):
+    _check(load().zero_dequantize_rows(_ptr(codes), _ptr(scales), fmt, n_rows, dim, lp, _ptr(out),
+                                       out_stride, _stream(stream)), "zero_dequantize_rows")
+
+
+def zero_norm_backward_workspace(n_rows: int, dim: int) -> int:
+    need = _i64()
+    _check(load().zero_norm_backward_workspace(n_rows, dim, C.byref(need)),
+           "zero_norm_backward_workspace")
+    return need.value
+
+
+def zero_norm_backward(sum_in, sum_stride: int, weight, grad_out, grad_out_stride: int, grad_sum,
+                       grad_sum_stride: int, eps: float, n_rows: int, dim: int, lp: int, grad_in,
+                       grad_in_stride: int, grad_weight, workspace, workspace_bytes: int,
+                       stream=None):
+    _check(load().zero_norm_backward(_ptr(sum_in), sum_stride, _ptr(weight), _ptr(grad_out),
+                                     grad_out_stride, _ptr(grad_sum), grad_sum_stride, eps, n_rows,
+                                     dim, lp, _ptr(grad_in), grad_in_stride, _ptr(grad_weight),
+                                     _ptr(workspace), workspace_bytes, _stream(stream)),
+           "zero_norm_backward")
+
+
+def zero_loss_workspace(n_tokens: int, vocab: int, dim: int):
+    """(forward bytes, backward bytes)."""
+    fwd, bwd = _i64(), _i64()
+    _check(load().zero_loss_workspace(n_tokens, vocab, dim, C.byref(fwd), C.byref(bwd)),
+           "zero_loss_workspace")
+    return fwd.value, bwd.value
+
+
+def zero_loss_forward(hidden, hidden_stride: int, weight, weight_stride: int, target, ignore: int,
+                      n_tokens: int, vocab: int, dim: int, lp: int, loss, lse, status, workspace,
+                      workspace_bytes: int, stream=None):
+    _check(load().zero_loss_forward(_ptr(hidden), hidden_stride, _ptr(weight), weight_stride,
+                                    _ptr(target), ignore, n_tokens, vocab, dim, lp, _ptr(loss),
+                                    _ptr(lse), _ptr(status), _ptr(workspace), workspace_bytes,
+                                    _stream(stream)), "zero_loss_forward")
+
+
+def zero_loss_backward(hidden, hidden_stride: int, weight, weight_stride: int, target, ignore: int,
+                       n_tokens: int, vocab: int, dim: int, lp: int, lse, grad_loss, grad_hidden,
+                       grad_hidden_stride: int, grad_weight, grad_weight_stride: int, status,
+                       workspace, workspace_bytes: int, stream=None):
+    _check(load().zero_loss_backward(_ptr(hidden), hidden_stride, _ptr(weight), weight_stride,
+                                     _ptr(target), ignore, n_tokens, vocab, dim, lp, _ptr(lse),
+                                     _ptr(grad_loss), _ptr(grad_hidden), grad_hidden_stride,
+                                     _ptr(grad_weight), grad_weight_stride, _ptr(status),
+                                     _ptr(workspace), workspace_bytes, _stream(stream)),
+           "zero_loss_backward")
+
+
+def zero_clip_workspace(lens) -> int:
+    ln = np.ascontiguousarray(lens, np.int64)
+    need = _i64()
+    _check(load().zero_clip_workspace(int(ln.size), _ptr(ln), C.byref(need)), "zero_clip_workspace")
+    return need.value
+
+
+def zero_clip_gradients(grads, lens, dtype: int, out, loss_scale: float, max_norm: float, norm, coef,
+                        nonfinite, workspace, workspace_bytes: int, stream=None):
+    """grads, out: one tensor or address per gradient (out None: norm only), or
+    uint64 arrays of addresses; lens: their element counts."""
+    ln = np.ascontiguousarray(lens, np.int64)
+    g = grads if isinstance(grads, np.ndarray) else np.array([_ptr(x) or 0 for x in grads], np.uint64)
+    o = out if out is None or isinstance(out, np.ndarray) else np.array([_ptr(x) or 0 for x in out],
+                                                                         np.uint64)
+    if g.size != ln.size or (o is not None and o.size != ln.size):
+        raise ValueError("grads, lens and out must have one entry per tensor")
+    _check(load().zero_clip_gradients(int(ln.size), _ptr(g), _ptr(ln), dtype, _ptr(o), loss_scale,
+                                      max_norm, _ptr(norm), _ptr(coef), _ptr(nonfinite),
+                                      _ptr(workspace), workspace_bytes, _stream(stream)),
+           "zero_clip_gradients")

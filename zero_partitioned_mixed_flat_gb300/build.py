@@ -41,7 +41,7 @@ def _sources():
 
 def _fingerprint(srcs) -> str:
     h = hashlib.sha256()
-    for f in srcs + sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".h")) \
+    for f in srcs + sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))) \
             + [os.path.join(INCLUDE, "zero.h"), os.path.abspath(__file__)]:
         h.update(f.encode())
         with open(f, "rb") as fh:
