@@ -554,6 +554,10 @@ zero_status zero_norm_backward(const void *sum, int64_t sum_stride, const void *
  * n_tokens in [0, 2^31 - 2^16), vocab in [1, 2^31 - 2^16). */
 #define ZERO_LOSS_TIMEOUT 1
 #define ZERO_LOSS_BAD_TARGET 2
+/* Bound on each device-side wait of the loss calls launched from now on, in SM
+ * clock cycles (default 4e9, about two seconds); 0 gives up at once where a
+ * wait is not already over (used to test that path).  Process-wide.  Host only. */
+zero_status zero_loss_set_wait_limit(int64_t cycles);
 zero_status zero_loss_workspace(int64_t n_tokens, int64_t vocab, int32_t dim,
                                 int64_t *forward_bytes, int64_t *backward_bytes);
 zero_status zero_loss_forward(const void *hidden, int64_t hidden_stride, const void *weight,

@@ -66,6 +66,7 @@ SIGNATURES = {
     "zero_norm_backward_workspace": (_i32, [_i64, _i32, _vp]),
     "zero_norm_backward": (_i32, [_vp, _i64, _vp, _vp, _i64, _vp, _i64, _f32, _i64, _i32, _i32, _vp,
                                   _i64, _vp, _vp, _i64, _vp]),
+    "zero_loss_set_wait_limit": (_i32, [_i64]),
     "zero_loss_workspace": (_i32, [_i64, _i64, _i32, _vp, _vp]),
     "zero_loss_forward": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i32, _i32, _vp, _vp,
                                  _vp, _vp, _i64, _vp]),
@@ -386,6 +387,10 @@ def zero_norm_backward(sum_in, sum_stride: int, weight, grad_out, grad_out_strid
                                      dim, lp, _ptr(grad_in), grad_in_stride, _ptr(grad_weight),
                                      _ptr(workspace), workspace_bytes, _stream(stream)),
            "zero_norm_backward")
+
+
+def zero_loss_set_wait_limit(cycles: int):
+    _check(load().zero_loss_set_wait_limit(cycles), "zero_loss_set_wait_limit")
 
 
 def zero_loss_workspace(n_tokens: int, vocab: int, dim: int):

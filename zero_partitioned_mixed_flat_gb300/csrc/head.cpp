@@ -183,6 +183,12 @@ zero_status zero_norm_backward(const void *sum, int64_t sum_stride, const void *
     return launched(zk::launch_norm_backward(a, static_cast<cudaStream_t>(stream)), "norm backward kernel launch");
 }
 
+zero_status zero_loss_set_wait_limit(int64_t cycles) {
+    if (cycles < 0) return refuse(ZERO_EINVAL, "cycles < 0");
+    zk::set_loss_wait(cycles);
+    return ZERO_OK;
+}
+
 zero_status zero_loss_workspace(int64_t n_tokens, int64_t vocab, int32_t dim, int64_t *forward_bytes,
                                 int64_t *backward_bytes) {
     TRY(loss_shape(n_tokens, vocab, dim, ZERO_BF16));

@@ -1,232 +1,939 @@
 // loss.cu -- softmax cross entropy of hidden states against a vocabulary
 // matrix, without keeping the logits, and its gradients (sm_103a).
+//
+// With H the hidden states [T, D], W the matrix [V, D], y the targets:
+//   z = H W^T,  lse[t] = log sum_v exp(z[t][v]),  loss[t] = lse[t] - z[t][y[t]]
+//   q[t][v] = g[t] (exp(z[t][v] - lse[t]) - [v == y[t]]),  gH = q W,  gW = q^T H
+// Forward is one product whose tiles are reduced to a maximum and a sum of
+// exponentials per row as they leave the tensor cores.  Backward takes the
+// vocabulary in pieces: a piece's logits again, q of the piece in lp, then the
+// two products that use it.  So 2 T D V operations forward and 6 T D V
+// backward, and no buffer holds more than a piece.
+//
+// All four products run in one kernel (loss_products): pairs of CTAs, each pair
+// one 256 x 256 tile, tcgen05.mma on 256 x 256 x 16 with operands that TMA
+// places in shared memory and sums that stay in tensor memory.
 #include "head_internal.h"
 #include "launch.h"
 #include "zero.h"
 #include "zero_internal.h"
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 
 namespace zk {
 namespace {
 
-constexpr int kT = 64;    // tile: kT x kT outputs, kK products at a time
-constexpr int kK = 16;
-constexpr int kThreads = 256;  // 16 x 16 threads, 4 x 4 outputs each
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
-template <bool BF16>
-__device__ __forceinline__ float lp_get(const void *p, long long i) {
-    if constexpr (BF16) return __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
-    return __half2float(static_cast<const __half *>(p)[i]);
-}
+constexpr int kTileM = 256, kTileN = 256;  // outputs of a pair of CTAs
+constexpr int kHalf = 128;                 // rows of A, and of B, that each CTA loads
+constexpr int kTileK = 64;                 // 128 bytes: one swizzle row
+constexpr int kStages = 6;
+constexpr int kOperandBytes = kHalf * kTileK * 2;
+constexpr int kStageBytes = 2 * kOperandBytes;
+constexpr int kBoxBytes = 64 * kTileK * 2;  // a 64 x 64 box of an operand whose rows run along K
+constexpr int kStoreBytes = 32 * 128;       // 32 rows of 128 bytes: one warp's store
+constexpr int kEpilogueWarps = 4;
+constexpr int kProductThreads = 64 + 32 * kEpilogueWarps;
+constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kEpilogueWarps * 2 * kStoreBytes;
+constexpr int kTmemColumns = 512;  // two accumulators of 256 columns
 
-template <bool BF16>
-__device__ __forceinline__ void lp_put(void *p, long long i, float v) {
-    if constexpr (BF16)
-        static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
-    else
-        static_cast<__half *>(p)[i] = __float2half_rn(v);
-}
+// The largest |grad_loss| becomes this in the lp operand q: fp16 keeps 15 more
+// binades below it, bf16 has float's range.
+__host__ __device__ constexpr float operand_top(bool bf16) { return bf16 ? 1.0f : 32768.0f; }
 
-// acc[4][4] of the tile at (m0, n0): sum over k of a(m, k) b(n, k)
-template <typename A, typename B>
-__device__ void tile_product(A a, B b, long long m0, long long n0, long long k1, float acc[4][4]) {
-    __shared__ float as[kK][kT + 1], bs[kK][kT + 1];
-    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
-    for (long long k0 = 0; k0 < k1; k0 += kK) {
-        for (int e = threadIdx.x; e < kT * kK; e += kThreads) {
-            as[e % kK][e / kK] = k0 + e % kK < k1 ? a(m0 + e / kK, k0 + e % kK) : 0.0f;
-            bs[e % kK][e / kK] = k0 + e % kK < k1 ? b(n0 + e / kK, k0 + e % kK) : 0.0f;
+// ------------------------------------------------------------------ workspace
+
+struct LossRecord {
+    int count;     // tokens that count
+    float factor;  // q in the products' operands times this is q
+};
+
+struct BackwardLayout {
+    int64_t rows;      // tokens rounded up to whole tiles
+    int64_t piece;     // columns of a piece of the vocabulary (whole tiles)
+    int pieces;
+    int splits;        // partial sums of grad_hidden
+    int64_t index, place, lse2, ratio, target, hidden, slopes, sums, bytes;  // byte offsets
+};
+
+constexpr int64_t kSlopeBytes = int64_t(256) << 20;  // a piece of q takes about this much at most
+
+int64_t up(int64_t x, int64_t q) { return (x + q - 1) / q * q; }
+
+BackwardLayout backward_layout(int64_t tokens, int64_t vocab, int dim) {
+    BackwardLayout l;
+    l.rows = up(std::max<int64_t>(tokens, 1), kTileM);
+    const int64_t most = std::max<int64_t>(kTileN, kSlopeBytes / 2 / l.rows / kTileN * kTileN);
+    l.pieces = (int)((vocab + most - 1) / most);
+    l.piece = up((vocab + l.pieces - 1) / l.pieces, kTileN);
+    l.pieces = (int)((vocab + l.piece - 1) / l.piece);
+    // grad_hidden has few tiles and long sums: cut the sums so that the last
+    // round of tiles is nearly full (at most 16 ways, 8 blocks of K each at least)
+    const int64_t tiles = l.rows / kTileM * ((dim + kTileN - 1) / kTileN), pairs = 76;
+    double best = 1e30;
+    l.splits = 1;
+    for (int s = 1; s <= 16 && l.piece / kTileK / s >= 8; ++s) {
+        const double rounds = double((tiles * s + pairs - 1) / pairs) / s + 0.02 * s;
+        if (rounds < best) {
+            best = rounds;
+            l.splits = s;
         }
-        __syncthreads();
-        for (int k = 0; k < kK; ++k)
-            for (int i = 0; i < 4; ++i)
-                for (int j = 0; j < 4; ++j) acc[i][j] = __fmaf_rn(as[k][ty * 4 + i], bs[k][tx * 4 + j], acc[i][j]);
-        __syncthreads();
     }
+    int64_t at = 256;
+    auto take = [&](int64_t bytes) {
+        const int64_t here = at;
+        at = up(at + bytes, 1024);
+        return here;
+    };
+    l.index = take(l.rows * 4);
+    l.place = take(l.rows * 4);
+    l.lse2 = take(l.rows * 4);
+    l.ratio = take(l.rows * 4);
+    l.target = take(l.rows * 4);
+    l.hidden = take(l.rows * dim * 2);
+    l.slopes = take(l.rows * l.piece * 2);
+    l.sums = take(l.splits * l.rows * dim * 4);
+    l.bytes = at;
+    return l;
 }
 
-// the logits' tile of block (x: vocabulary, y: tokens)
+// ------------------------------------------------------------- PTX primitives
+
+__device__ __forceinline__ uint32_t smem_addr(const void *p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// the address of this CTA's `addr` in CTA `rank` of the pair
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// a box of `map` at (x, y) to this CTA's shared memory; the bytes count on `bar`,
+// which may be the other CTA's
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+        "%3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_store(const CUtensorMap *map, int x, int y, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x),
+                 "r"(y), "r"(src)
+                 : "memory");
+}
+
+__device__ __forceinline__ void tma_add(const CUtensorMap *map, int x, int y, uint32_t src) {
+    asm volatile("cp.reduce.async.bulk.tensor.2d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map),
+                 "r"(x), "r"(y), "r"(src)
+                 : "memory");
+}
+
+__device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void store_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void store_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// Shared-memory operand descriptor, 128-byte swizzle.  Rows of 128 bytes, eight
+// to a 1024-byte group (the stride offset).  K-major: a row holds 64 values of
+// K.  MN-major: a row holds 64 values of M or N at one K, and the next 64 of M
+// or N lie a whole box further (the leading offset).
+__device__ __forceinline__ uint64_t operand_desc(uint32_t addr, bool mn) {
+    uint64_t d = (addr & 0x3ffffu) >> 4;
+    d |= (uint64_t)(mn ? kBoxBytes >> 4 : 1) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+
+// arrive on `bar` of both CTAs once every product issued so far is done
+__device__ __forceinline__ void mma_commit(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// 32 consecutive columns of this lane's accumulator row
+__device__ __forceinline__ void tmem_load32(uint32_t addr, float v[32]) {
+    uint32_t r[32];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 template <bool BF16>
-__device__ void logits_tile(const LossArgs &p, long long m0, long long n0, float acc[4][4]) {
-    tile_product(
-        [&](long long m, long long k) { return m < p.tokens ? lp_get<BF16>(p.hidden, m * p.hidden_stride + k) : 0.0f; },
-        [&](long long n, long long k) { return n < p.vocab ? lp_get<BF16>(p.weight, n * p.weight_stride + k) : 0.0f; },
-        m0, n0, p.dim, acc);
-}
-
-// forward workspace: partial (maximum, sum) [tile][token], then target logits
-template <bool BF16>
-__global__ void loss_tiles(const LossArgs p) {
-    pdl_enter();
-    const long long m0 = (long long)blockIdx.y * kT, n0 = (long long)blockIdx.x * kT;
-    float acc[4][4];
-    logits_tile<BF16>(p, m0, n0, acc);
-    __shared__ float z[kT][kT + 1];
-    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) z[ty * 4 + i][tx * 4 + j] = acc[i][j];
-    __syncthreads();
-    const long long t = m0 + threadIdx.x;
-    if (threadIdx.x >= kT || t >= p.tokens) return;
-    const int n = p.vocab - n0 < kT ? (int)(p.vocab - n0) : kT;
-    float top = -INFINITY, sum = 0.0f;
-    for (int j = 0; j < n; ++j) top = fmaxf(top, z[threadIdx.x][j]);
-    for (int j = 0; j < n; ++j) sum += expf(z[threadIdx.x][j] - top);
-    float2 *part = static_cast<float2 *>(p.workspace);
-    part[blockIdx.x * p.tokens + t] = make_float2(top, sum);
-    const long long at = p.target[t] - n0;
-    if (at >= 0 && at < n) reinterpret_cast<float *>(part + (long long)gridDim.x * p.tokens)[t] = z[threadIdx.x][at];
-}
-
-__global__ void loss_join(const LossArgs p, int tiles) {
-    pdl_enter();
-    const long long t = (long long)blockIdx.x * kThreads + threadIdx.x;
-    if (t >= p.tokens) return;
-    const float2 *part = static_cast<const float2 *>(p.workspace);
-    float top = -INFINITY, sum = 0.0f;
-    for (int i = 0; i < tiles; ++i) top = fmaxf(top, part[i * p.tokens + t].x);
-    for (int i = 0; i < tiles; ++i) sum += part[i * p.tokens + t].y * expf(part[i * p.tokens + t].x - top);
-    const float lse = top + logf(sum);
-    p.lse[t] = lse;
-    const long long y = p.target[t];
-    if (y == p.ignore) {
-        p.loss[t] = 0.0f;
-    } else if (y < 0 || y >= p.vocab) {
-        p.loss[t] = NAN;
-        atomicOr(p.status, ZERO_LOSS_BAD_TARGET);
+__device__ __forceinline__ uint32_t pack_lp(float a, float b) {
+    if constexpr (BF16) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
     } else {
-        p.loss[t] = lse - reinterpret_cast<const float *>(part + (long long)tiles * p.tokens)[t];
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
     }
 }
 
-__device__ __forceinline__ bool counted(const LossArgs &p, long long t) {
-    const long long y = p.target[t];
-    return y != p.ignore && y >= 0 && y < p.vocab;
+// ------------------------------------------------------------------- products
+
+enum Product { kStats = 0, kSlopes = 1, kGradHidden = 2, kGradWeight = 3 };
+
+struct ProductParams {
+    CUtensorMap h_k, hc_k;    // hidden states (all, the counted ones): boxes 64 of D x 128 tokens
+    CUtensorMap w_k;          // weight: 64 of D x 128 vocabulary
+    CUtensorMap w_mn;         // weight: 64 of D x 64 vocabulary
+    CUtensorMap h_mn, hc_mn;  // hidden states: 64 of D x 64 tokens
+    CUtensorMap q_k;          // q: 64 vocabulary x 128 tokens
+    CUtensorMap q_mn;         // q: 64 vocabulary x 64 tokens
+    CUtensorMap q_out;        // q: 64 vocabulary x 32 tokens
+    CUtensorMap gh_out;       // partial grad_hidden: 32 of D x 32 tokens, float
+    CUtensorMap gw_out;       // grad_weight: 64 of D x 32 vocabulary
+    int kind;
+    long long tokens, vocab;
+    int dim;
+    long long piece0, piece;  // the piece of the vocabulary (kStats: all of it)
+    long long rows;           // tokens rounded up to whole tiles
+    int splits;
+    int first_piece;
+    const LossRecord *record;  // NULL: every token counts
+    // kStats
+    const int64_t *target;
+    float2 *parts;  // [tile of the vocabulary][token]
+    float *picked;  // the target's logit
+    // kSlopes (by place among the counted tokens)
+    const float *lse2, *ratio;
+    const int *place_target;
+    int *status;
+    long long wait_cycles;
+};
+
+struct Tile {
+    int m, n;        // tile coordinates
+    int k0, k1;      // blocks of K
+    int split;
+};
+
+// Consecutive tiles take 8 tiles of M for one of N before the next of N, so the
+// pairs that run together read few different rows of either operand from L2.
+__device__ __forceinline__ Tile tile_of(long long i, int m_tiles, int n_tiles, int k_blocks, int splits) {
+    Tile t;
+    const long long per_split = (long long)m_tiles * n_tiles;
+    t.split = (int)(i / per_split);
+    const long long r = i - t.split * per_split;
+    constexpr int kGroup = 8;
+    const long long per_group = (long long)kGroup * n_tiles;
+    const int g = (int)(r / per_group);
+    const int in_group = m_tiles - g * kGroup < kGroup ? m_tiles - g * kGroup : kGroup;
+    const int q = (int)(r - g * per_group);
+    t.n = q / in_group;
+    t.m = g * kGroup + q % in_group;
+    t.k0 = (int)((long long)k_blocks * t.split / splits);
+    t.k1 = (int)((long long)k_blocks * (t.split + 1) / splits);
+    return t;
 }
 
-// backward workspace: one float (the largest finite |grad_loss|), then at byte
-// 256 the float gradients of a piece of the vocabulary, then grad_hidden's sums
-constexpr long long kPiece = 4096;
+struct Shared {
+    uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
+    uint32_t tmem;
+    int dead;  // a wait of this CTA gave up
+};
 
-__global__ void loss_largest(const LossArgs p) {
-    pdl_enter();
-    __shared__ float shared[kThreads];
-    float top = 0.0f;
-    for (long long t = threadIdx.x; t < p.tokens; t += kThreads) {
-        const float g = fabsf(p.grad_loss[t]);
-        if (counted(p, t) && g <= 3.402823466e38f) top = fmaxf(top, g);
-        if (p.target[t] != p.ignore && !counted(p, t)) atomicOr(p.status, ZERO_LOSS_BAD_TARGET);
+// A bounded wait: false once `limit` cycles have passed (or another wait of the
+// CTA has given up); the CTA then stops and the status says so.
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatile int *dead, long long limit, int *status) {
+    const uint32_t b = smem_addr(bar);
+    if (*dead) return false;
+    if (bar_try(b, parity)) return true;
+    const long long t0 = clock64();
+    while (!bar_try(b, parity)) {
+        if (*dead || clock64() - t0 >= limit) {
+            *dead = 1;
+            atomicOr(status, ZERO_LOSS_TIMEOUT);
+            return false;
+        }
     }
-    shared[threadIdx.x] = top;
-    __syncthreads();
+    return true;
+}
+
+template <bool BF16>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
+loss_products(const __grid_constant__ ProductParams p) {
+    extern __shared__ unsigned char raw[];
+    __shared__ Shared sh;
+    unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t stage0 = smem_addr(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t rank;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+
     if (threadIdx.x == 0) {
-        for (int i = 1; i < kThreads; ++i) top = fmaxf(top, shared[i]);
-        *static_cast<float *>(p.workspace) = top;
+        for (int s = 0; s < kStages; ++s) {
+            bar_init(smem_addr(&sh.full[s]), 1);
+            bar_init(smem_addr(&sh.empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            bar_init(smem_addr(&sh.acc_full[b]), 1);
+            bar_init(smem_addr(&sh.acc_empty[b]), 2 * kEpilogueWarps);
+        }
+        bar_init(smem_addr(&sh.drained), 1);
+        sh.dead = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sh.tmem)),
+                     "r"(kTmemColumns)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    pdl_enter();
+
+    volatile int *dead = &sh.dead;
+    const long long limit = p.wait_cycles;
+    const bool all = p.record == nullptr || p.record->count == p.tokens;
+    const long long count = p.record ? p.record->count : p.tokens;
+    int m_tiles, n_tiles, k_blocks;
+    const long long piece_end = p.piece0 + p.piece < p.vocab ? p.piece0 + p.piece : p.vocab;
+    const int row_tiles = (int)((count + kTileM - 1) / kTileM);
+    const int vocab_tiles = (int)((piece_end - p.piece0 + kTileN - 1) / kTileN);
+    if (p.kind == kGradHidden) {
+        m_tiles = row_tiles;
+        n_tiles = (p.dim + kTileN - 1) / kTileN;
+        k_blocks = (int)((piece_end - p.piece0 + kTileK - 1) / kTileK);
+    } else if (p.kind == kGradWeight) {
+        m_tiles = vocab_tiles;
+        n_tiles = (p.dim + kTileN - 1) / kTileN;
+        k_blocks = (int)((count + kTileK - 1) / kTileK);
+    } else {
+        m_tiles = row_tiles;
+        n_tiles = vocab_tiles;
+        k_blocks = (p.dim + kTileK - 1) / kTileK;
+    }
+    const long long n_work = (long long)m_tiles * n_tiles * p.splits;
+    const long long pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const bool a_mn = p.kind == kGradWeight, b_mn = p.kind >= kGradHidden;
+
+    if (warp == 0) {
+        if (lane == 0) {  // ------------------------------------------ loads
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (long long i = pair; i < n_work && ok; i += pairs) {
+                const Tile t = tile_of(i, m_tiles, n_tiles, k_blocks, p.splits);
+                const int m0 = t.m * kTileM + (int)rank * kHalf, n0 = t.n * kTileN + (int)rank * kHalf;
+                for (int k = t.k0; k < t.k1; ++k) {
+                    ok = wait_for(&sh.empty[stage], phase ^ 1, dead, limit, p.status);
+                    if (!ok) break;
+                    const uint32_t a = stage0 + stage * kStageBytes, b = a + kOperandBytes;
+                    const uint32_t bar = in_cta(smem_addr(&sh.full[stage]), 0);
+                    if (rank == 0) bar_expect(smem_addr(&sh.full[stage]), 2 * kStageBytes);
+                    const int kk = k * kTileK;
+                    if (p.kind <= kSlopes) {
+                        tma_load(a, all ? &p.h_k : &p.hc_k, kk, m0, bar);
+                        tma_load(b, &p.w_k, kk, (int)p.piece0 + n0, bar);
+                    } else if (p.kind == kGradHidden) {
+                        tma_load(a, &p.q_k, kk, m0, bar);
+                        tma_load(b, &p.w_mn, n0, (int)p.piece0 + kk, bar);
+                        tma_load(b + kBoxBytes, &p.w_mn, n0 + 64, (int)p.piece0 + kk, bar);
+                    } else {
+                        const CUtensorMap *h = all ? &p.h_mn : &p.hc_mn;
+                        tma_load(a, &p.q_mn, m0, kk, bar);
+                        tma_load(a + kBoxBytes, &p.q_mn, m0 + 64, kk, bar);
+                        tma_load(b, h, n0, kk, bar);
+                        tma_load(b + kBoxBytes, h, n0 + 64, kk, bar);
+                    }
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (rank == 0 && lane == 0) {  // ------------------------- products
+            uint32_t idesc = 1u << 4;  // float sums
+            if (BF16) idesc |= 1u << 7 | 1u << 10;
+            idesc |= (uint32_t)a_mn << 15 | (uint32_t)b_mn << 16;
+            idesc |= (uint32_t)(kTileN >> 3) << 17 | (uint32_t)(kTileM >> 4) << 24;
+            // 16 of K further: 32 bytes along a row, or 16 rows
+            const uint64_t a_step = (a_mn ? 16 * 128 : 32) >> 4, b_step = (b_mn ? 16 * 128 : 32) >> 4;
+            int stage = 0, buf = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            bool ok = true;
+            for (long long i = pair; i < n_work && ok; i += pairs) {
+                const Tile t = tile_of(i, m_tiles, n_tiles, k_blocks, p.splits);
+                ok = wait_for(&sh.acc_empty[buf], acc_phase ^ 1, dead, limit, p.status);
+                if (!ok) break;
+                tc_fence_after();
+                for (int k = t.k0; k < t.k1; ++k) {
+                    ok = wait_for(&sh.full[stage], phase, dead, limit, p.status);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t a = operand_desc(stage0 + stage * kStageBytes, a_mn);
+                    const uint64_t b = operand_desc(stage0 + stage * kStageBytes + kOperandBytes, b_mn);
+#pragma unroll
+                    for (int j = 0; j < kTileK / 16; ++j)
+                        mma_pair(tmem + buf * kTileN, a + j * a_step, b + j * b_step, idesc, k > t.k0 || j > 0);
+                    mma_commit(smem_addr(&sh.empty[stage]));
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (!ok) break;
+                mma_commit(smem_addr(&sh.acc_full[buf]));
+                buf ^= 1;
+                if (buf == 0) acc_phase ^= 1;
+            }
+            if (!ok) {  // the products already issued still read shared memory
+                mma_commit(smem_addr(&sh.drained));
+                for (int i = 0; i < 4096 && !bar_try(smem_addr(&sh.drained), 0); ++i) __nanosleep(256);
+            }
+        }
+    } else {  // ------------------------------------------------------ results
+        const int quad = warp & 3;  // the quarter of the lanes this warp may read
+        const uint32_t stage_out = stage0 + kStages * kStageBytes + (warp - 2) * 2 * kStoreBytes;
+        const float factor = p.kind >= kGradHidden ? p.record->factor : 1.0f;
+        int buf = 0, out_buf = 0;
+        uint32_t acc_phase = 0;
+        // one swizzled row of 128 bytes per lane, then one store by lane 0
+        auto put = [&](const uint32_t w[32], const CUtensorMap *map, int x, int y, bool add, bool skip) {
+            if (lane == 0) store_wait_read<1>();
+            __syncwarp();
+            const uint32_t row = stage_out + out_buf * kStoreBytes + lane * 128;
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((c ^ (lane & 7)) << 4)), "r"(w[4 * c]),
+                             "r"(w[4 * c + 1]), "r"(w[4 * c + 2]), "r"(w[4 * c + 3])
+                             : "memory");
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+                if (!skip) {
+                    if (add)
+                        tma_add(map, x, y, stage_out + out_buf * kStoreBytes);
+                    else
+                        tma_store(map, x, y, stage_out + out_buf * kStoreBytes);
+                }
+                store_commit();
+            }
+            out_buf ^= 1;
+        };
+        for (long long i = pair; i < n_work; i += pairs) {
+            const Tile t = tile_of(i, m_tiles, n_tiles, k_blocks, p.splits);
+            const int row0 = t.m * kTileM + (int)rank * kHalf + quad * 32;  // this warp's first row of M
+            const bool got = wait_for(&sh.acc_full[buf], acc_phase, dead, limit, p.status);
+            if (!__all_sync(0xffffffffu, got)) break;
+            tc_fence_after();
+            const uint32_t acc = tmem + buf * kTileN + ((uint32_t)(quad * 32) << 16);
+            if (p.kind == kStats) {
+                const long long token = row0 + lane;
+                const bool mine = token < p.tokens;
+                const long long y = mine ? p.target[token] : -1;
+                const long long v0 = p.piece0 + (long long)t.n * kTileN;
+                const long long left = p.vocab - v0;  // columns of the tile that exist
+                float top = -INFINITY, sum = 0.0f;
+                for (int c = 0; c < kTileN && c < left; c += 32) {
+                    float z[32];
+                    tmem_load32(acc + c, z);
+                    if (left - c < 32) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (j >= left - c) z[j] = -INFINITY;
+                    }
+                    const long long at = y - v0 - c;
+                    if (__any_sync(0xffffffffu, at >= 0 && at < 32)) {
+                        float z_y = 0.0f;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) z_y = j == at ? z[j] : z_y;
+                        if (at >= 0 && at < 32) p.picked[token] = z_y;
+                    }
+                    float high = z[0];
+#pragma unroll
+                    for (int j = 1; j < 32; ++j) high = fmaxf(high, z[j]);
+                    high = fmaxf(high, top);
+                    // a row of -inf so far: any finite base leaves its sum at 0
+                    const float base = (high == -INFINITY ? 0.0f : high) * kLog2e;
+                    float s = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) s += exp2_approx(__fmaf_rn(z[j], kLog2e, -base));
+                    sum = sum * exp2_approx(__fmaf_rn(top, kLog2e, -base)) + s;
+                    top = high;
+                }
+                if (mine) p.parts[t.n * p.tokens + token] = make_float2(top, sum);
+            } else if (p.kind == kSlopes) {
+                const int place = row0 + lane;
+                const float lse2 = p.lse2[place], ratio = p.ratio[place];
+                const bool live = p.place_target[place] >= 0;  // not a row that fills the last tile
+                const int y = p.place_target[place] - (int)p.piece0 - t.n * kTileN;
+                const long long left = p.vocab - p.piece0 - (long long)t.n * kTileN;
+                for (int c = 0; c < kTileN; c += 64) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float z[32];
+                        const int col = c + 32 * h;
+                        tmem_load32(acc + col, z);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) z[j] = exp2_approx(__fmaf_rn(z[j], kLog2e, -lse2));
+                        if (__any_sync(0xffffffffu, y >= col && y < col + 32)) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) z[j] = j == y - col ? z[j] - 1.0f : z[j];
+                        }
+                        if (left - col < 32) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (j >= left - col) z[j] = 0.0f;
+                        }
+                        if (!live) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) z[j] = 0.0f;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) w[16 * h + j / 2] = pack_lp<BF16>(z[j] * ratio, z[j + 1] * ratio);
+                    }
+                    put(w, &p.q_out, t.n * kTileN + c, row0, false, false);
+                }
+            } else if (p.kind == kGradHidden) {
+                const bool any = t.k1 > t.k0;  // else the accumulator was never written
+                for (int c = 0; c < kTileN; c += 32) {
+                    float z[32];
+                    tmem_load32(acc + c, z);
+                    uint32_t w[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) w[j] = any ? __float_as_uint(z[j] * factor) : 0u;
+                    put(w, &p.gh_out, t.n * kTileN + c, (int)(t.split * p.rows) + row0, !p.first_piece,
+                        t.n * kTileN + c >= p.dim);
+                }
+            } else {
+                for (int c = 0; c < kTileN; c += 64) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float z[32];
+                        tmem_load32(acc + c + 32 * h, z);
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            // no token counts: the accumulator was never written
+                            const float x0 = k_blocks ? z[j] * factor : 0.0f, x1 = k_blocks ? z[j + 1] * factor : 0.0f;
+                            w[16 * h + j / 2] = pack_lp<BF16>(x0, x1);
+                        }
+                    }
+                    put(w, &p.gw_out, t.n * kTileN + c, (int)p.piece0 + row0, false,
+                        t.n * kTileN + c >= p.dim || p.piece0 + row0 >= p.vocab);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive_cluster(in_cta(smem_addr(&sh.acc_empty[buf]), 0));
+            buf ^= 1;
+            if (buf == 0) acc_phase ^= 1;
+        }
+        if (lane == 0) store_wait_all();
+    }
+    __syncwarp();
+    __syncthreads();
+    // after a wait that gave up, loads may still be on their way to either CTA's
+    // shared memory: nothing counts them any more, so give them time
+    if (*dead && threadIdx.x == 0)
+        for (int i = 0; i < 4096; ++i) __nanosleep(512);
+    __syncthreads();
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemColumns) : "memory");
+}
+
+// ---------------------------------------------------------- the smaller kernels
+
+constexpr int kJoinTokens = 32, kJoinWays = 8;
+
+// lse and loss of 32 tokens: 8 ways along the vocabulary's tiles, joined in order
+__global__ void __launch_bounds__(kJoinTokens *kJoinWays)
+loss_join(const float2 *__restrict__ parts, const float *__restrict__ picked, int tiles, const int64_t *__restrict__ target,
+          long long ignore, long long tokens, long long vocab, float *loss, float *lse, int *status) {
+    pdl_enter();
+    __shared__ float2 way[kJoinWays][kJoinTokens];
+    const int x = threadIdx.x % kJoinTokens, w = threadIdx.x / kJoinTokens;
+    const long long t = (long long)blockIdx.x * kJoinTokens + x;
+    auto join = [](float2 a, float2 b) {
+        const float top = fmaxf(a.x, b.x);
+        const float base = top == -INFINITY ? 0.0f : top;
+        return make_float2(top, a.y * exp2_approx((a.x - base) * kLog2e) + b.y * exp2_approx((b.x - base) * kLog2e));
+    };
+    float2 acc = make_float2(-INFINITY, 0.0f);
+    if (t < tokens) {
+        int i = w;
+        for (; i + 3 * kJoinWays < tiles; i += 4 * kJoinWays) {
+            float2 v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = parts[(long long)(i + j * kJoinWays) * tokens + t];
+            acc = join(acc, join(join(v[0], v[1]), join(v[2], v[3])));
+        }
+        for (; i < tiles; i += kJoinWays) acc = join(acc, parts[(long long)i * tokens + t]);
+    }
+    way[w][x] = acc;
+    __syncthreads();
+    if (w != 0 || t >= tokens) return;
+    for (int i = 1; i < kJoinWays; ++i) acc = join(acc, way[i][x]);
+    const float l = acc.x + log2f(acc.y) * kLn2;
+    lse[t] = l;
+    const long long y = target[t];
+    if (y == ignore) {
+        loss[t] = 0.0f;
+    } else if (y < 0 || y >= vocab) {
+        loss[t] = __int_as_float(0x7fffffff);
+        atomicOr(status, ZERO_LOSS_BAD_TARGET);
+    } else {
+        loss[t] = l - picked[t];
     }
 }
 
-__device__ __forceinline__ float *slopes(const LossArgs &p) { return static_cast<float *>(p.workspace) + 64; }
+constexpr int kPlaceThreads = 1024;
 
-template <bool BF16>
-__global__ void loss_slopes(const LossArgs p, long long piece0) {
+// The counted tokens in order (index: token of a place; place: place of a token
+// or -1), what the slopes need of each, and the largest finite |grad_loss|.
+// One block; a thread takes consecutive tokens.
+__global__ void __launch_bounds__(kPlaceThreads)
+loss_place(const int64_t *__restrict__ target, long long ignore, long long tokens, long long rows, long long vocab,
+           const float *__restrict__ lse, const float *__restrict__ grad_loss, float top_operand, LossRecord *record,
+           int *index, int *place, float *lse2, float *ratio, int *place_target, int *status) {
     pdl_enter();
-    const long long m0 = (long long)blockIdx.y * kT, n0 = piece0 + (long long)blockIdx.x * kT;
-    float acc[4][4];
-    logits_tile<BF16>(p, m0, n0, acc);
-    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    for (int i = 0; i < 4; ++i) {
-        const long long t = m0 + ty * 4 + i;
-        if (t >= p.tokens) continue;
-        const bool counts = counted(p, t);
-        for (int j = 0; j < 4; ++j) {
-            const long long v = n0 + tx * 4 + j;
-            float q = 0.0f;
-            if (counts && v < p.vocab) q = (expf(acc[i][j] - p.lse[t]) - (v == p.target[t] ? 1.0f : 0.0f)) * p.grad_loss[t];
-            slopes(p)[t * kPiece + v - piece0] = q;
+    __shared__ int sums[kPlaceThreads / 32];
+    __shared__ float tops[kPlaceThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long each = (tokens + kPlaceThreads - 1) / kPlaceThreads;
+    const long long t0 = threadIdx.x * each < tokens ? threadIdx.x * each : tokens;
+    const long long t1 = t0 + each < tokens ? t0 + each : tokens;
+    int mine = 0;
+    float top = 0.0f;
+    bool bad = false;
+    for (long long t = t0; t < t1; ++t) {
+        const long long y = target[t];
+        const float g = fabsf(grad_loss[t]);
+        const bool counts = y != ignore && y >= 0 && y < vocab;
+        bad |= y != ignore && !counts;
+        mine += counts;
+        if (counts && g <= 3.402823466e38f) top = fmaxf(top, g);
+    }
+    if (bad) atomicOr(status, ZERO_LOSS_BAD_TARGET);
+    int before = mine;  // inclusive sum over the warp's lanes, then over the warps
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += x;
+    }
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 31) sums[warp] = before;
+    if (lane == 0) tops[warp] = top;
+    __syncthreads();
+    int all = 0;
+    for (int w = 0; w < kPlaceThreads / 32; ++w) {
+        if (w < warp) before += sums[w];
+        all += sums[w];
+        top = fmaxf(top, tops[w]);
+    }
+    int at = before - mine;
+    for (long long t = t0; t < t1; ++t) {
+        const long long y = target[t];
+        const bool counts = y != ignore && y >= 0 && y < vocab;
+        place[t] = counts ? at : -1;
+        if (!counts) continue;
+        index[at] = (int)t;
+        lse2[at] = lse[t] * kLog2e;
+        ratio[at] = top > 0.0f ? grad_loss[t] / top * top_operand : grad_loss[t];
+        place_target[at++] = (int)y;
+    }
+    for (long long i = all + threadIdx.x; i < rows; i += kPlaceThreads) {  // rows that fill the last tile
+        lse2[i] = ratio[i] = 0.0f;
+        place_target[i] = -1;
+    }
+    if (threadIdx.x == 0) {
+        record->count = all;
+        record->factor = top / top_operand;
+    }
+}
+
+constexpr int kCopyThreads = 128;
+
+// hidden states of the counted tokens, then zeros up to whole blocks of K;
+// nothing where every token counts
+__global__ void __launch_bounds__(kCopyThreads)
+loss_compact(const uint4 *__restrict__ hidden, long long stride, const LossRecord *record, const int *__restrict__ index,
+             long long tokens, int vecs, uint4 *out) {
+    pdl_enter();
+    const long long count = record->count;
+    if (count == tokens) return;
+    const long long end = (count + kTileK - 1) / kTileK * kTileK < tokens ? (count + kTileK - 1) / kTileK * kTileK : tokens;
+    for (long long i = blockIdx.x; i < end; i += gridDim.x) {
+        const uint4 *src = i < count ? hidden + index[i] * stride : nullptr;
+        for (int v = threadIdx.x; v < vecs; v += kCopyThreads)
+            out[i * vecs + v] = src ? src[v] : make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
+// grad_hidden of a token: the partial sums in order, rounded once
+template <bool BF16>
+__global__ void __launch_bounds__(kCopyThreads)
+loss_finish(const float4 *__restrict__ sums, const int *__restrict__ place, long long tokens, long long rows, int splits,
+            int vecs, uint4 *out, long long stride) {
+    pdl_enter();
+    for (long long t = blockIdx.x; t < tokens; t += gridDim.x) {
+        const int i = place[t];
+        for (int v = threadIdx.x; v < vecs; v += kCopyThreads) {
+            float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
+            for (int s = 0; s < splits && i >= 0; ++s) {
+                const float4 *src = sums + ((s * rows + i) * vecs + v) * 2;
+                const float4 a = src[0], b = src[1];
+                lo.x += a.x; lo.y += a.y; lo.z += a.z; lo.w += a.w;
+                hi.x += b.x; hi.y += b.y; hi.z += b.z; hi.w += b.w;
+            }
+            out[t * stride + v] = make_uint4(pack_lp<BF16>(lo.x, lo.y), pack_lp<BF16>(lo.z, lo.w), pack_lp<BF16>(hi.x, hi.y),
+                                             pack_lp<BF16>(hi.z, hi.w));
         }
     }
 }
 
+// ------------------------------------------------------------------------ host
+
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encoder() {
+    static const EncodeTiled f = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return f;
+}
+
+// rows x cols elements (lp, or float) at p, read or written in boxes of 128
+// bytes x box_rows with the 128-byte swizzle; what lies outside reads as zero
+bool make_map(CUtensorMap *m, const void *p, int64_t rows, int64_t cols, int64_t stride, int lp, bool f32, int box_rows) {
+    const int size = f32 ? 4 : 2;
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)(stride * size)};
+    const cuuint32_t box[2] = {(cuuint32_t)(128 / size), (cuuint32_t)box_rows};
+    const cuuint32_t ones[2] = {1, 1};
+    const CUtensorMapDataType type = f32  ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                     : lp ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                          : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    return encoder()(m, type, 2, const_cast<void *>(p), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// pairs of CTAs that run at once
 template <bool BF16>
-__global__ void loss_grad_hidden(const LossArgs p, long long piece0) {
-    pdl_enter();
-    const long long m0 = (long long)blockIdx.y * kT, n0 = (long long)blockIdx.x * kT;
-    const long long n = p.vocab - piece0 < kPiece ? p.vocab - piece0 : kPiece;
-    float acc[4][4];
-    tile_product([&](long long m, long long k) { return m < p.tokens ? slopes(p)[m * kPiece + k] : 0.0f; },
-                 [&](long long d, long long k) {
-                     return d < p.dim ? lp_get<BF16>(p.weight, (piece0 + k) * p.weight_stride + d) : 0.0f;
-                 },
-                 m0, n0, n, acc);
-    float *sums = slopes(p) + p.tokens * kPiece;
-    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const long long t = m0 + ty * 4 + i, d = n0 + tx * 4 + j;
-            if (t >= p.tokens || d >= p.dim) continue;
-            const float v = acc[i][j] + (piece0 ? sums[t * p.dim + d] : 0.0f);
-            sums[t * p.dim + d] = v;
-            if (piece0 + n == p.vocab) lp_put<BF16>(p.grad_hidden, t * p.grad_hidden_stride + d, v);
+int pairs_at_once() {
+    static const int n = [] {
+        if (cudaFuncSetAttribute(loss_products<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess)
+            return 0;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2);
+        cfg.blockDim = dim3(kProductThreads);
+        cfg.dynamicSmemBytes = kSmemBytes;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int clusters = 0;
+        if (cudaOccupancyMaxActiveClusters(&clusters, loss_products<BF16>, &cfg) != cudaSuccess || clusters < 1) {
+            cudaGetLastError();
+            clusters = sm_count() / 2;
         }
+        return clusters < 1 ? 1 : clusters;
+    }();
+    return n;
+}
+
+std::atomic<long long> g_wait_cycles{4000000000ll};  // about two seconds
+
+template <bool BF16>
+cudaError_t launch_products(const ProductParams &p, int64_t tiles, cudaStream_t stream) {
+    const int pairs = pairs_at_once<BF16>();
+    if (pairs < 1) return cudaErrorInvalidConfiguration;
+    const int64_t use = std::max<int64_t>(1, std::min<int64_t>(pairs, tiles));
+    return launch_pdl(loss_products<BF16>, dim3((unsigned)(2 * use)), dim3(kProductThreads), kSmemBytes, stream, p);
 }
 
 template <bool BF16>
-__global__ void loss_grad_weight(const LossArgs p, long long piece0) {
-    pdl_enter();
-    const long long m0 = (long long)blockIdx.y * kT, n0 = (long long)blockIdx.x * kT;
-    float acc[4][4];
-    tile_product([&](long long m, long long k) { return m < kPiece ? slopes(p)[k * kPiece + m] : 0.0f; },
-                 [&](long long d, long long k) {
-                     return d < p.dim && counted(p, k) ? lp_get<BF16>(p.hidden, k * p.hidden_stride + d) : 0.0f;
-                 },
-                 m0, n0, p.tokens, acc);
-    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const long long v = piece0 + m0 + ty * 4 + i, d = n0 + tx * 4 + j;
-            if (v < p.vocab && d < p.dim) lp_put<BF16>(p.grad_weight, v * p.grad_weight_stride + d, acc[i][j]);
-        }
+cudaError_t forward_impl(const LossArgs &a, cudaStream_t stream) {
+    ProductParams p = {};
+    if (!encoder() || !make_map(&p.h_k, a.hidden, a.tokens, a.dim, a.hidden_stride, a.lp, false, kHalf) ||
+        !make_map(&p.w_k, a.weight, a.vocab, a.dim, a.weight_stride, a.lp, false, kHalf))
+        return cudaErrorNotSupported;
+    p.kind = kStats;
+    p.tokens = a.tokens;
+    p.vocab = p.piece = a.vocab;
+    p.dim = a.dim;
+    p.splits = 1;
+    p.target = a.target;
+    const int64_t tiles = up(a.vocab, kTileN) / kTileN;
+    p.parts = static_cast<float2 *>(a.workspace);
+    p.picked = reinterpret_cast<float *>(p.parts + tiles * a.tokens);
+    p.status = a.status;
+    p.wait_cycles = g_wait_cycles.load();
+    cudaError_t e = launch_products<BF16>(p, up(a.tokens, kTileM) / kTileM * tiles, stream);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(loss_join, dim3((unsigned)((a.tokens + kJoinTokens - 1) / kJoinTokens)),
+                      dim3(kJoinTokens * kJoinWays), 0, stream, (const float2 *)p.parts, (const float *)p.picked, (int)tiles,
+                      a.target, (long long)a.ignore, (long long)a.tokens, (long long)a.vocab, a.loss, a.lse, a.status);
 }
 
-unsigned tiles(int64_t n) { return (unsigned)((n + kT - 1) / kT); }
+template <bool BF16>
+cudaError_t backward_impl(const LossArgs &a, cudaStream_t stream) {
+    const BackwardLayout l = backward_layout(a.tokens, a.vocab, a.dim);
+    char *ws = static_cast<char *>(a.workspace);
+    LossRecord *record = reinterpret_cast<LossRecord *>(ws);
+    int *index = reinterpret_cast<int *>(ws + l.index), *place = reinterpret_cast<int *>(ws + l.place);
+    float *lse2 = reinterpret_cast<float *>(ws + l.lse2), *ratio = reinterpret_cast<float *>(ws + l.ratio);
+    int *place_target = reinterpret_cast<int *>(ws + l.target);
+    void *compact = ws + l.hidden, *slopes = ws + l.slopes;
+    float *sums = reinterpret_cast<float *>(ws + l.sums);
+    ProductParams p = {};
+    if (!encoder() || !make_map(&p.h_k, a.hidden, a.tokens, a.dim, a.hidden_stride, a.lp, false, kHalf) ||
+        !make_map(&p.hc_k, compact, a.tokens, a.dim, a.dim, a.lp, false, kHalf) ||
+        !make_map(&p.w_k, a.weight, a.vocab, a.dim, a.weight_stride, a.lp, false, kHalf) ||
+        !make_map(&p.w_mn, a.weight, a.vocab, a.dim, a.weight_stride, a.lp, false, kTileK) ||
+        !make_map(&p.h_mn, a.hidden, a.tokens, a.dim, a.hidden_stride, a.lp, false, kTileK) ||
+        !make_map(&p.hc_mn, compact, a.tokens, a.dim, a.dim, a.lp, false, kTileK) ||
+        !make_map(&p.q_k, slopes, l.rows, l.piece, l.piece, a.lp, false, kHalf) ||
+        !make_map(&p.q_mn, slopes, l.rows, l.piece, l.piece, a.lp, false, kTileK) ||
+        !make_map(&p.q_out, slopes, l.rows, l.piece, l.piece, a.lp, false, 32) ||
+        !make_map(&p.gh_out, sums, l.splits * l.rows, a.dim, a.dim, a.lp, true, 32) ||
+        !make_map(&p.gw_out, a.grad_weight, a.vocab, a.dim, a.grad_weight_stride, a.lp, false, 32))
+        return cudaErrorNotSupported;
+    p.tokens = a.tokens;
+    p.vocab = a.vocab;
+    p.dim = a.dim;
+    p.piece = l.piece;
+    p.rows = l.rows;
+    p.record = record;
+    p.lse2 = lse2;
+    p.ratio = ratio;
+    p.place_target = place_target;
+    p.status = a.status;
+    p.wait_cycles = g_wait_cycles.load();
+    cudaError_t e = launch_pdl(loss_place, dim3(1), dim3(kPlaceThreads), 0, stream, a.target, (long long)a.ignore,
+                               (long long)a.tokens, (long long)l.rows, (long long)a.vocab, (const float *)a.lse, a.grad_loss,
+                               operand_top(BF16), record, index, place, lse2, ratio, place_target, a.status);
+    const int copies = (int)std::min<int64_t>(a.tokens, 8 * sm_count());
+    if (e == cudaSuccess)
+        e = launch_pdl(loss_compact, dim3((unsigned)copies), dim3(kCopyThreads), 0, stream, static_cast<const uint4 *>(a.hidden),
+                       (long long)(a.hidden_stride / 8), (const LossRecord *)record, (const int *)index, (long long)a.tokens,
+                       a.dim / 8, static_cast<uint4 *>(compact));
+    const int64_t row_tiles = l.rows / kTileM, dim_tiles = up(a.dim, kTileN) / kTileN, piece_tiles = l.piece / kTileN;
+    for (int i = 0; i < l.pieces && e == cudaSuccess; ++i) {
+        p.piece0 = i * l.piece;
+        p.first_piece = i == 0;
+        p.splits = 1;
+        p.kind = kSlopes;
+        e = launch_products<BF16>(p, row_tiles * piece_tiles, stream);
+        p.kind = kGradWeight;
+        if (e == cudaSuccess) e = launch_products<BF16>(p, piece_tiles * dim_tiles, stream);
+        p.kind = kGradHidden;
+        p.splits = l.splits;
+        if (e == cudaSuccess) e = launch_products<BF16>(p, row_tiles * dim_tiles * l.splits, stream);
+    }
+    if (e == cudaSuccess)
+        e = launch_pdl(loss_finish<BF16>, dim3((unsigned)copies), dim3(kCopyThreads), 0, stream, reinterpret_cast<const float4 *>(sums),
+                       (const int *)place, (long long)a.tokens, (long long)l.rows, l.splits, a.dim / 8,
+                       static_cast<uint4 *>(a.grad_hidden), (long long)(a.grad_hidden_stride / 8));
+    return e;
+}
 
 }  // namespace
 
-int64_t loss_forward_bytes(int64_t tokens, int64_t vocab) { return (int64_t)tiles(vocab) * tokens * 8 + tokens * 4; }
+void set_loss_wait(int64_t cycles) { g_wait_cycles.store(cycles); }
+
+int64_t loss_forward_bytes(int64_t tokens, int64_t vocab) { return up(vocab, kTileN) / kTileN * tokens * 8 + up(tokens * 4, 16); }
 
 cudaError_t launch_loss_forward(const LossArgs &a, cudaStream_t stream) {
-    if (tiles(a.tokens) > 65535u) return cudaErrorInvalidValue;
-    cudaError_t e = launch_pdl(a.lp ? loss_tiles<true> : loss_tiles<false>, dim3(tiles(a.vocab), tiles(a.tokens)),
-                               dim3(kThreads), 0, stream, a);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(loss_join, dim3((unsigned)((a.tokens + kThreads - 1) / kThreads)), dim3(kThreads), 0, stream, a,
-                      (int)tiles(a.vocab));
+    return a.lp ? forward_impl<true>(a, stream) : forward_impl<false>(a, stream);
 }
 
-int64_t loss_backward_bytes(int64_t tokens, int64_t vocab, int dim) { return 256 + tokens * (kPiece + dim) * 4; }
+int64_t loss_backward_bytes(int64_t tokens, int64_t vocab, int dim) { return backward_layout(tokens, vocab, dim).bytes; }
 
 cudaError_t launch_loss_backward(const LossArgs &a, cudaStream_t stream) {
-    if (tiles(a.tokens) > 65535u) return cudaErrorInvalidValue;
-    cudaError_t e = launch_pdl(loss_largest, dim3(1), dim3(kThreads), 0, stream, a);
-    for (long long piece0 = 0; piece0 < a.vocab; piece0 += kPiece) {
-        const dim3 by_token(tiles(kPiece), tiles(a.tokens)), sums(tiles(a.dim), tiles(a.tokens));
-        const dim3 rows(tiles(a.dim), tiles(std::min<long long>(kPiece, a.vocab - piece0)));
-        if (e == cudaSuccess && a.tokens)
-            e = launch_pdl(a.lp ? loss_slopes<true> : loss_slopes<false>, by_token, dim3(kThreads), 0, stream, a, piece0);
-        if (e == cudaSuccess && a.tokens)
-            e = launch_pdl(a.lp ? loss_grad_hidden<true> : loss_grad_hidden<false>, sums, dim3(kThreads), 0, stream, a,
-                           piece0);
-        if (e == cudaSuccess)
-            e = launch_pdl(a.lp ? loss_grad_weight<true> : loss_grad_weight<false>, rows, dim3(kThreads), 0, stream, a,
-                           piece0);
-    }
-    return e;
+    if (a.tokens == 0)  // no token: a zero grad_weight
+        return cudaMemset2DAsync(a.grad_weight, size_t(a.grad_weight_stride) * 2, 0, size_t(a.dim) * 2, size_t(a.vocab), stream);
+    return a.lp ? backward_impl<true>(a, stream) : backward_impl<false>(a, stream);
 }
 
 }  // namespace zk
