@@ -492,7 +492,7 @@ zero_status zero_memory_report(int64_t psi, int32_t n_ranks, int32_t align,
  * bits from run to run.  Sums, statistics and products are held in float or
  * wider; what is rounded to lp on the way is named below.
  */
-#define ZERO_HEAD_MAX_DIM 32768
+#define ZERO_HEAD_MAX_DIM 16384
 
 /* Residual addition and root-mean-square norm of each of n_rows rows:
  *   s[i] = x[i] + residual[i]  (residual NULL: s = x)

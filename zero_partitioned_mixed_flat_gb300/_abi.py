@@ -23,7 +23,7 @@ ZERO_MAX_RANKS = 1024
 ZERO_NORM_TILE = 4096
 ZERO_QUANT_INT8, ZERO_QUANT_FP8_E4M3 = 0, 1
 ZERO_FP32 = 2                     # an element type of zero_clip_gradients only
-ZERO_HEAD_MAX_DIM = 32768
+ZERO_HEAD_MAX_DIM = 16384
 ZERO_LOSS_TIMEOUT, ZERO_LOSS_BAD_TARGET = 1, 2
 
 # every exported entry point of include/zero.h, with its ctypes signature
