@@ -39,9 +39,17 @@ constexpr int kOperandBytes = kHalf * kTileK * 2;
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kBoxBytes = 64 * kTileK * 2;  // a 64 x 64 box of an operand whose rows run along K
 constexpr int kStoreBytes = 32 * 128;       // 32 rows of 128 bytes: one warp's store
-constexpr int kEpilogueWarps = 4;
-constexpr int kProductThreads = 64 + 32 * kEpilogueWarps;
-constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kEpilogueWarps * 2 * kStoreBytes;
+constexpr int kStatsWarps = 8;     // that take a tile's results, two on each quarter of the rows
+constexpr int kStoreWarps = 4;
+constexpr int kStoreSmem = kStoreWarps * 2 * kStoreBytes;
+constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kStoreSmem;
+constexpr int kStatsColumns = kTileN / 2;  // of one statistics warp
+// The tensor core's float sum drops the low bits of every step of 16, always
+// towards zero: a logit of 15 over 4096 products came out 6e-5 too small, a
+// relative 4e-6 where float addition has 4e-8.  The losses are float, so the
+// statistics take the sum off after kChunk blocks (512 products) and add it up
+// in registers, rounded to nearest; q is rounded to lp anyway and does without.
+constexpr int kChunk = 8;
 constexpr int kTmemColumns = 512;  // two accumulators of 256 columns
 
 // The largest |grad_loss| becomes this in the lp operand q: fp16 keeps 15 more
@@ -221,6 +229,19 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, float v[32]) {
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+__device__ __forceinline__ void tmem_load16(uint32_t addr, float v[16]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+        "[%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
 __device__ __forceinline__ float exp2_approx(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -262,7 +283,7 @@ struct ProductParams {
     const LossRecord *record;  // NULL: every token counts
     // kStats
     const int64_t *target;
-    float2 *parts;  // [tile of the vocabulary][token]
+    float2 *parts;  // [kStatsColumns columns of the vocabulary][token]
     float *picked;  // the target's logit
     // kSlopes (by place among the counted tokens)
     const float *lse2, *ratio;
@@ -319,8 +340,36 @@ __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatil
     return true;
 }
 
-template <bool BF16>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
+// 32 rows of 128 bytes, one a lane, to a box of `map`: swizzled into this half of
+// the warp's two buffers (whose last store lies two calls back), then one store
+__device__ __forceinline__ void put_rows(const uint32_t (&w)[32], uint32_t buffer, int lane, const CUtensorMap *map, int x,
+                                         int y, bool add, bool skip) {
+    if (lane == 0) store_wait_read<1>();
+    __syncwarp();
+    const uint32_t row = buffer + lane * 128;
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((c ^ (lane & 7)) << 4)), "r"(w[4 * c]),
+                     "r"(w[4 * c + 1]), "r"(w[4 * c + 2]), "r"(w[4 * c + 3])
+                     : "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) {
+        if (!skip) {
+            if (add)
+                tma_add(map, x, y, buffer);
+            else
+                tma_store(map, x, y, buffer);
+        }
+        store_commit();
+    }
+}
+
+template <bool STATS>
+constexpr int product_threads() { return 64 + 32 * (STATS ? kStatsWarps : kStoreWarps); }
+
+template <bool BF16, bool STATS>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(product_threads<STATS>(), 1)
 loss_products(const __grid_constant__ ProductParams p) {
     extern __shared__ unsigned char raw[];
     __shared__ Shared sh;
@@ -337,7 +386,7 @@ loss_products(const __grid_constant__ ProductParams p) {
         }
         for (int b = 0; b < 2; ++b) {
             bar_init(smem_addr(&sh.acc_full[b]), 1);
-            bar_init(smem_addr(&sh.acc_empty[b]), 2 * kEpilogueWarps);
+            bar_init(smem_addr(&sh.acc_empty[b]), 2 * (STATS ? kStatsWarps : kStoreWarps));
         }
         bar_init(smem_addr(&sh.drained), 1);
         sh.dead = 0;
@@ -430,33 +479,100 @@ loss_products(const __grid_constant__ ProductParams p) {
             bool ok = true;
             for (long long i = pair; i < n_work && ok; i += pairs) {
                 const Tile t = tile_of(i, m_tiles, n_tiles, k_blocks, p.splits);
-                ok = wait_for(&sh.acc_empty[buf], acc_phase ^ 1, dead, limit, p.status);
-                if (!ok) break;
-                tc_fence_after();
-                for (int k = t.k0; k < t.k1; ++k) {
-                    ok = wait_for(&sh.full[stage], phase, dead, limit, p.status);
+                for (int k0 = t.k0; k0 < t.k1 || k0 == t.k0; k0 += kChunk) {
+                    const int k1 = STATS && t.k1 > k0 + kChunk ? k0 + kChunk : t.k1;
+                    ok = wait_for(&sh.acc_empty[buf], acc_phase ^ 1, dead, limit, p.status);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint64_t a = operand_desc(stage0 + stage * kStageBytes, a_mn);
-                    const uint64_t b = operand_desc(stage0 + stage * kStageBytes + kOperandBytes, b_mn);
+                    for (int k = k0; k < k1; ++k) {
+                        ok = wait_for(&sh.full[stage], phase, dead, limit, p.status);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t a = operand_desc(stage0 + stage * kStageBytes, a_mn);
+                        const uint64_t b = operand_desc(stage0 + stage * kStageBytes + kOperandBytes, b_mn);
 #pragma unroll
-                    for (int j = 0; j < kTileK / 16; ++j)
-                        mma_pair(tmem + buf * kTileN, a + j * a_step, b + j * b_step, idesc, k > t.k0 || j > 0);
-                    mma_commit(smem_addr(&sh.empty[stage]));
-                    if (++stage == kStages) {
-                        stage = 0;
-                        phase ^= 1;
+                        for (int j = 0; j < kTileK / 16; ++j)
+                            mma_pair(tmem + buf * kTileN, a + j * a_step, b + j * b_step, idesc, k > k0 || j > 0);
+                        mma_commit(smem_addr(&sh.empty[stage]));
+                        if (++stage == kStages) {
+                            stage = 0;
+                            phase ^= 1;
+                        }
                     }
+                    if (!ok) break;
+                    mma_commit(smem_addr(&sh.acc_full[buf]));
+                    buf ^= 1;
+                    if (buf == 0) acc_phase ^= 1;
+                    if (!STATS) break;
                 }
-                if (!ok) break;
-                mma_commit(smem_addr(&sh.acc_full[buf]));
-                buf ^= 1;
-                if (buf == 0) acc_phase ^= 1;
             }
             if (!ok) {  // the products already issued still read shared memory
                 mma_commit(smem_addr(&sh.drained));
                 for (int i = 0; i < 4096 && !bar_try(smem_addr(&sh.drained), 0); ++i) __nanosleep(256);
             }
+        }
+    } else if constexpr (STATS) {  // ------------------------------- statistics
+        const int quad = warp & 3;  // the quarter of the lanes this warp may read
+        const int half = (warp - 2) >> 2;  // which half of the columns it takes
+        int buf = 0;
+        uint32_t acc_phase = 0;
+        bool ok = true;
+        for (long long i = pair; i < n_work && ok; i += pairs) {
+            const Tile t = tile_of(i, m_tiles, n_tiles, k_blocks, p.splits);
+            float z[kStatsColumns];
+#pragma unroll
+            for (int j = 0; j < kStatsColumns; ++j) z[j] = 0.0f;
+            for (int k0 = t.k0; k0 < t.k1; k0 += kChunk) {
+                const bool got = wait_for(&sh.acc_full[buf], acc_phase, dead, limit, p.status);
+                ok = __all_sync(0xffffffffu, got);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t acc = tmem + buf * kTileN + half * kStatsColumns + ((uint32_t)(quad * 32) << 16);
+#pragma unroll
+                for (int c = 0; c < kStatsColumns; c += 16) {
+                    float part[16];
+                    tmem_load16(acc + c, part);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) z[c + j] = __fadd_rn(z[c + j], part[j]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive_cluster(in_cta(smem_addr(&sh.acc_empty[buf]), 0));
+                buf ^= 1;
+                if (buf == 0) acc_phase ^= 1;
+            }
+            if (!ok) break;
+            const long long token = (long long)t.m * kTileM + (int)rank * kHalf + quad * 32 + lane;
+            const bool mine = token < p.tokens;
+            const int part_index = t.n * 2 + half;
+            const long long v0 = (long long)part_index * kStatsColumns;
+            const long long left = p.vocab - v0;  // columns that exist
+            if (left <= 0) continue;
+            const long long at = mine ? p.target[token] - v0 : -1;
+            if (left < kStatsColumns) {
+#pragma unroll
+                for (int j = 0; j < kStatsColumns; ++j)
+                    if (j >= left) z[j] = -INFINITY;
+            }
+            if (__any_sync(0xffffffffu, at >= 0 && at < kStatsColumns)) {
+                float z_y = 0.0f;
+#pragma unroll
+                for (int j = 0; j < kStatsColumns; ++j) z_y = j == at ? z[j] : z_y;
+                if (at >= 0 && at < kStatsColumns) p.picked[token] = z_y;
+            }
+            float tops[4] = {z[0], z[1], z[2], z[3]}, sums[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int j = 4; j < kStatsColumns; ++j) tops[j & 3] = fmaxf(tops[j & 3], z[j]);
+            const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+            // a row of -inf: any finite base leaves its sum at 0
+            const float high = top == -INFINITY ? 0.0f : top;
+            const float base = __fmul_rn(high, kLog2e);
+#pragma unroll
+            for (int j = 0; j < kStatsColumns; ++j) sums[j & 3] += exp2_approx(__fmaf_rn(z[j], kLog2e, -base));
+            // the sum is relative to 2^base, and base to top log2(e) rounded once
+            const float miss = __fmaf_rn(high, kLog2e, -base);
+            const float sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+            if (mine) p.parts[part_index * p.tokens + token] = make_float2(top, __fmaf_rn(sum, -miss * kLn2, sum));
         }
     } else {  // ------------------------------------------------------ results
         const int quad = warp & 3;  // the quarter of the lanes this warp may read
@@ -464,27 +580,8 @@ loss_products(const __grid_constant__ ProductParams p) {
         const float factor = p.kind >= kGradHidden ? p.record->factor : 1.0f;
         int buf = 0, out_buf = 0;
         uint32_t acc_phase = 0;
-        // one swizzled row of 128 bytes per lane, then one store by lane 0
-        auto put = [&](const uint32_t w[32], const CUtensorMap *map, int x, int y, bool add, bool skip) {
-            if (lane == 0) store_wait_read<1>();
-            __syncwarp();
-            const uint32_t row = stage_out + out_buf * kStoreBytes + lane * 128;
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((c ^ (lane & 7)) << 4)), "r"(w[4 * c]),
-                             "r"(w[4 * c + 1]), "r"(w[4 * c + 2]), "r"(w[4 * c + 3])
-                             : "memory");
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) {
-                if (!skip) {
-                    if (add)
-                        tma_add(map, x, y, stage_out + out_buf * kStoreBytes);
-                    else
-                        tma_store(map, x, y, stage_out + out_buf * kStoreBytes);
-                }
-                store_commit();
-            }
+        auto put = [&](const uint32_t (&w)[32], const CUtensorMap *map, int x, int y, bool add, bool skip) __attribute__((always_inline)) {
+            put_rows(w, stage_out + out_buf * kStoreBytes, lane, map, x, y, add, skip);
             out_buf ^= 1;
         };
         for (long long i = pair; i < n_work; i += pairs) {
@@ -494,72 +591,34 @@ loss_products(const __grid_constant__ ProductParams p) {
             if (!__all_sync(0xffffffffu, got)) break;
             tc_fence_after();
             const uint32_t acc = tmem + buf * kTileN + ((uint32_t)(quad * 32) << 16);
-            if (p.kind == kStats) {
-                const long long token = row0 + lane;
-                const bool mine = token < p.tokens;
-                const long long y = mine ? p.target[token] : -1;
-                const long long v0 = p.piece0 + (long long)t.n * kTileN;
-                const long long left = p.vocab - v0;  // columns of the tile that exist
-                float top = -INFINITY, sum = 0.0f;
-                for (int c = 0; c < kTileN && c < left; c += 32) {
-                    float z[32];
-                    tmem_load32(acc + c, z);
-                    if (left - c < 32) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (j >= left - c) z[j] = -INFINITY;
-                    }
-                    const long long at = y - v0 - c;
-                    if (__any_sync(0xffffffffu, at >= 0 && at < 32)) {
-                        float z_y = 0.0f;
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) z_y = j == at ? z[j] : z_y;
-                        if (at >= 0 && at < 32) p.picked[token] = z_y;
-                    }
-                    float high = z[0];
-#pragma unroll
-                    for (int j = 1; j < 32; ++j) high = fmaxf(high, z[j]);
-                    high = fmaxf(high, top);
-                    // a row of -inf so far: any finite base leaves its sum at 0
-                    const float base = (high == -INFINITY ? 0.0f : high) * kLog2e;
-                    float s = 0.0f;
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) s += exp2_approx(__fmaf_rn(z[j], kLog2e, -base));
-                    sum = sum * exp2_approx(__fmaf_rn(top, kLog2e, -base)) + s;
-                    top = high;
-                }
-                if (mine) p.parts[t.n * p.tokens + token] = make_float2(top, sum);
-            } else if (p.kind == kSlopes) {
+            if (p.kind == kSlopes) {
                 const int place = row0 + lane;
                 const float lse2 = p.lse2[place], ratio = p.ratio[place];
                 const bool live = p.place_target[place] >= 0;  // not a row that fills the last tile
                 const int y = p.place_target[place] - (int)p.piece0 - t.n * kTileN;
                 const long long left = p.vocab - p.piece0 - (long long)t.n * kTileN;
+                // q of 32 columns, packed
+                auto q_of = [&](int col, uint32_t *w) __attribute__((always_inline)) {
+                    float z[32];
+                    tmem_load32(acc + col, z);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) z[j] = exp2_approx(__fmaf_rn(z[j], kLog2e, -lse2));
+                    if (__any_sync(0xffffffffu, y >= col && y < col + 32)) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) z[j] = j == y - col ? z[j] - 1.0f : z[j];
+                    }
+                    const long long keep = live ? left - col : 0;  // columns that exist, in a row that counts
+                    if (keep < 32) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) z[j] = j < keep ? z[j] : 0.0f;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) w[j] = pack_lp<BF16>(z[2 * j] * ratio, z[2 * j + 1] * ratio);
+                };
                 for (int c = 0; c < kTileN; c += 64) {
                     uint32_t w[32];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float z[32];
-                        const int col = c + 32 * h;
-                        tmem_load32(acc + col, z);
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) z[j] = exp2_approx(__fmaf_rn(z[j], kLog2e, -lse2));
-                        if (__any_sync(0xffffffffu, y >= col && y < col + 32)) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) z[j] = j == y - col ? z[j] - 1.0f : z[j];
-                        }
-                        if (left - col < 32) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (j >= left - col) z[j] = 0.0f;
-                        }
-                        if (!live) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) z[j] = 0.0f;
-                        }
-#pragma unroll
-                        for (int j = 0; j < 32; j += 2) w[16 * h + j / 2] = pack_lp<BF16>(z[j] * ratio, z[j + 1] * ratio);
-                    }
+                    q_of(c, w);
+                    q_of(c + 32, w + 16);
                     put(w, &p.q_out, t.n * kTileN + c, row0, false, false);
                 }
             } else if (p.kind == kGradHidden) {
@@ -574,19 +633,18 @@ loss_products(const __grid_constant__ ProductParams p) {
                         t.n * kTileN + c >= p.dim);
                 }
             } else {
+                // no token counts: the accumulator was never written
+                auto scaled = [&](int col, uint32_t *w) __attribute__((always_inline)) {
+                    float z[32];
+                    tmem_load32(acc + col, z);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        w[j] = k_blocks ? pack_lp<BF16>(z[2 * j] * factor, z[2 * j + 1] * factor) : 0u;
+                };
                 for (int c = 0; c < kTileN; c += 64) {
                     uint32_t w[32];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float z[32];
-                        tmem_load32(acc + c + 32 * h, z);
-#pragma unroll
-                        for (int j = 0; j < 32; j += 2) {
-                            // no token counts: the accumulator was never written
-                            const float x0 = k_blocks ? z[j] * factor : 0.0f, x1 = k_blocks ? z[j + 1] * factor : 0.0f;
-                            w[16 * h + j / 2] = pack_lp<BF16>(x0, x1);
-                        }
-                    }
+                    scaled(c, w);
+                    scaled(c + 32, w + 16);
                     put(w, &p.gw_out, t.n * kTileN + c, (int)p.piece0 + row0, false,
                         t.n * kTileN + c >= p.dim || p.piece0 + row0 >= p.vocab);
                 }
@@ -797,14 +855,14 @@ bool make_map(CUtensorMap *m, const void *p, int64_t rows, int64_t cols, int64_t
 }
 
 // pairs of CTAs that run at once
-template <bool BF16>
+template <bool BF16, bool STATS>
 int pairs_at_once() {
     static const int n = [] {
-        if (cudaFuncSetAttribute(loss_products<BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess)
+        if (cudaFuncSetAttribute(loss_products<BF16, STATS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess)
             return 0;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2);
-        cfg.blockDim = dim3(kProductThreads);
+        cfg.blockDim = dim3(product_threads<STATS>());
         cfg.dynamicSmemBytes = kSmemBytes;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -813,7 +871,7 @@ int pairs_at_once() {
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         int clusters = 0;
-        if (cudaOccupancyMaxActiveClusters(&clusters, loss_products<BF16>, &cfg) != cudaSuccess || clusters < 1) {
+        if (cudaOccupancyMaxActiveClusters(&clusters, loss_products<BF16, STATS>, &cfg) != cudaSuccess || clusters < 1) {
             cudaGetLastError();
             clusters = sm_count() / 2;
         }
@@ -824,12 +882,12 @@ int pairs_at_once() {
 
 std::atomic<long long> g_wait_cycles{4000000000ll};  // about two seconds
 
-template <bool BF16>
+template <bool BF16, bool STATS>
 cudaError_t launch_products(const ProductParams &p, int64_t tiles, cudaStream_t stream) {
-    const int pairs = pairs_at_once<BF16>();
+    const int pairs = pairs_at_once<BF16, STATS>();
     if (pairs < 1) return cudaErrorInvalidConfiguration;
     const int64_t use = std::max<int64_t>(1, std::min<int64_t>(pairs, tiles));
-    return launch_pdl(loss_products<BF16>, dim3((unsigned)(2 * use)), dim3(kProductThreads), kSmemBytes, stream, p);
+    return launch_pdl(loss_products<BF16, STATS>, dim3((unsigned)(2 * use)), dim3(product_threads<STATS>()), kSmemBytes, stream, p);
 }
 
 template <bool BF16>
@@ -844,15 +902,15 @@ cudaError_t forward_impl(const LossArgs &a, cudaStream_t stream) {
     p.dim = a.dim;
     p.splits = 1;
     p.target = a.target;
-    const int64_t tiles = up(a.vocab, kTileN) / kTileN;
+    const int64_t tiles = up(a.vocab, kTileN) / kTileN, parts = up(a.vocab, kStatsColumns) / kStatsColumns;
     p.parts = static_cast<float2 *>(a.workspace);
-    p.picked = reinterpret_cast<float *>(p.parts + tiles * a.tokens);
+    p.picked = reinterpret_cast<float *>(p.parts + parts * a.tokens);
     p.status = a.status;
     p.wait_cycles = g_wait_cycles.load();
-    cudaError_t e = launch_products<BF16>(p, up(a.tokens, kTileM) / kTileM * tiles, stream);
+    cudaError_t e = launch_products<BF16, true>(p, up(a.tokens, kTileM) / kTileM * tiles, stream);
     if (e != cudaSuccess) return e;
     return launch_pdl(loss_join, dim3((unsigned)((a.tokens + kJoinTokens - 1) / kJoinTokens)),
-                      dim3(kJoinTokens * kJoinWays), 0, stream, (const float2 *)p.parts, (const float *)p.picked, (int)tiles,
+                      dim3(kJoinTokens * kJoinWays), 0, stream, (const float2 *)p.parts, (const float *)p.picked, (int)parts,
                       a.target, (long long)a.ignore, (long long)a.tokens, (long long)a.vocab, a.loss, a.lse, a.status);
 }
 
@@ -904,12 +962,12 @@ cudaError_t backward_impl(const LossArgs &a, cudaStream_t stream) {
         p.first_piece = i == 0;
         p.splits = 1;
         p.kind = kSlopes;
-        e = launch_products<BF16>(p, row_tiles * piece_tiles, stream);
+        e = launch_products<BF16, false>(p, row_tiles * piece_tiles, stream);
         p.kind = kGradWeight;
-        if (e == cudaSuccess) e = launch_products<BF16>(p, piece_tiles * dim_tiles, stream);
+        if (e == cudaSuccess) e = launch_products<BF16, false>(p, piece_tiles * dim_tiles, stream);
         p.kind = kGradHidden;
         p.splits = l.splits;
-        if (e == cudaSuccess) e = launch_products<BF16>(p, row_tiles * dim_tiles * l.splits, stream);
+        if (e == cudaSuccess) e = launch_products<BF16, false>(p, row_tiles * dim_tiles * l.splits, stream);
     }
     if (e == cudaSuccess)
         e = launch_pdl(loss_finish<BF16>, dim3((unsigned)copies), dim3(kCopyThreads), 0, stream, reinterpret_cast<const float4 *>(sums),
@@ -922,7 +980,7 @@ cudaError_t backward_impl(const LossArgs &a, cudaStream_t stream) {
 
 void set_loss_wait(int64_t cycles) { g_wait_cycles.store(cycles); }
 
-int64_t loss_forward_bytes(int64_t tokens, int64_t vocab) { return up(vocab, kTileN) / kTileN * tokens * 8 + up(tokens * 4, 16); }
+int64_t loss_forward_bytes(int64_t tokens, int64_t vocab) { return up(vocab, kStatsColumns) / kStatsColumns * tokens * 8 + up(tokens * 4, 16); }
 
 cudaError_t launch_loss_forward(const LossArgs &a, cudaStream_t stream) {
     return a.lp ? forward_impl<true>(a, stream) : forward_impl<false>(a, stream);
