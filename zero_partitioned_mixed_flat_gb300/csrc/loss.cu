@@ -39,17 +39,17 @@ constexpr int kOperandBytes = kHalf * kTileK * 2;
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kBoxBytes = 64 * kTileK * 2;  // a 64 x 64 box of an operand whose rows run along K
 constexpr int kStoreBytes = 32 * 128;       // 32 rows of 128 bytes: one warp's store
-constexpr int kStatsWarps = 8;     // that take a tile's results, two on each quarter of the rows
-constexpr int kStoreWarps = 4;
-constexpr int kStoreSmem = kStoreWarps * 2 * kStoreBytes;
-constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kStoreSmem;
-constexpr int kStatsColumns = kTileN / 2;  // of one statistics warp
+constexpr int kResultWarps = 8;              // that take a tile's results: two on each quarter of its rows
+constexpr int kResultColumns = kTileN / 2;   // of one of them
+constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kResultWarps * kStoreBytes;
+constexpr int kProductThreads = 64 + 32 * kResultWarps;
 // The tensor core's float sum drops the low bits of every step of 16, always
 // towards zero: a logit of 15 over 4096 products came out 6e-5 too small, a
 // relative 4e-6 where float addition has 4e-8.  The losses are float, so the
 // statistics take the sum off after kChunk blocks (512 products) and add it up
 // in registers, rounded to nearest; q is rounded to lp anyway and does without.
 constexpr int kChunk = 8;
+constexpr int kTileCost = 4;  // blocks of K that starting and storing a tile cost, about
 constexpr int kTmemColumns = 512;  // two accumulators of 256 columns
 
 // The largest |grad_loss| becomes this in the lp operand q: fp16 keeps 15 more
@@ -71,6 +71,7 @@ struct BackwardLayout {
     int64_t index, place, lse2, ratio, target, hidden, slopes, sums, bytes;  // byte offsets
 };
 
+constexpr int kPairs = 76;  // of SMs
 constexpr int64_t kSlopeBytes = int64_t(256) << 20;  // a piece of q takes about this much at most
 
 int64_t up(int64_t x, int64_t q) { return (x + q - 1) / q * q; }
@@ -82,18 +83,13 @@ BackwardLayout backward_layout(int64_t tokens, int64_t vocab, int dim) {
     l.pieces = (int)((vocab + most - 1) / most);
     l.piece = up((vocab + l.pieces - 1) / l.pieces, kTileN);
     l.pieces = (int)((vocab + l.piece - 1) / l.piece);
-    // grad_hidden has few tiles and long sums: cut the sums so that the last
-    // round of tiles is nearly full (at most 16 ways, 8 blocks of K each at least)
-    const int64_t tiles = l.rows / kTileM * ((dim + kTileN - 1) / kTileN), pairs = 76;
-    double best = 1e30;
+    // grad_hidden has few tiles and long sums: cut its sums until no part is longer
+    // than a pair's share of both gradients (at most 16 ways, 8 blocks of K each)
+    const int64_t dim_tiles = (dim + kTileN - 1) / kTileN, row_tiles = l.rows / kTileM;
+    const int64_t long_sum = l.piece / kTileK, short_sum = (tokens + kTileK - 1) / kTileK;
+    const int64_t share = (row_tiles * dim_tiles * long_sum + l.piece / kTileN * dim_tiles * short_sum) / kPairs;
     l.splits = 1;
-    for (int s = 1; s <= 16 && l.piece / kTileK / s >= 8; ++s) {
-        const double rounds = double((tiles * s + pairs - 1) / pairs) / s + 0.02 * s;
-        if (rounds < best) {
-            best = rounds;
-            l.splits = s;
-        }
-    }
+    while (l.splits < 16 && long_sum / l.splits > share && long_sum / (l.splits + 1) >= 8) ++l.splits;
     int64_t at = 256;
     auto take = [&](int64_t bytes) {
         const int64_t here = at;
@@ -174,10 +170,7 @@ __device__ __forceinline__ void tma_add(const CUtensorMap *map, int x, int y, ui
 }
 
 __device__ __forceinline__ void store_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void store_wait_read() {
-    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
-}
+__device__ __forceinline__ void store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void store_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 // Shared-memory operand descriptor, 128-byte swizzle.  Rows of 128 bytes, eight
@@ -261,7 +254,7 @@ __device__ __forceinline__ uint32_t pack_lp(float a, float b) {
 
 // ------------------------------------------------------------------- products
 
-enum Product { kStats = 0, kSlopes = 1, kGradHidden = 2, kGradWeight = 3 };
+enum Product { kLogits = 0, kGradHidden = 1, kGradWeight = 2 };
 
 struct ProductParams {
     CUtensorMap h_k, hc_k;    // hidden states (all, the counted ones): boxes 64 of D x 128 tokens
@@ -273,49 +266,124 @@ struct ProductParams {
     CUtensorMap q_out;        // q: 64 vocabulary x 32 tokens
     CUtensorMap gh_out;       // partial grad_hidden: 32 of D x 32 tokens, float
     CUtensorMap gw_out;       // grad_weight: 64 of D x 32 vocabulary
-    int kind;
+    int gradients;  // both gradients of the piece, else its logits (statistics or q)
     long long tokens, vocab;
     int dim;
-    long long piece0, piece;  // the piece of the vocabulary (kStats: all of it)
+    long long piece0, piece;  // the piece of the vocabulary (statistics: all of it)
     long long rows;           // tokens rounded up to whole tiles
     int splits;
     int first_piece;
     const LossRecord *record;  // NULL: every token counts
-    // kStats
+    // statistics
     const int64_t *target;
-    float2 *parts;  // [kStatsColumns columns of the vocabulary][token]
+    float2 *parts;  // [kResultColumns columns of the vocabulary][token]
     float *picked;  // the target's logit
-    // kSlopes (by place among the counted tokens)
+    // q, by place among the counted tokens
     const float *lse2, *ratio;
     const int *place_target;
     int *status;
     long long wait_cycles;
 };
 
+// A tile's product.
 struct Tile {
-    int m, n;        // tile coordinates
-    int k0, k1;      // blocks of K
-    int split;
+    int kind;
+    int m0, n0;   // its first row and column
+    int width;    // columns of the product: fewer in a last tile that few columns need
+    int k0, k1;   // blocks of K
+    int split;    // which of the partial sums of grad_hidden
+    int n;        // its number along the columns
 };
 
-// Consecutive tiles take 8 tiles of M for one of N before the next of N, so the
-// pairs that run together read few different rows of either operand from L2.
-__device__ __forceinline__ Tile tile_of(long long i, int m_tiles, int n_tiles, int k_blocks, int splits) {
-    Tile t;
-    const long long per_split = (long long)m_tiles * n_tiles;
-    t.split = (int)(i / per_split);
-    const long long r = i - t.split * per_split;
-    constexpr int kGroup = 8;
-    const long long per_group = (long long)kGroup * n_tiles;
-    const int g = (int)(r / per_group);
-    const int in_group = m_tiles - g * kGroup < kGroup ? m_tiles - g * kGroup : kGroup;
-    const int q = (int)(r - g * per_group);
-    t.n = q / in_group;
-    t.m = g * kGroup + q % in_group;
-    t.k0 = (int)((long long)k_blocks * t.split / splits);
-    t.k1 = (int)((long long)k_blocks * (t.split + 1) / splits);
-    return t;
-}
+// A grid of tiles.
+struct Tiles {
+    int m, n, columns, k_blocks, splits;
+
+    __device__ __forceinline__ long long size() const { return (long long)m * n * splits; }
+
+    // Consecutive tiles take 8 tiles of M for one of N before the next of N, so the
+    // pairs that run together read few different rows of either operand from L2.
+    __device__ __forceinline__ Tile at(long long i, int kind) const {
+        Tile t;
+        t.kind = kind;
+        const long long per_split = (long long)m * n;
+        t.split = (int)(i / per_split);
+        const long long r = i - t.split * per_split;
+        constexpr int kGroup = 8;
+        const long long per_group = (long long)kGroup * n;
+        const int g = (int)(r / per_group);
+        const int in_group = m - g * kGroup < kGroup ? m - g * kGroup : kGroup;
+        const int q = (int)(r - g * per_group);
+        t.n = q / in_group;
+        t.n0 = t.n * kTileN;
+        t.m0 = (g * kGroup + q % in_group) * kTileM;
+        const int left = (columns - t.n0 + 31) / 32 * 32;
+        t.width = left < kTileN ? left : kTileN;
+        t.k0 = (int)((long long)k_blocks * t.split / splits);
+        t.k1 = (int)((long long)k_blocks * (t.split + 1) / splits);
+        return t;
+    }
+};
+
+// The work of one launch, and which of it each pair does, in order.  Logits:
+// every pair-th tile.  Gradients: first the tiles of grad_hidden, few and long,
+// every pair-th; the pairs that get one fewer of them then take `catch_up` tiles
+// of grad_weight each, about as long together as one of the others; the rest of
+// grad_weight goes round all pairs.  Both products run in one launch because
+// grad_hidden alone leaves the last round of pairs mostly idle.
+struct Work {
+    Tiles logits, hidden, weight;
+    int gradients;
+    long long pair, pairs, n_hidden, n_weight;
+    int fuller;  // pairs with one more tile of grad_hidden than the others, if not all have as many
+    int catch_up;
+
+    __device__ __forceinline__ Work(const ProductParams &p, long long count) {
+        const long long end = p.piece0 + p.piece < p.vocab ? p.piece0 + p.piece : p.vocab;
+        const int columns = (int)(end - p.piece0);
+        const int row_tiles = (int)((count + kTileM - 1) / kTileM);
+        const int dim_tiles = (p.dim + kTileN - 1) / kTileN, piece_tiles = (columns + kTileN - 1) / kTileN;
+        logits = {row_tiles, piece_tiles, columns, (p.dim + kTileK - 1) / kTileK, 1};
+        hidden = {row_tiles, dim_tiles, p.dim, (columns + kTileK - 1) / kTileK, p.splits};
+        weight = {piece_tiles, dim_tiles, p.dim, (int)((count + kTileK - 1) / kTileK), 1};
+        gradients = p.gradients;
+        pair = blockIdx.x >> 1;
+        pairs = gridDim.x >> 1;
+        n_hidden = hidden.size();
+        n_weight = weight.size();
+        fuller = (int)(n_hidden % pairs);
+        const int long_tile = hidden.k_blocks / hidden.splits + kTileCost, short_tile = weight.k_blocks + kTileCost;
+        catch_up = fuller ? (long_tile + short_tile / 2) / short_tile : 0;
+        const long long most = fuller ? n_weight / (pairs - fuller) : 0;
+        if (catch_up > most) catch_up = (int)most;
+    }
+
+    __device__ __forceinline__ bool at(long long j, Tile &t) const {
+        if (!gradients) {
+            const long long i = pair + j * pairs;
+            if (i >= logits.size()) return false;
+            t = logits.at(i, kLogits);
+            return true;
+        }
+        const long long mine = n_hidden > pair ? (n_hidden - pair + pairs - 1) / pairs : 0;
+        if (j < mine) {
+            t = hidden.at(pair + j * pairs, kGradHidden);
+            return true;
+        }
+        j -= mine;
+        const long long others = pairs - fuller;
+        long long i;
+        if (catch_up && pair >= fuller && j < catch_up) {
+            i = pair - fuller + j * others;
+        } else {
+            if (catch_up && pair >= fuller) j -= catch_up;
+            i = catch_up * others + pair + j * pairs;
+        }
+        if (i >= n_weight) return false;
+        t = weight.at(i, kGradWeight);
+        return true;
+    }
+};
 
 struct Shared {
     uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
@@ -340,11 +408,12 @@ __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatil
     return true;
 }
 
-// 32 rows of 128 bytes, one a lane, to a box of `map`: swizzled into this half of
-// the warp's two buffers (whose last store lies two calls back), then one store
+// 32 rows of 128 bytes, one a lane, to a box of `map`: swizzled into the warp's
+// buffer once its last store has read it, then one store.  (A second buffer a
+// warp costs a stage of operands: 4096 x 4096 x 50257 took 4.71 ms, not 4.66.)
 __device__ __forceinline__ void put_rows(const uint32_t (&w)[32], uint32_t buffer, int lane, const CUtensorMap *map, int x,
                                          int y, bool add, bool skip) {
-    if (lane == 0) store_wait_read<1>();
+    if (lane == 0) store_wait_read();
     __syncwarp();
     const uint32_t row = buffer + lane * 128;
 #pragma unroll
@@ -365,11 +434,8 @@ __device__ __forceinline__ void put_rows(const uint32_t (&w)[32], uint32_t buffe
     }
 }
 
-template <bool STATS>
-constexpr int product_threads() { return 64 + 32 * (STATS ? kStatsWarps : kStoreWarps); }
-
 template <bool BF16, bool STATS>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(product_threads<STATS>(), 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
 loss_products(const __grid_constant__ ProductParams p) {
     extern __shared__ unsigned char raw[];
     __shared__ Shared sh;
@@ -386,7 +452,7 @@ loss_products(const __grid_constant__ ProductParams p) {
         }
         for (int b = 0; b < 2; ++b) {
             bar_init(smem_addr(&sh.acc_full[b]), 1);
-            bar_init(smem_addr(&sh.acc_empty[b]), 2 * (STATS ? kStatsWarps : kStoreWarps));
+            bar_init(smem_addr(&sh.acc_empty[b]), 2 * kResultWarps);
         }
         bar_init(smem_addr(&sh.drained), 1);
         sh.dead = 0;
@@ -409,55 +475,39 @@ loss_products(const __grid_constant__ ProductParams p) {
     const long long limit = p.wait_cycles;
     const bool all = p.record == nullptr || p.record->count == p.tokens;
     const long long count = p.record ? p.record->count : p.tokens;
-    int m_tiles, n_tiles, k_blocks;
-    const long long piece_end = p.piece0 + p.piece < p.vocab ? p.piece0 + p.piece : p.vocab;
-    const int row_tiles = (int)((count + kTileM - 1) / kTileM);
-    const int vocab_tiles = (int)((piece_end - p.piece0 + kTileN - 1) / kTileN);
-    if (p.kind == kGradHidden) {
-        m_tiles = row_tiles;
-        n_tiles = (p.dim + kTileN - 1) / kTileN;
-        k_blocks = (int)((piece_end - p.piece0 + kTileK - 1) / kTileK);
-    } else if (p.kind == kGradWeight) {
-        m_tiles = vocab_tiles;
-        n_tiles = (p.dim + kTileN - 1) / kTileN;
-        k_blocks = (int)((count + kTileK - 1) / kTileK);
-    } else {
-        m_tiles = row_tiles;
-        n_tiles = vocab_tiles;
-        k_blocks = (p.dim + kTileK - 1) / kTileK;
-    }
-    const long long n_work = (long long)m_tiles * n_tiles * p.splits;
-    const long long pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-    const bool a_mn = p.kind == kGradWeight, b_mn = p.kind >= kGradHidden;
+    const Work work(p, count);
+    Tile t;
 
     if (warp == 0) {
         if (lane == 0) {  // ------------------------------------------ loads
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (long long i = pair; i < n_work && ok; i += pairs) {
-                const Tile t = tile_of(i, m_tiles, n_tiles, k_blocks, p.splits);
-                const int m0 = t.m * kTileM + (int)rank * kHalf, n0 = t.n * kTileN + (int)rank * kHalf;
+            for (long long j = 0; ok && work.at(j, t); ++j) {
+                // this CTA's rows of A, and its half of the columns of B
+                const int m0 = t.m0 + (int)rank * kHalf, n0 = t.n0 + (int)rank * (t.width / 2);
+                const bool two = t.width > kTileN / 2;  // boxes of 64 columns that hold its half
+                const uint32_t bytes = 2 * (t.kind == kLogits || two ? kStageBytes : kStageBytes - kBoxBytes);
                 for (int k = t.k0; k < t.k1; ++k) {
                     ok = wait_for(&sh.empty[stage], phase ^ 1, dead, limit, p.status);
                     if (!ok) break;
                     const uint32_t a = stage0 + stage * kStageBytes, b = a + kOperandBytes;
                     const uint32_t bar = in_cta(smem_addr(&sh.full[stage]), 0);
-                    if (rank == 0) bar_expect(smem_addr(&sh.full[stage]), 2 * kStageBytes);
+                    if (rank == 0) bar_expect(smem_addr(&sh.full[stage]), bytes);
                     const int kk = k * kTileK;
-                    if (p.kind <= kSlopes) {
+                    if (t.kind == kLogits) {
                         tma_load(a, all ? &p.h_k : &p.hc_k, kk, m0, bar);
                         tma_load(b, &p.w_k, kk, (int)p.piece0 + n0, bar);
-                    } else if (p.kind == kGradHidden) {
+                    } else if (t.kind == kGradHidden) {
                         tma_load(a, &p.q_k, kk, m0, bar);
                         tma_load(b, &p.w_mn, n0, (int)p.piece0 + kk, bar);
-                        tma_load(b + kBoxBytes, &p.w_mn, n0 + 64, (int)p.piece0 + kk, bar);
+                        if (two) tma_load(b + kBoxBytes, &p.w_mn, n0 + 64, (int)p.piece0 + kk, bar);
                     } else {
                         const CUtensorMap *h = all ? &p.h_mn : &p.hc_mn;
                         tma_load(a, &p.q_mn, m0, kk, bar);
                         tma_load(a + kBoxBytes, &p.q_mn, m0 + 64, kk, bar);
                         tma_load(b, h, n0, kk, bar);
-                        tma_load(b + kBoxBytes, h, n0 + 64, kk, bar);
+                        if (two) tma_load(b + kBoxBytes, h, n0 + 64, kk, bar);
                     }
                     if (++stage == kStages) {
                         stage = 0;
@@ -468,17 +518,17 @@ loss_products(const __grid_constant__ ProductParams p) {
         }
     } else if (warp == 1) {
         if (rank == 0 && lane == 0) {  // ------------------------- products
-            uint32_t idesc = 1u << 4;  // float sums
-            if (BF16) idesc |= 1u << 7 | 1u << 10;
-            idesc |= (uint32_t)a_mn << 15 | (uint32_t)b_mn << 16;
-            idesc |= (uint32_t)(kTileN >> 3) << 17 | (uint32_t)(kTileM >> 4) << 24;
-            // 16 of K further: 32 bytes along a row, or 16 rows
-            const uint64_t a_step = (a_mn ? 16 * 128 : 32) >> 4, b_step = (b_mn ? 16 * 128 : 32) >> 4;
             int stage = 0, buf = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true;
-            for (long long i = pair; i < n_work && ok; i += pairs) {
-                const Tile t = tile_of(i, m_tiles, n_tiles, k_blocks, p.splits);
+            for (long long j = 0; ok && work.at(j, t); ++j) {
+                const bool a_mn = t.kind == kGradWeight, b_mn = t.kind != kLogits;
+                uint32_t idesc = 1u << 4;  // float sums
+                if (BF16) idesc |= 1u << 7 | 1u << 10;
+                idesc |= (uint32_t)a_mn << 15 | (uint32_t)b_mn << 16;
+                idesc |= (uint32_t)(t.width >> 3) << 17 | (uint32_t)(kTileM >> 4) << 24;
+                // 16 of K further: 32 bytes along a row, or 16 rows
+                const uint64_t a_step = (a_mn ? 16 * 128 : 32) >> 4, b_step = (b_mn ? 16 * 128 : 32) >> 4;
                 for (int k0 = t.k0; k0 < t.k1 || k0 == t.k0; k0 += kChunk) {
                     const int k1 = STATS && t.k1 > k0 + kChunk ? k0 + kChunk : t.k1;
                     ok = wait_for(&sh.acc_empty[buf], acc_phase ^ 1, dead, limit, p.status);
@@ -491,8 +541,8 @@ loss_products(const __grid_constant__ ProductParams p) {
                         const uint64_t a = operand_desc(stage0 + stage * kStageBytes, a_mn);
                         const uint64_t b = operand_desc(stage0 + stage * kStageBytes + kOperandBytes, b_mn);
 #pragma unroll
-                        for (int j = 0; j < kTileK / 16; ++j)
-                            mma_pair(tmem + buf * kTileN, a + j * a_step, b + j * b_step, idesc, k > k0 || j > 0);
+                        for (int i = 0; i < kTileK / 16; ++i)
+                            mma_pair(tmem + buf * kTileN, a + i * a_step, b + i * b_step, idesc, k > k0 || i > 0);
                         mma_commit(smem_addr(&sh.empty[stage]));
                         if (++stage == kStages) {
                             stage = 0;
@@ -517,19 +567,18 @@ loss_products(const __grid_constant__ ProductParams p) {
         int buf = 0;
         uint32_t acc_phase = 0;
         bool ok = true;
-        for (long long i = pair; i < n_work && ok; i += pairs) {
-            const Tile t = tile_of(i, m_tiles, n_tiles, k_blocks, p.splits);
-            float z[kStatsColumns];
+        for (long long j = 0; ok && work.at(j, t); ++j) {
+            float z[kResultColumns];
 #pragma unroll
-            for (int j = 0; j < kStatsColumns; ++j) z[j] = 0.0f;
+            for (int j = 0; j < kResultColumns; ++j) z[j] = 0.0f;
             for (int k0 = t.k0; k0 < t.k1; k0 += kChunk) {
                 const bool got = wait_for(&sh.acc_full[buf], acc_phase, dead, limit, p.status);
                 ok = __all_sync(0xffffffffu, got);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t acc = tmem + buf * kTileN + half * kStatsColumns + ((uint32_t)(quad * 32) << 16);
+                const uint32_t acc = tmem + buf * kTileN + half * kResultColumns + ((uint32_t)(quad * 32) << 16);
 #pragma unroll
-                for (int c = 0; c < kStatsColumns; c += 16) {
+                for (int c = 0; c < kResultColumns; c += 16) {
                     float part[16];
                     tmem_load16(acc + c, part);
 #pragma unroll
@@ -542,70 +591,67 @@ loss_products(const __grid_constant__ ProductParams p) {
                 if (buf == 0) acc_phase ^= 1;
             }
             if (!ok) break;
-            const long long token = (long long)t.m * kTileM + (int)rank * kHalf + quad * 32 + lane;
+            const long long token = (long long)t.m0 + (int)rank * kHalf + quad * 32 + lane;
             const bool mine = token < p.tokens;
             const int part_index = t.n * 2 + half;
-            const long long v0 = (long long)part_index * kStatsColumns;
+            const long long v0 = (long long)part_index * kResultColumns;
             const long long left = p.vocab - v0;  // columns that exist
             if (left <= 0) continue;
             const long long at = mine ? p.target[token] - v0 : -1;
-            if (left < kStatsColumns) {
+            if (left < kResultColumns) {
 #pragma unroll
-                for (int j = 0; j < kStatsColumns; ++j)
+                for (int j = 0; j < kResultColumns; ++j)
                     if (j >= left) z[j] = -INFINITY;
             }
-            if (__any_sync(0xffffffffu, at >= 0 && at < kStatsColumns)) {
+            if (__any_sync(0xffffffffu, at >= 0 && at < kResultColumns)) {
                 float z_y = 0.0f;
 #pragma unroll
-                for (int j = 0; j < kStatsColumns; ++j) z_y = j == at ? z[j] : z_y;
-                if (at >= 0 && at < kStatsColumns) p.picked[token] = z_y;
+                for (int j = 0; j < kResultColumns; ++j) z_y = j == at ? z[j] : z_y;
+                if (at >= 0 && at < kResultColumns) p.picked[token] = z_y;
             }
             float tops[4] = {z[0], z[1], z[2], z[3]}, sums[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int j = 4; j < kStatsColumns; ++j) tops[j & 3] = fmaxf(tops[j & 3], z[j]);
+            for (int j = 4; j < kResultColumns; ++j) tops[j & 3] = fmaxf(tops[j & 3], z[j]);
             const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
             // a row of -inf: any finite base leaves its sum at 0
             const float high = top == -INFINITY ? 0.0f : top;
             const float base = __fmul_rn(high, kLog2e);
 #pragma unroll
-            for (int j = 0; j < kStatsColumns; ++j) sums[j & 3] += exp2_approx(__fmaf_rn(z[j], kLog2e, -base));
+            for (int j = 0; j < kResultColumns; ++j) sums[j & 3] += exp2_approx(__fmaf_rn(z[j], kLog2e, -base));
             // the sum is relative to 2^base, and base to top log2(e) rounded once
             const float miss = __fmaf_rn(high, kLog2e, -base);
             const float sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
             if (mine) p.parts[part_index * p.tokens + token] = make_float2(top, __fmaf_rn(sum, -miss * kLn2, sum));
         }
     } else {  // ------------------------------------------------------ results
-        const int quad = warp & 3;  // the quarter of the lanes this warp may read
-        const uint32_t stage_out = stage0 + kStages * kStageBytes + (warp - 2) * 2 * kStoreBytes;
-        const float factor = p.kind >= kGradHidden ? p.record->factor : 1.0f;
-        int buf = 0, out_buf = 0;
+        const int quad = warp & 3;
+        const int first = (warp - 2 >> 2) * kResultColumns;  // its columns
+        const uint32_t buffer = stage0 + kStages * kStageBytes + (warp - 2) * kStoreBytes;
+        const float factor = p.record->factor;
+        int buf = 0;
         uint32_t acc_phase = 0;
-        auto put = [&](const uint32_t (&w)[32], const CUtensorMap *map, int x, int y, bool add, bool skip) __attribute__((always_inline)) {
-            put_rows(w, stage_out + out_buf * kStoreBytes, lane, map, x, y, add, skip);
-            out_buf ^= 1;
-        };
-        for (long long i = pair; i < n_work; i += pairs) {
-            const Tile t = tile_of(i, m_tiles, n_tiles, k_blocks, p.splits);
-            const int row0 = t.m * kTileM + (int)rank * kHalf + quad * 32;  // this warp's first row of M
+        for (long long j = 0; work.at(j, t); ++j) {
+            const int row0 = t.m0 + (int)rank * kHalf + quad * 32;  // this warp's first row of M
             const bool got = wait_for(&sh.acc_full[buf], acc_phase, dead, limit, p.status);
             if (!__all_sync(0xffffffffu, got)) break;
             tc_fence_after();
             const uint32_t acc = tmem + buf * kTileN + ((uint32_t)(quad * 32) << 16);
-            if (p.kind == kSlopes) {
+            if (t.kind == kLogits) {
                 const int place = row0 + lane;
                 const float lse2 = p.lse2[place], ratio = p.ratio[place];
                 const bool live = p.place_target[place] >= 0;  // not a row that fills the last tile
-                const int y = p.place_target[place] - (int)p.piece0 - t.n * kTileN;
-                const long long left = p.vocab - p.piece0 - (long long)t.n * kTileN;
+                const int y = p.place_target[place] - (int)p.piece0 - t.n0;
+                const long long left = p.vocab - p.piece0 - (long long)t.n0;
                 // q of 32 columns, packed
                 auto q_of = [&](int col, uint32_t *w) __attribute__((always_inline)) {
                     float z[32];
                     tmem_load32(acc + col, z);
 #pragma unroll
                     for (int j = 0; j < 32; ++j) z[j] = exp2_approx(__fmaf_rn(z[j], kLog2e, -lse2));
-                    if (__any_sync(0xffffffffu, y >= col && y < col + 32)) {
+                    const uint32_t hit = y >= col && y < col + 32 ? 1u << (y - col) : 0u;
+                    if (__any_sync(0xffffffffu, hit != 0u)) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) z[j] = j == y - col ? z[j] - 1.0f : z[j];
+                        for (int j = 0; j < 32; ++j) z[j] = hit >> j & 1u ? z[j] - 1.0f : z[j];
                     }
                     const long long keep = live ? left - col : 0;  // columns that exist, in a row that counts
                     if (keep < 32) {
@@ -615,38 +661,38 @@ loss_products(const __grid_constant__ ProductParams p) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) w[j] = pack_lp<BF16>(z[2 * j] * ratio, z[2 * j + 1] * ratio);
                 };
-                for (int c = 0; c < kTileN; c += 64) {
+                for (int c = first; c < first + kResultColumns; c += 64) {
                     uint32_t w[32];
                     q_of(c, w);
                     q_of(c + 32, w + 16);
-                    put(w, &p.q_out, t.n * kTileN + c, row0, false, false);
+                    put_rows(w, buffer, lane, &p.q_out, t.n0 + c, row0, false, false);
                 }
-            } else if (p.kind == kGradHidden) {
+            } else if (t.kind == kGradHidden) {
                 const bool any = t.k1 > t.k0;  // else the accumulator was never written
-                for (int c = 0; c < kTileN; c += 32) {
+                for (int c = first; c < first + kResultColumns; c += 32) {
                     float z[32];
                     tmem_load32(acc + c, z);
                     uint32_t w[32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) w[j] = any ? __float_as_uint(z[j] * factor) : 0u;
-                    put(w, &p.gh_out, t.n * kTileN + c, (int)(t.split * p.rows) + row0, !p.first_piece,
-                        t.n * kTileN + c >= p.dim);
+                    put_rows(w, buffer, lane, &p.gh_out, t.n0 + c, (int)(t.split * p.rows) + row0, !p.first_piece,
+                             t.n0 + c >= p.dim);
                 }
             } else {
-                // no token counts: the accumulator was never written
+                const bool any = t.k1 > t.k0;  // no token counts: the accumulator was never written
                 auto scaled = [&](int col, uint32_t *w) __attribute__((always_inline)) {
                     float z[32];
                     tmem_load32(acc + col, z);
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
-                        w[j] = k_blocks ? pack_lp<BF16>(z[2 * j] * factor, z[2 * j + 1] * factor) : 0u;
+                        w[j] = any ? pack_lp<BF16>(z[2 * j] * factor, z[2 * j + 1] * factor) : 0u;
                 };
-                for (int c = 0; c < kTileN; c += 64) {
+                for (int c = first; c < first + kResultColumns; c += 64) {
                     uint32_t w[32];
                     scaled(c, w);
                     scaled(c + 32, w + 16);
-                    put(w, &p.gw_out, t.n * kTileN + c, (int)p.piece0 + row0, false,
-                        t.n * kTileN + c >= p.dim || p.piece0 + row0 >= p.vocab);
+                    put_rows(w, buffer, lane, &p.gw_out, t.n0 + c, (int)p.piece0 + row0, false,
+                             t.n0 + c >= p.dim || p.piece0 + row0 >= p.vocab);
                 }
             }
             tc_fence_before();
@@ -673,16 +719,16 @@ loss_products(const __grid_constant__ ProductParams p) {
 
 // ---------------------------------------------------------- the smaller kernels
 
-constexpr int kJoinTokens = 32, kJoinWays = 8;
+constexpr int kJoinTokens = 32, kJoinWays = 32;
 
-// lse and loss of 32 tokens: 8 ways along the vocabulary's tiles, joined in order
+// lse and loss of 32 tokens: 32 ways along the vocabulary, joined in order
 __global__ void __launch_bounds__(kJoinTokens *kJoinWays)
 loss_join(const float2 *__restrict__ parts, const float *__restrict__ picked, int tiles, const int64_t *__restrict__ target,
           long long ignore, long long tokens, long long vocab, float *loss, float *lse, int *status) {
     pdl_enter();
-    __shared__ float2 way[kJoinWays][kJoinTokens];
+    __shared__ float2 way[kJoinWays][kJoinTokens + 1];
     const int x = threadIdx.x % kJoinTokens, w = threadIdx.x / kJoinTokens;
-    const long long t = (long long)blockIdx.x * kJoinTokens + x;
+    long long t = (long long)blockIdx.x * kJoinTokens + x;
     auto join = [](float2 a, float2 b) {
         const float top = fmaxf(a.x, b.x);
         const float base = top == -INFINITY ? 0.0f : top;
@@ -690,19 +736,31 @@ loss_join(const float2 *__restrict__ parts, const float *__restrict__ picked, in
     };
     float2 acc = make_float2(-INFINITY, 0.0f);
     if (t < tokens) {
-        int i = w;
-        for (; i + 3 * kJoinWays < tiles; i += 4 * kJoinWays) {
-            float2 v[4];
+        for (int i = w; i < tiles; i += 8 * kJoinWays) {
+            float2 v[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = parts[(long long)(i + j * kJoinWays) * tokens + t];
-            acc = join(acc, join(join(v[0], v[1]), join(v[2], v[3])));
+            for (int j = 0; j < 8; ++j)
+                v[j] = i + j * kJoinWays < tiles ? parts[(long long)(i + j * kJoinWays) * tokens + t] : make_float2(-INFINITY, 0.0f);
+            float top = acc.x;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) top = fmaxf(top, v[j].x);
+            const float base = top == -INFINITY ? 0.0f : top;
+            float sum = acc.y * exp2_approx((acc.x - base) * kLog2e);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum += v[j].y * exp2_approx((v[j].x - base) * kLog2e);
+            acc = make_float2(top, sum);
         }
-        for (; i < tiles; i += kJoinWays) acc = join(acc, parts[(long long)i * tokens + t]);
     }
     way[w][x] = acc;
     __syncthreads();
-    if (w != 0 || t >= tokens) return;
-    for (int i = 1; i < kJoinWays; ++i) acc = join(acc, way[i][x]);
+    // then a warp for each token, a lane for each way
+    const int lane = threadIdx.x & 31;
+    acc = way[lane][w];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        acc = join(acc, make_float2(__shfl_xor_sync(0xffffffffu, acc.x, o), __shfl_xor_sync(0xffffffffu, acc.y, o)));
+    t = (long long)blockIdx.x * kJoinTokens + w;
+    if (lane != 0 || t >= tokens) return;
     const float l = acc.x + log2f(acc.y) * kLn2;
     lse[t] = l;
     const long long y = target[t];
@@ -862,7 +920,7 @@ int pairs_at_once() {
             return 0;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2);
-        cfg.blockDim = dim3(product_threads<STATS>());
+        cfg.blockDim = dim3(kProductThreads);
         cfg.dynamicSmemBytes = kSmemBytes;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -887,7 +945,7 @@ cudaError_t launch_products(const ProductParams &p, int64_t tiles, cudaStream_t 
     const int pairs = pairs_at_once<BF16, STATS>();
     if (pairs < 1) return cudaErrorInvalidConfiguration;
     const int64_t use = std::max<int64_t>(1, std::min<int64_t>(pairs, tiles));
-    return launch_pdl(loss_products<BF16, STATS>, dim3((unsigned)(2 * use)), dim3(product_threads<STATS>()), kSmemBytes, stream, p);
+    return launch_pdl(loss_products<BF16, STATS>, dim3((unsigned)(2 * use)), dim3(kProductThreads), kSmemBytes, stream, p);
 }
 
 template <bool BF16>
@@ -896,13 +954,12 @@ cudaError_t forward_impl(const LossArgs &a, cudaStream_t stream) {
     if (!encoder() || !make_map(&p.h_k, a.hidden, a.tokens, a.dim, a.hidden_stride, a.lp, false, kHalf) ||
         !make_map(&p.w_k, a.weight, a.vocab, a.dim, a.weight_stride, a.lp, false, kHalf))
         return cudaErrorNotSupported;
-    p.kind = kStats;
     p.tokens = a.tokens;
     p.vocab = p.piece = a.vocab;
     p.dim = a.dim;
     p.splits = 1;
     p.target = a.target;
-    const int64_t tiles = up(a.vocab, kTileN) / kTileN, parts = up(a.vocab, kStatsColumns) / kStatsColumns;
+    const int64_t tiles = up(a.vocab, kTileN) / kTileN, parts = up(a.vocab, kResultColumns) / kResultColumns;
     p.parts = static_cast<float2 *>(a.workspace);
     p.picked = reinterpret_cast<float *>(p.parts + parts * a.tokens);
     p.status = a.status;
@@ -942,6 +999,7 @@ cudaError_t backward_impl(const LossArgs &a, cudaStream_t stream) {
     p.dim = a.dim;
     p.piece = l.piece;
     p.rows = l.rows;
+    p.splits = l.splits;
     p.record = record;
     p.lse2 = lse2;
     p.ratio = ratio;
@@ -960,14 +1018,10 @@ cudaError_t backward_impl(const LossArgs &a, cudaStream_t stream) {
     for (int i = 0; i < l.pieces && e == cudaSuccess; ++i) {
         p.piece0 = i * l.piece;
         p.first_piece = i == 0;
-        p.splits = 1;
-        p.kind = kSlopes;
+        p.gradients = 0;
         e = launch_products<BF16, false>(p, row_tiles * piece_tiles, stream);
-        p.kind = kGradWeight;
-        if (e == cudaSuccess) e = launch_products<BF16, false>(p, piece_tiles * dim_tiles, stream);
-        p.kind = kGradHidden;
-        p.splits = l.splits;
-        if (e == cudaSuccess) e = launch_products<BF16, false>(p, row_tiles * dim_tiles * l.splits, stream);
+        p.gradients = 1;
+        if (e == cudaSuccess) e = launch_products<BF16, false>(p, row_tiles * dim_tiles * l.splits + piece_tiles * dim_tiles, stream);
     }
     if (e == cudaSuccess)
         e = launch_pdl(loss_finish<BF16>, dim3((unsigned)copies), dim3(kCopyThreads), 0, stream, reinterpret_cast<const float4 *>(sums),
@@ -980,7 +1034,7 @@ cudaError_t backward_impl(const LossArgs &a, cudaStream_t stream) {
 
 void set_loss_wait(int64_t cycles) { g_wait_cycles.store(cycles); }
 
-int64_t loss_forward_bytes(int64_t tokens, int64_t vocab) { return up(vocab, kStatsColumns) / kStatsColumns * tokens * 8 + up(tokens * 4, 16); }
+int64_t loss_forward_bytes(int64_t tokens, int64_t vocab) { return up(vocab, kResultColumns) / kResultColumns * tokens * 8 + up(tokens * 4, 16); }
 
 cudaError_t launch_loss_forward(const LossArgs &a, cudaStream_t stream) {
     return a.lp ? forward_impl<true>(a, stream) : forward_impl<false>(a, stream);
