@@ -130,7 +130,7 @@ def _ptr_array(xs: Sequence):
 def _stream(s) -> Optional[int]:
     if s is None:
         import torch
-        return int(torch.cuda.current_stream().cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(s, int):
         return s
     return int(s.cuda_stream)

@@ -192,7 +192,7 @@ zero_status zero_loss_set_wait_limit(int64_t cycles) {
 zero_status zero_loss_workspace(int64_t n_tokens, int64_t vocab, int32_t dim, int64_t *forward_bytes,
                                 int64_t *backward_bytes) {
     TRY(loss_shape(n_tokens, vocab, dim, ZERO_BF16));
-    if (forward_bytes) *forward_bytes = zk::loss_forward_bytes(n_tokens, vocab);
+    if (forward_bytes) *forward_bytes = zk::loss_forward_bytes(n_tokens, vocab, dim);
     if (backward_bytes) *backward_bytes = zk::loss_backward_bytes(n_tokens, vocab, dim);
     return ZERO_OK;
 }
@@ -204,7 +204,7 @@ zero_status zero_loss_forward(const void *hidden, int64_t hidden_stride, const v
     TRY(loss_arguments(hidden, hidden_stride, weight, weight_stride, target, n_tokens, vocab, dim, lp, status));
     TRY(vector("loss", loss, n_tokens));
     TRY(vector("lse", lse, n_tokens));
-    TRY(scratch(workspace, workspace_bytes, zk::loss_forward_bytes(n_tokens, vocab)));
+    TRY(scratch(workspace, workspace_bytes, zk::loss_forward_bytes(n_tokens, vocab, dim)));
     if (n_tokens == 0) return ZERO_OK;
     const zk::LossArgs a = {hidden, hidden_stride, weight, weight_stride, target, ignore, n_tokens, vocab, dim, lp,
                             loss, lse, nullptr, nullptr, 0, nullptr, 0, status, workspace};

@@ -39,14 +39,17 @@ constexpr int kOperandBytes = kHalf * kTileK * 2;
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kBoxBytes = 64 * kTileK * 2;  // a 64 x 64 box of an operand whose rows run along K
 constexpr int kStoreBytes = 32 * 128;       // 32 rows of 128 bytes: one warp's store
-constexpr int kResultWarps = 8;              // that take a tile's results: two on each quarter of its rows
-constexpr int kResultColumns = kTileN / 2;   // of one of them
-constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kResultWarps * kStoreBytes;
-constexpr int kProductThreads = 64 + 32 * kResultWarps;
+// Warps that take a tile's results, and the columns of each: a quarter of the
+// warps on each quarter of the rows.  The statistics keep their columns in
+// registers and have the longer way (1023 tokens x 768: 65 us with eight warps
+// for them, STATS16 us with sixteen); the others need room to store from.
+constexpr int kStatsWarps = 16, kStatsColumns = kTileN / (kStatsWarps / 4);
+constexpr int kStoreWarps = 8, kStoreColumns = kTileN / (kStoreWarps / 4);
+constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kStoreWarps * kStoreBytes;
 // The tensor core's float sum drops the low bits of every step of 16, always
 // towards zero: a logit of 15 over 4096 products came out 6e-5 too small, a
 // relative 4e-6 where float addition has 4e-8.  The losses are float, so the
-// statistics take the sum off after kChunk blocks (512 products) and add it up
+// statistics take the sum off after at most kChunk blocks (512 products) and add it up
 // in registers, rounded to nearest; q is rounded to lp anyway and does without.
 constexpr int kChunk = 8;
 constexpr int kTileCost = 4;  // blocks of K that starting and storing a tile cost, about
@@ -125,6 +128,19 @@ __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// the same without waiting for a moment where it is not yet
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
         : "r"(bar), "r"(parity)
@@ -252,6 +268,13 @@ __device__ __forceinline__ uint32_t pack_lp(float a, float b) {
     }
 }
 
+// the joint (maximum, sum of exponentials relative to it) of two parts
+__device__ __forceinline__ float2 join_parts(float2 a, float2 b) {
+    const float top = fmaxf(a.x, b.x);
+    const float base = top == -INFINITY ? 0.0f : top;
+    return make_float2(top, a.y * exp2_approx((a.x - base) * kLog2e) + b.y * exp2_approx((b.x - base) * kLog2e));
+}
+
 // ------------------------------------------------------------------- products
 
 enum Product { kLogits = 0, kGradHidden = 1, kGradWeight = 2 };
@@ -276,7 +299,7 @@ struct ProductParams {
     const LossRecord *record;  // NULL: every token counts
     // statistics
     const int64_t *target;
-    float2 *parts;  // [kResultColumns columns of the vocabulary][token]
+    float2 *parts;  // [tile of the vocabulary][token]
     float *picked;  // the target's logit
     // q, by place among the counted tokens
     const float *lse2, *ratio;
@@ -295,32 +318,60 @@ struct Tile {
     int n;        // its number along the columns
 };
 
+// The statistics' sums: parts of at most kChunk blocks of K, as even as can be (a
+// short last part would have the tensor core wait for its accumulator).
+__device__ __forceinline__ int chunks_of(const Tile &t) { return (t.k1 - t.k0 + kChunk - 1) / kChunk; }
+
+// Division by a number that stays: the product with 2^32 / d rounded up gives the
+// quotient or one more.  (A plain division took the thread that feeds the tensor
+// core long enough to leave it idle at every tile.)
+struct Divisor {
+    uint32_t d, inverse;
+
+    __device__ __forceinline__ void set(uint32_t by) {
+        d = by ? by : 1u;
+        inverse = 0xffffffffu / d + 1u;
+    }
+    __device__ __forceinline__ uint32_t into(uint32_t x) const {
+        const uint32_t q = d == 1u ? x : __umulhi(x, inverse);
+        return q * d > x ? q - 1u : q;
+    }
+};
+
 // A grid of tiles.
 struct Tiles {
     int m, n, columns, k_blocks, splits;
+    Divisor per_split, per_group, last_group;
+    static constexpr int kGroup = 8;
 
-    __device__ __forceinline__ long long size() const { return (long long)m * n * splits; }
+    __device__ __forceinline__ void set(int m_, int n_, int columns_, int k_blocks_, int splits_) {
+        m = m_;
+        n = n_;
+        columns = columns_;
+        k_blocks = k_blocks_;
+        splits = splits_;
+        per_split.set(m * n);
+        per_group.set(kGroup * n);
+        last_group.set(m % kGroup);
+    }
+    __device__ __forceinline__ int size() const { return m * n * splits; }
 
     // Consecutive tiles take 8 tiles of M for one of N before the next of N, so the
     // pairs that run together read few different rows of either operand from L2.
-    __device__ __forceinline__ Tile at(long long i, int kind) const {
+    __device__ __forceinline__ Tile at(uint32_t i, int kind) const {
         Tile t;
         t.kind = kind;
-        const long long per_split = (long long)m * n;
-        t.split = (int)(i / per_split);
-        const long long r = i - t.split * per_split;
-        constexpr int kGroup = 8;
-        const long long per_group = (long long)kGroup * n;
-        const int g = (int)(r / per_group);
-        const int in_group = m - g * kGroup < kGroup ? m - g * kGroup : kGroup;
-        const int q = (int)(r - g * per_group);
-        t.n = q / in_group;
+        t.split = splits == 1 ? 0 : (int)per_split.into(i);
+        const uint32_t r = i - t.split * per_split.d;
+        const uint32_t g = per_group.into(r), q = r - g * per_group.d;
+        const bool whole = (int)(g + 1) * kGroup <= m;
+        t.n = (int)(whole ? q / kGroup : last_group.into(q));
         t.n0 = t.n * kTileN;
-        t.m0 = (g * kGroup + q % in_group) * kTileM;
+        t.m0 = (int)(g * kGroup + (q - t.n * (whole ? kGroup : last_group.d))) * kTileM;
         const int left = (columns - t.n0 + 31) / 32 * 32;
         t.width = left < kTileN ? left : kTileN;
-        t.k0 = (int)((long long)k_blocks * t.split / splits);
-        t.k1 = (int)((long long)k_blocks * (t.split + 1) / splits);
+        t.k0 = splits == 1 ? 0 : k_blocks * t.split / splits;
+        t.k1 = splits == 1 ? k_blocks : k_blocks * (t.split + 1) / splits;
         return t;
     }
 };
@@ -334,45 +385,46 @@ struct Tiles {
 struct Work {
     Tiles logits, hidden, weight;
     int gradients;
-    long long pair, pairs, n_hidden, n_weight;
+    int pair, pairs, n_hidden, n_weight;
     int fuller;  // pairs with one more tile of grad_hidden than the others, if not all have as many
     int catch_up;
+    int mine;      // tiles of grad_hidden of this pair
 
     __device__ __forceinline__ Work(const ProductParams &p, long long count) {
         const long long end = p.piece0 + p.piece < p.vocab ? p.piece0 + p.piece : p.vocab;
         const int columns = (int)(end - p.piece0);
         const int row_tiles = (int)((count + kTileM - 1) / kTileM);
         const int dim_tiles = (p.dim + kTileN - 1) / kTileN, piece_tiles = (columns + kTileN - 1) / kTileN;
-        logits = {row_tiles, piece_tiles, columns, (p.dim + kTileK - 1) / kTileK, 1};
-        hidden = {row_tiles, dim_tiles, p.dim, (columns + kTileK - 1) / kTileK, p.splits};
-        weight = {piece_tiles, dim_tiles, p.dim, (int)((count + kTileK - 1) / kTileK), 1};
+        logits.set(row_tiles, piece_tiles, columns, (p.dim + kTileK - 1) / kTileK, 1);
+        hidden.set(row_tiles, dim_tiles, p.dim, (columns + kTileK - 1) / kTileK, p.splits);
+        weight.set(piece_tiles, dim_tiles, p.dim, (int)((count + kTileK - 1) / kTileK), 1);
         gradients = p.gradients;
         pair = blockIdx.x >> 1;
         pairs = gridDim.x >> 1;
         n_hidden = hidden.size();
         n_weight = weight.size();
-        fuller = (int)(n_hidden % pairs);
+        fuller = n_hidden % pairs;
         const int long_tile = hidden.k_blocks / hidden.splits + kTileCost, short_tile = weight.k_blocks + kTileCost;
         catch_up = fuller ? (long_tile + short_tile / 2) / short_tile : 0;
-        const long long most = fuller ? n_weight / (pairs - fuller) : 0;
-        if (catch_up > most) catch_up = (int)most;
+        const int most = fuller ? n_weight / (pairs - fuller) : 0;
+        if (catch_up > most) catch_up = most;
+        mine = n_hidden > pair ? (n_hidden - pair + pairs - 1) / pairs : 0;
     }
 
-    __device__ __forceinline__ bool at(long long j, Tile &t) const {
+    __device__ __forceinline__ bool at(int j, Tile &t) const {
         if (!gradients) {
-            const long long i = pair + j * pairs;
+            const int i = pair + j * pairs;
             if (i >= logits.size()) return false;
             t = logits.at(i, kLogits);
             return true;
         }
-        const long long mine = n_hidden > pair ? (n_hidden - pair + pairs - 1) / pairs : 0;
         if (j < mine) {
             t = hidden.at(pair + j * pairs, kGradHidden);
             return true;
         }
         j -= mine;
-        const long long others = pairs - fuller;
-        long long i;
+        const int others = pairs - fuller;
+        int i;
         if (catch_up && pair >= fuller && j < catch_up) {
             i = pair - fuller + j * others;
         } else {
@@ -395,7 +447,6 @@ struct Shared {
 // CTA has given up); the CTA then stops and the status says so.
 __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatile int *dead, long long limit, int *status) {
     const uint32_t b = smem_addr(bar);
-    if (*dead) return false;
     if (bar_try(b, parity)) return true;
     const long long t0 = clock64();
     while (!bar_try(b, parity)) {
@@ -434,8 +485,28 @@ __device__ __forceinline__ void put_rows(const uint32_t (&w)[32], uint32_t buffe
     }
 }
 
+// an OR over `threads` threads that meet at barrier `id`
+__device__ __forceinline__ bool any_of(int id, int threads, bool mine) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)mine), "r"(id), "r"(threads)
+        : "memory");
+    return r != 0;
+}
+
+template <bool STATS>
+struct Block {
+    static constexpr int kWarps = STATS ? kStatsWarps : kStoreWarps;
+    static constexpr int kThreads = 64 + 32 * kWarps;
+};
+
 template <bool BF16, bool STATS>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Block<STATS>::kThreads, 1)
 loss_products(const __grid_constant__ ProductParams p) {
     extern __shared__ unsigned char raw[];
     __shared__ Shared sh;
@@ -452,7 +523,7 @@ loss_products(const __grid_constant__ ProductParams p) {
         }
         for (int b = 0; b < 2; ++b) {
             bar_init(smem_addr(&sh.acc_full[b]), 1);
-            bar_init(smem_addr(&sh.acc_empty[b]), 2 * kResultWarps);
+            bar_init(smem_addr(&sh.acc_empty[b]), 2 * Block<STATS>::kWarps);
         }
         bar_init(smem_addr(&sh.drained), 1);
         sh.dead = 0;
@@ -483,7 +554,10 @@ loss_products(const __grid_constant__ ProductParams p) {
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
-            for (long long j = 0; ok && work.at(j, t); ++j) {
+            Tile next;
+            bool more = work.at(0, t);
+            for (int j = 1; ok && more; ++j) {
+                more = false;
                 // this CTA's rows of A, and its half of the columns of B
                 const int m0 = t.m0 + (int)rank * kHalf, n0 = t.n0 + (int)rank * (t.width / 2);
                 const bool two = t.width > kTileN / 2;  // boxes of 64 columns that hold its half
@@ -513,48 +587,71 @@ loss_products(const __grid_constant__ ProductParams p) {
                         stage = 0;
                         phase ^= 1;
                     }
+                    // the divisions of the next tile's place, while loads are on their way
+                    if (k == t.k0) more = work.at(j, next);
                 }
+                if (t.k0 >= t.k1) more = work.at(j, next);
+                t = next;
             }
         }
     } else if (warp == 1) {
         if (rank == 0 && lane == 0) {  // ------------------------- products
             int stage = 0, buf = 0;
             uint32_t phase = 0, acc_phase = 0;
-            bool ok = true;
-            for (long long j = 0; ok && work.at(j, t); ++j) {
+            // The tensor core takes little ahead of what it computes, so this thread asks for
+            // what comes next while a block is under way: whether the next block of K
+            // is there (ready) and whether the next accumulator is free (vacant).
+            bool ok = true, ready = false, vacant = false;
+            Tile after;
+            bool more = work.at(0, t);
+            for (int j = 1; ok && more; ++j) {
+                more = false;
                 const bool a_mn = t.kind == kGradWeight, b_mn = t.kind != kLogits;
                 uint32_t idesc = 1u << 4;  // float sums
                 if (BF16) idesc |= 1u << 7 | 1u << 10;
                 idesc |= (uint32_t)a_mn << 15 | (uint32_t)b_mn << 16;
                 idesc |= (uint32_t)(t.width >> 3) << 17 | (uint32_t)(kTileM >> 4) << 24;
                 // 16 of K further: 32 bytes along a row, or 16 rows
-                const uint64_t a_step = (a_mn ? 16 * 128 : 32) >> 4, b_step = (b_mn ? 16 * 128 : 32) >> 4;
-                for (int k0 = t.k0; k0 < t.k1 || k0 == t.k0; k0 += kChunk) {
-                    const int k1 = STATS && t.k1 > k0 + kChunk ? k0 + kChunk : t.k1;
-                    ok = wait_for(&sh.acc_empty[buf], acc_phase ^ 1, dead, limit, p.status);
+                const uint32_t a_step = (a_mn ? 16 * 128 : 32) >> 4, b_step = (b_mn ? 16 * 128 : 32) >> 4;
+                const uint64_t a0 = operand_desc(stage0, a_mn), b0 = operand_desc(stage0 + kOperandBytes, b_mn);
+                const int chunks = STATS ? chunks_of(t) : 1;
+                const int each = (t.k1 - t.k0) / chunks, longer = (t.k1 - t.k0) % chunks;
+                int k = t.k0;
+                for (int c = 0; c < chunks; ++c) {
+                    const int k1 = k + each + (c < longer);
+                    if (!vacant) ok = wait_for(&sh.acc_empty[buf], acc_phase ^ 1, dead, limit, p.status);
                     if (!ok) break;
-                    tc_fence_after();
-                    for (int k = k0; k < k1; ++k) {
-                        ok = wait_for(&sh.full[stage], phase, dead, limit, p.status);
+                    const uint32_t acc = tmem + buf * kTileN;
+                    const uint32_t next_acc_phase = buf ? acc_phase ^ 1 : acc_phase;
+                    vacant = false;
+                    uint32_t add = 0;
+                    for (; k < k1; ++k) {
+                        if (!ready) ok = wait_for(&sh.full[stage], phase, dead, limit, p.status);
                         if (!ok) break;
                         tc_fence_after();
-                        const uint64_t a = operand_desc(stage0 + stage * kStageBytes, a_mn);
-                        const uint64_t b = operand_desc(stage0 + stage * kStageBytes + kOperandBytes, b_mn);
-#pragma unroll
-                        for (int i = 0; i < kTileK / 16; ++i)
-                            mma_pair(tmem + buf * kTileN, a + i * a_step, b + i * b_step, idesc, k > k0 || i > 0);
+                        const uint64_t a = a0 + (uint32_t)stage * (kStageBytes >> 4), b = b0 + (uint32_t)stage * (kStageBytes >> 4);
+                        mma_pair(acc, a, b, idesc, add);
+                        mma_pair(acc, a + a_step, b + b_step, idesc, 1);
+                        mma_pair(acc, a + 2 * a_step, b + 2 * b_step, idesc, 1);
+                        mma_pair(acc, a + 3 * a_step, b + 3 * b_step, idesc, 1);
                         mma_commit(smem_addr(&sh.empty[stage]));
+                        add = 1;
                         if (++stage == kStages) {
                             stage = 0;
                             phase ^= 1;
                         }
+                        ready = bar_test(smem_addr(&sh.full[stage]), phase);
+                        if (k + 1 == k1) vacant = bar_test(smem_addr(&sh.acc_empty[buf ^ 1]), next_acc_phase ^ 1);
+                        // the divisions of the next tile's place
+                        if (k == t.k0) more = work.at(j, after);
                     }
                     if (!ok) break;
                     mma_commit(smem_addr(&sh.acc_full[buf]));
                     buf ^= 1;
-                    if (buf == 0) acc_phase ^= 1;
-                    if (!STATS) break;
+                    acc_phase = next_acc_phase;
                 }
+                if (t.k0 >= t.k1) more = work.at(j, after);
+                t = after;
             }
             if (!ok) {  // the products already issued still read shared memory
                 mma_commit(smem_addr(&sh.drained));
@@ -563,26 +660,33 @@ loss_products(const __grid_constant__ ProductParams p) {
         }
     } else if constexpr (STATS) {  // ------------------------------- statistics
         const int quad = warp & 3;  // the quarter of the lanes this warp may read
-        const int half = (warp - 2) >> 2;  // which half of the columns it takes
+        const int group = (warp - 2) >> 2;  // which of the tile's columns it takes
+        float2(*const joined)[kStatsWarps / 4][kHalf] = reinterpret_cast<float2(*)[kStatsWarps / 4][kHalf]>(smem + kStages * kStageBytes);
         int buf = 0;
         uint32_t acc_phase = 0;
-        bool ok = true;
-        for (long long j = 0; ok && work.at(j, t); ++j) {
-            float z[kResultColumns];
+        for (int j = 0; work.at(j, t); ++j) {
+            const int row = quad * 32 + lane;
+            const long long token = (long long)t.m0 + (int)rank * kHalf + row;
+            const bool mine = token < p.tokens;
+            const long long v0 = (long long)t.n0 + group * kStatsColumns;
+            const long long left = p.vocab - v0;  // columns that exist
+            const long long at = mine ? p.target[token] - v0 : -1;
+            float z[kStatsColumns];
 #pragma unroll
-            for (int j = 0; j < kResultColumns; ++j) z[j] = 0.0f;
-            for (int k0 = t.k0; k0 < t.k1; k0 += kChunk) {
+            for (int i = 0; i < kStatsColumns; ++i) z[i] = 0.0f;
+            bool ok = true;
+            for (int c = chunks_of(t); c > 0; --c) {
                 const bool got = wait_for(&sh.acc_full[buf], acc_phase, dead, limit, p.status);
                 ok = __all_sync(0xffffffffu, got);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t acc = tmem + buf * kTileN + half * kResultColumns + ((uint32_t)(quad * 32) << 16);
+                const uint32_t acc = tmem + buf * kTileN + group * kStatsColumns + ((uint32_t)(quad * 32) << 16);
 #pragma unroll
-                for (int c = 0; c < kResultColumns; c += 16) {
+                for (int i = 0; i < kStatsColumns; i += 16) {
                     float part[16];
-                    tmem_load16(acc + c, part);
+                    tmem_load16(acc + i, part);
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) z[c + j] = __fadd_rn(z[c + j], part[j]);
+                    for (int k = 0; k < 16; ++k) z[i + k] = __fadd_rn(z[i + k], part[k]);
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -590,47 +694,50 @@ loss_products(const __grid_constant__ ProductParams p) {
                 buf ^= 1;
                 if (buf == 0) acc_phase ^= 1;
             }
-            if (!ok) break;
-            const long long token = (long long)t.m0 + (int)rank * kHalf + quad * 32 + lane;
-            const bool mine = token < p.tokens;
-            const int part_index = t.n * 2 + half;
-            const long long v0 = (long long)part_index * kResultColumns;
-            const long long left = p.vocab - v0;  // columns that exist
-            if (left <= 0) continue;
-            const long long at = mine ? p.target[token] - v0 : -1;
-            if (left < kResultColumns) {
+            float2 part = make_float2(-INFINITY, 0.0f);
+            if (ok && left > 0) {
+                if (left < kStatsColumns) {
 #pragma unroll
-                for (int j = 0; j < kResultColumns; ++j)
-                    if (j >= left) z[j] = -INFINITY;
+                    for (int i = 0; i < kStatsColumns; ++i)
+                        if (i >= left) z[i] = -INFINITY;
+                }
+                if (__any_sync(0xffffffffu, at >= 0 && at < kStatsColumns)) {
+                    float z_y = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < kStatsColumns; ++i) z_y = i == at ? z[i] : z_y;
+                    if (at >= 0 && at < kStatsColumns) p.picked[token] = z_y;
+                }
+                float tops[4] = {z[0], z[1], z[2], z[3]}, sums[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int i = 4; i < kStatsColumns; ++i) tops[i & 3] = fmaxf(tops[i & 3], z[i]);
+                const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+                // a row of -inf: any finite base leaves its sum at 0
+                const float high = top == -INFINITY ? 0.0f : top;
+                const float base = __fmul_rn(high, kLog2e);
+#pragma unroll
+                for (int i = 0; i < kStatsColumns; ++i) sums[i & 3] += exp2_approx(__fmaf_rn(z[i], kLog2e, -base));
+                // the sum is relative to 2^base, and base to top log2(e) rounded once
+                const float miss = __fmaf_rn(high, kLog2e, -base);
+                const float sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
+                part = make_float2(top, __fmaf_rn(sum, -miss * kLn2, sum));
             }
-            if (__any_sync(0xffffffffu, at >= 0 && at < kResultColumns)) {
-                float z_y = 0.0f;
+            // the warps of a row join their parts; if one gave up, all stop
+            joined[j & 1][group][row] = part;
+            if (any_of(1 + quad, 32 * (kStatsWarps / 4), !ok)) break;
+            if (group == 0 && mine) {
 #pragma unroll
-                for (int j = 0; j < kResultColumns; ++j) z_y = j == at ? z[j] : z_y;
-                if (at >= 0 && at < kResultColumns) p.picked[token] = z_y;
+                for (int g = 1; g < kStatsWarps / 4; ++g) part = join_parts(part, joined[j & 1][g][row]);
+                p.parts[t.n * p.tokens + token] = part;
             }
-            float tops[4] = {z[0], z[1], z[2], z[3]}, sums[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-            for (int j = 4; j < kResultColumns; ++j) tops[j & 3] = fmaxf(tops[j & 3], z[j]);
-            const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-            // a row of -inf: any finite base leaves its sum at 0
-            const float high = top == -INFINITY ? 0.0f : top;
-            const float base = __fmul_rn(high, kLog2e);
-#pragma unroll
-            for (int j = 0; j < kResultColumns; ++j) sums[j & 3] += exp2_approx(__fmaf_rn(z[j], kLog2e, -base));
-            // the sum is relative to 2^base, and base to top log2(e) rounded once
-            const float miss = __fmaf_rn(high, kLog2e, -base);
-            const float sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
-            if (mine) p.parts[part_index * p.tokens + token] = make_float2(top, __fmaf_rn(sum, -miss * kLn2, sum));
         }
     } else {  // ------------------------------------------------------ results
         const int quad = warp & 3;
-        const int first = (warp - 2 >> 2) * kResultColumns;  // its columns
+        const int first = ((warp - 2) >> 2) * kStoreColumns;  // its columns
         const uint32_t buffer = stage0 + kStages * kStageBytes + (warp - 2) * kStoreBytes;
         const float factor = p.record->factor;
         int buf = 0;
         uint32_t acc_phase = 0;
-        for (long long j = 0; work.at(j, t); ++j) {
+        for (int j = 0; work.at(j, t); ++j) {
             const int row0 = t.m0 + (int)rank * kHalf + quad * 32;  // this warp's first row of M
             const bool got = wait_for(&sh.acc_full[buf], acc_phase, dead, limit, p.status);
             if (!__all_sync(0xffffffffu, got)) break;
@@ -661,7 +768,7 @@ loss_products(const __grid_constant__ ProductParams p) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) w[j] = pack_lp<BF16>(z[2 * j] * ratio, z[2 * j + 1] * ratio);
                 };
-                for (int c = first; c < first + kResultColumns; c += 64) {
+                for (int c = first; c < first + kStoreColumns; c += 64) {
                     uint32_t w[32];
                     q_of(c, w);
                     q_of(c + 32, w + 16);
@@ -669,7 +776,7 @@ loss_products(const __grid_constant__ ProductParams p) {
                 }
             } else if (t.kind == kGradHidden) {
                 const bool any = t.k1 > t.k0;  // else the accumulator was never written
-                for (int c = first; c < first + kResultColumns; c += 32) {
+                for (int c = first; c < first + kStoreColumns; c += 32) {
                     float z[32];
                     tmem_load32(acc + c, z);
                     uint32_t w[32];
@@ -687,7 +794,7 @@ loss_products(const __grid_constant__ ProductParams p) {
                     for (int j = 0; j < 16; ++j)
                         w[j] = any ? pack_lp<BF16>(z[2 * j] * factor, z[2 * j + 1] * factor) : 0u;
                 };
-                for (int c = first; c < first + kResultColumns; c += 64) {
+                for (int c = first; c < first + kStoreColumns; c += 64) {
                     uint32_t w[32];
                     scaled(c, w);
                     scaled(c + 32, w + 16);
@@ -729,11 +836,6 @@ loss_join(const float2 *__restrict__ parts, const float *__restrict__ picked, in
     __shared__ float2 way[kJoinWays][kJoinTokens + 1];
     const int x = threadIdx.x % kJoinTokens, w = threadIdx.x / kJoinTokens;
     long long t = (long long)blockIdx.x * kJoinTokens + x;
-    auto join = [](float2 a, float2 b) {
-        const float top = fmaxf(a.x, b.x);
-        const float base = top == -INFINITY ? 0.0f : top;
-        return make_float2(top, a.y * exp2_approx((a.x - base) * kLog2e) + b.y * exp2_approx((b.x - base) * kLog2e));
-    };
     float2 acc = make_float2(-INFINITY, 0.0f);
     if (t < tokens) {
         for (int i = w; i < tiles; i += 8 * kJoinWays) {
@@ -758,7 +860,7 @@ loss_join(const float2 *__restrict__ parts, const float *__restrict__ picked, in
     acc = way[lane][w];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
-        acc = join(acc, make_float2(__shfl_xor_sync(0xffffffffu, acc.x, o), __shfl_xor_sync(0xffffffffu, acc.y, o)));
+        acc = join_parts(acc, make_float2(__shfl_xor_sync(0xffffffffu, acc.x, o), __shfl_xor_sync(0xffffffffu, acc.y, o)));
     t = (long long)blockIdx.x * kJoinTokens + w;
     if (lane != 0 || t >= tokens) return;
     const float l = acc.x + log2f(acc.y) * kLn2;
@@ -771,6 +873,121 @@ loss_join(const float2 *__restrict__ parts, const float *__restrict__ picked, in
         atomicOr(status, ZERO_LOSS_BAD_TARGET);
     } else {
         loss[t] = l - picked[t];
+    }
+}
+
+// Statistics of a few tokens, without the tensor cores: a tile of theirs has 256
+// tokens, and what takes the time is the matrix, read once.  The hidden states
+// lie in shared memory as floats; a warp takes four or eight rows of the matrix
+// at a time, its lanes the same vectors of each, and the sums of all rows and tokens
+// are exchanged together: with N sums each step hands half of them over, so N - 1
+// exchanges and not 5 N, and leaves every lane one sum to keep statistics of.
+// One token, 768 x 50257 in fp16, the matrix in L2: 10.5 us, 24 us in a tile; four
+// tokens 16 and 24 us; eight would be no faster than in a tile.
+constexpr int kFewTokens = 4;
+constexpr int kFewThreads = 256;
+constexpr int kFewBlocks = 304;              // two on each SM
+constexpr int kFewSmem = 96 * 1024;          // floats of the hidden states, at most
+
+template <bool BF16>
+__device__ __forceinline__ void widen8(uint4 q, float f[8]) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if constexpr (BF16) {
+            f[2 * k] = __uint_as_float(w[k] << 16);
+            f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+        } else {
+            const float2 t = __half22float2(*reinterpret_cast<const __half2 *>(&w[k]));
+            f[2 * k] = t.x;
+            f[2 * k + 1] = t.y;
+        }
+    }
+}
+
+template <bool BF16, int T>
+__global__ void __launch_bounds__(kFewThreads, 2)
+loss_few(const uint4 *__restrict__ hidden, long long hidden_stride, const uint4 *__restrict__ weight, long long weight_stride,
+         const int64_t *__restrict__ target, int tokens, long long vocab, int vecs, float2 *parts, float *picked) {
+    pdl_enter();
+    constexpr int R = T == 1 ? 8 : 4, N = R * T;  // rows at a time, sums
+    extern __shared__ float4 h[];  // [token][half of a vector][vector]
+    __shared__ float2 warp_part[kFewThreads / 32][T];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int i = threadIdx.x; i < T * vecs; i += kFewThreads) {
+        const int t = i / vecs, v = i - t * vecs;
+        float f[8] = {};
+        if (t < tokens) widen8<BF16>(hidden[t * hidden_stride + v], f);
+        h[2 * t * vecs + v] = make_float4(f[0], f[1], f[2], f[3]);
+        h[(2 * t + 1) * vecs + v] = make_float4(f[4], f[5], f[6], f[7]);
+    }
+    __syncthreads();
+    constexpr int kBits = N == 8 ? 3 : 4;
+    const int mine = lane >> (5 - kBits);  // the sum this lane keeps: row mine / T, token mine % T
+    const int token = mine % T;
+    const long long y = token < tokens ? target[token] : -1;
+    float2 stat = make_float2(-INFINITY, 0.0f);
+    const long long groups = (vocab + R - 1) / R;
+    for (long long g = (long long)blockIdx.x * (kFewThreads / 32) + warp; g < groups;
+         g += (long long)gridDim.x * (kFewThreads / 32)) {
+        float acc[N];
+#pragma unroll
+        for (int n = 0; n < N; ++n) acc[n] = 0.0f;
+        const uint4 *row[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) row[r] = weight + (g * R + r < vocab ? g * R + r : vocab - 1) * weight_stride;
+        for (int v = lane; v < vecs; v += 32) {
+            uint4 q[R];
+#pragma unroll
+            for (int r = 0; r < R; ++r) q[r] = __ldg(row[r] + v);
+#pragma unroll
+            for (int t = 0; t < T; ++t) {
+                const float4 a = h[2 * t * vecs + v], b = h[(2 * t + 1) * vecs + v];
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    float w[8];
+                    widen8<BF16>(q[r], w);
+                    float &s = acc[r * T + t];
+                    s = __fmaf_rn(w[0], a.x, s);
+                    s = __fmaf_rn(w[1], a.y, s);
+                    s = __fmaf_rn(w[2], a.z, s);
+                    s = __fmaf_rn(w[3], a.w, s);
+                    s = __fmaf_rn(w[4], b.x, s);
+                    s = __fmaf_rn(w[5], b.y, s);
+                    s = __fmaf_rn(w[6], b.z, s);
+                    s = __fmaf_rn(w[7], b.w, s);
+                }
+            }
+        }
+        int off = 16;
+#pragma unroll
+        for (int half = N / 2; half >= 1; half /= 2, off >>= 1) {
+            const bool upper = lane & off;
+#pragma unroll
+            for (int n = 0; n < half; ++n) {
+                const float give = upper ? acc[n] : acc[n + half], keep = upper ? acc[n + half] : acc[n];
+                acc[n] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+            }
+        }
+#pragma unroll
+        for (; off >= 1; off >>= 1) acc[0] += __shfl_xor_sync(0xffffffffu, acc[0], off);
+        const long long v = g * R + mine / T;
+        if (v < vocab) {
+            if (v == y) picked[token] = acc[0];
+            stat = join_parts(stat, make_float2(acc[0], 1.0f));
+        }
+    }
+    // lanes that keep the same sum hold the same statistics; rows join, then warps
+    for (int off = 32 / R; off < 32; off <<= 1) {
+        const float2 other = make_float2(__shfl_xor_sync(0xffffffffu, stat.x, off), __shfl_xor_sync(0xffffffffu, stat.y, off));
+        stat = join_parts(stat, other);
+    }
+    if (lane < 32 / R && (lane & ((1 << (5 - kBits)) - 1)) == 0) warp_part[warp][token] = stat;
+    __syncthreads();
+    if (threadIdx.x < tokens) {
+        stat = warp_part[0][threadIdx.x];
+        for (int w = 1; w < kFewThreads / 32; ++w) stat = join_parts(stat, warp_part[w][threadIdx.x]);
+        parts[(long long)blockIdx.x * tokens + threadIdx.x] = stat;
     }
 }
 
@@ -920,7 +1137,7 @@ int pairs_at_once() {
             return 0;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2);
-        cfg.blockDim = dim3(kProductThreads);
+        cfg.blockDim = dim3(Block<STATS>::kThreads);
         cfg.dynamicSmemBytes = kSmemBytes;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -944,30 +1161,62 @@ template <bool BF16, bool STATS>
 cudaError_t launch_products(const ProductParams &p, int64_t tiles, cudaStream_t stream) {
     const int pairs = pairs_at_once<BF16, STATS>();
     if (pairs < 1) return cudaErrorInvalidConfiguration;
+    if (tiles > 0x3fffffff) return cudaErrorInvalidValue;
     const int64_t use = std::max<int64_t>(1, std::min<int64_t>(pairs, tiles));
-    return launch_pdl(loss_products<BF16, STATS>, dim3((unsigned)(2 * use)), dim3(kProductThreads), kSmemBytes, stream, p);
+    return launch_pdl(loss_products<BF16, STATS>, dim3((unsigned)(2 * use)), dim3(Block<STATS>::kThreads), kSmemBytes, stream, p);
+}
+
+// whether the few tokens' hidden states fit into shared memory twice on an SM
+bool few(int64_t tokens, int dim) {
+    const int64_t t = tokens <= 2 ? tokens : 4;
+    return tokens <= kFewTokens && t * dim * 4 <= kFewSmem;
+}
+
+template <bool BF16, int T>
+cudaError_t launch_few(const LossArgs &a, float2 *parts, float *picked, cudaStream_t stream) {
+    static const cudaError_t attr =
+        cudaFuncSetAttribute(loss_few<BF16, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem);
+    if (attr != cudaSuccess) return attr;
+    return launch_pdl(loss_few<BF16, T>, dim3(kFewBlocks), dim3(kFewThreads), size_t(T) * a.dim * 4, stream,
+                      static_cast<const uint4 *>(a.hidden), (long long)(a.hidden_stride / 8),
+                      static_cast<const uint4 *>(a.weight), (long long)(a.weight_stride / 8), a.target, (int)a.tokens,
+                      (long long)a.vocab, a.dim / 8, parts, picked);
+}
+
+// parts of the vocabulary that the statistics come in
+int64_t parts_of(int64_t tokens, int64_t vocab, int dim) {
+    return few(tokens, dim) ? kFewBlocks : up(vocab, kTileN) / kTileN;
 }
 
 template <bool BF16>
 cudaError_t forward_impl(const LossArgs &a, cudaStream_t stream) {
-    ProductParams p = {};
-    if (!encoder() || !make_map(&p.h_k, a.hidden, a.tokens, a.dim, a.hidden_stride, a.lp, false, kHalf) ||
-        !make_map(&p.w_k, a.weight, a.vocab, a.dim, a.weight_stride, a.lp, false, kHalf))
-        return cudaErrorNotSupported;
-    p.tokens = a.tokens;
-    p.vocab = p.piece = a.vocab;
-    p.dim = a.dim;
-    p.splits = 1;
-    p.target = a.target;
-    const int64_t tiles = up(a.vocab, kTileN) / kTileN, parts = up(a.vocab, kResultColumns) / kResultColumns;
-    p.parts = static_cast<float2 *>(a.workspace);
-    p.picked = reinterpret_cast<float *>(p.parts + parts * a.tokens);
-    p.status = a.status;
-    p.wait_cycles = g_wait_cycles.load();
-    cudaError_t e = launch_products<BF16, true>(p, up(a.tokens, kTileM) / kTileM * tiles, stream);
+    const int64_t n = parts_of(a.tokens, a.vocab, a.dim);
+    float2 *parts = static_cast<float2 *>(a.workspace);
+    float *picked = reinterpret_cast<float *>(parts + n * a.tokens);
+    cudaError_t e;
+    if (few(a.tokens, a.dim)) {
+        e = a.tokens == 1   ? launch_few<BF16, 1>(a, parts, picked, stream)
+            : a.tokens == 2 ? launch_few<BF16, 2>(a, parts, picked, stream)
+                            : launch_few<BF16, 4>(a, parts, picked, stream);
+    } else {
+        ProductParams p = {};
+        if (!encoder() || !make_map(&p.h_k, a.hidden, a.tokens, a.dim, a.hidden_stride, a.lp, false, kHalf) ||
+            !make_map(&p.w_k, a.weight, a.vocab, a.dim, a.weight_stride, a.lp, false, kHalf))
+            return cudaErrorNotSupported;
+        p.tokens = a.tokens;
+        p.vocab = p.piece = a.vocab;
+        p.dim = a.dim;
+        p.splits = 1;
+        p.target = a.target;
+        p.parts = parts;
+        p.picked = picked;
+        p.status = a.status;
+        p.wait_cycles = g_wait_cycles.load();
+        e = launch_products<BF16, true>(p, up(a.tokens, kTileM) / kTileM * (up(a.vocab, kTileN) / kTileN), stream);
+    }
     if (e != cudaSuccess) return e;
     return launch_pdl(loss_join, dim3((unsigned)((a.tokens + kJoinTokens - 1) / kJoinTokens)),
-                      dim3(kJoinTokens * kJoinWays), 0, stream, (const float2 *)p.parts, (const float *)p.picked, (int)parts,
+                      dim3(kJoinTokens * kJoinWays), 0, stream, (const float2 *)parts, (const float *)picked, (int)n,
                       a.target, (long long)a.ignore, (long long)a.tokens, (long long)a.vocab, a.loss, a.lse, a.status);
 }
 
@@ -1034,7 +1283,9 @@ cudaError_t backward_impl(const LossArgs &a, cudaStream_t stream) {
 
 void set_loss_wait(int64_t cycles) { g_wait_cycles.store(cycles); }
 
-int64_t loss_forward_bytes(int64_t tokens, int64_t vocab) { return up(vocab, kResultColumns) / kResultColumns * tokens * 8 + up(tokens * 4, 16); }
+int64_t loss_forward_bytes(int64_t tokens, int64_t vocab, int dim) {
+    return parts_of(tokens, vocab, dim) * tokens * 8 + up(tokens * 4, 16);
+}
 
 cudaError_t launch_loss_forward(const LossArgs &a, cudaStream_t stream) {
     return a.lp ? forward_impl<true>(a, stream) : forward_impl<false>(a, stream);

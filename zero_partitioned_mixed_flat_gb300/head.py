@@ -12,7 +12,12 @@ that stream, so a caller on several streams orders its own tensors between
 them and nothing else.  Wrong shapes, types or devices raise ZeroError
 (ZERO_EINVAL) before any device work.
 """
-import numpy as np
+import contextlib
+from array import array
+from ctypes import byref, c_int64 as _i64
+from itertools import accumulate
+from operator import attrgetter
+
 import torch
 
 from . import _abi as A
@@ -20,48 +25,53 @@ from . import _abi as A
 _LP = {torch.float16: A.ZERO_FP16, torch.bfloat16: A.ZERO_BF16}
 _CLIP = {**_LP, torch.float32: A.ZERO_FP32}
 _STATUS = {}   # device index -> the int32 that every loss call of the process ORs into
+_HERE = contextlib.nullcontext()
 
 
 def _refuse(where, why):
     raise A.ZeroError(A.ZERO_EINVAL, where, why)
 
 
-class _On:
-    """Allocations inside belong to `stream` (None: the current stream)."""
-
-    def __init__(self, stream):
-        if stream is not None and not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
-        self.ctx = None if stream is None else torch.cuda.stream(stream)
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+def _call(name, *args):
+    """One libzero call; args are numbers and addresses."""
+    code = getattr(A.load(), name)(*args)
+    if code:
+        A._check(code, name)
 
 
-def _matrix(where, name, t, like=None, shape=None):
-    """(rows, columns, row stride) of a 2-D tensor with contiguous rows."""
-    if t.dim() != 2 or t.dtype not in _LP or not t.is_cuda:
-        _refuse(where, "%s must be a 2-D float16 or bfloat16 CUDA tensor" % name)
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
-        _refuse(where, "%s differs in type or device" % name)
+def _on(stream):
+    """A context whose allocations belong to `stream` (None: the current stream)."""
+    if stream is None:
+        return _HERE
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _matrix(where, name, t, dtype=None, shape=None):
+    """(rows, columns, row stride) of a 2-D tensor with contiguous rows on the current device."""
+    if t.ndim != 2 or t.dtype not in _LP or t.get_device() != torch._C._cuda_getDevice():
+        _refuse(where, "%s must be a 2-D float16 or bfloat16 tensor on the current CUDA device" % name)
+    if dtype is not None and t.dtype != dtype:
+        _refuse(where, "%s is %s, expected %s" % (name, t.dtype, dtype))
     rows, cols = t.shape
     if shape is not None and (rows, cols) != shape:
         _refuse(where, "%s is %d x %d, expected %d x %d" % (name, rows, cols, *shape))
     s0, s1 = t.stride()
-    if cols > 1 and s1 != 1:
+    if s1 != 1 and cols > 1:
         _refuse(where, "%s: the elements of a row must be contiguous" % name)
     # the stride of a single row (or of none) says nothing
     return rows, cols, s0 if rows > 1 else -(-cols // 8) * 8
 
 
-def _vector(where, name, t, n, dtype, device):
-    if t.dim() != 1 or t.shape[0] != n or t.dtype != dtype or t.device != device or (n > 1 and t.stride(0) != 1):
-        _refuse(where, "%s must be a contiguous vector of %d %s on %s" % (name, n, dtype, device))
+def _vector(where, name, t, n, dtype):
+    if (t.ndim != 1 or t.dtype != dtype or t.get_device() != torch._C._cuda_getDevice() or t.shape[0] != n
+            or (n > 1 and t.stride(0) != 1)):
+        _refuse(where, "%s must be a contiguous vector of %d %s on the current CUDA device" % (name, n, dtype))
 
 
 def _status(device):
@@ -92,8 +102,8 @@ def check_losses(device=None):
 
 def _norm_inputs(where, x, residual, weight):
     rows, dim, xs = _matrix(where, "x", x)
-    rs = 0 if residual is None else _matrix(where, "residual", residual, x, (rows, dim))[2]
-    _vector(where, "weight", weight, dim, x.dtype, x.device)
+    rs = 0 if residual is None else _matrix(where, "residual", residual, x.dtype, (rows, dim))[2]
+    _vector(where, "weight", weight, dim, x.dtype)
     return rows, dim, xs, rs
 
 
@@ -101,11 +111,11 @@ def residual_norm(x, residual, weight, eps, stream=None):
     """(out, sum): sum = x + residual (residual None: x), out = sum * rstd * weight
     with rstd = (mean(sum^2) + eps)^(-1/2) over each row."""
     rows, dim, xs, rs = _norm_inputs("residual_norm", x, residual, weight)
-    with _On(stream):
-        out = torch.empty((rows, dim), dtype=x.dtype, device=x.device)
-        total = torch.empty((rows, dim), dtype=x.dtype, device=x.device)
-        A.zero_norm_forward(x, xs, residual, rs, weight, eps, rows, dim, _LP[x.dtype], out, dim, total, dim,
-                            stream)
+    with _on(stream):
+        out = x.new_empty((rows, dim))
+        total = x.new_empty((rows, dim))
+        _call("zero_norm_forward", x.data_ptr(), xs, _addr(residual), rs, weight.data_ptr(), eps, rows, dim,
+              _LP[x.dtype], out.data_ptr(), dim, total.data_ptr(), dim, A._stream(stream))
     return out, total
 
 
@@ -113,27 +123,29 @@ def residual_norm_quantized(x, residual, weight, eps, fmt=A.ZERO_QUANT_INT8, str
     """(codes, scales, sum): residual_norm's out as int8 or E4M3 codes (one byte
     each, int8 tensor) with a float scale per block of 128 elements of a row."""
     rows, dim, xs, rs = _norm_inputs("residual_norm_quantized", x, residual, weight)
-    with _On(stream):
-        codes = torch.empty((rows, dim), dtype=torch.int8, device=x.device)
-        scales = torch.empty((rows, -(-dim // A.ZERO_QUANT_BLOCK)), dtype=torch.float32, device=x.device)
-        total = torch.empty((rows, dim), dtype=x.dtype, device=x.device)
-        A.zero_norm_forward_quantized(x, xs, residual, rs, weight, eps, rows, dim, _LP[x.dtype], fmt, codes,
-                                      scales, total, dim, stream)
+    with _on(stream):
+        codes = x.new_empty((rows, dim), dtype=torch.int8)
+        scales = x.new_empty((rows, -(-dim // A.ZERO_QUANT_BLOCK)), dtype=torch.float32)
+        total = x.new_empty((rows, dim))
+        _call("zero_norm_forward_quantized", x.data_ptr(), xs, _addr(residual), rs, weight.data_ptr(), eps, rows,
+              dim, _LP[x.dtype], fmt, codes.data_ptr(), scales.data_ptr(), total.data_ptr(), dim, A._stream(stream))
     return codes, scales, total
 
 
 def dequantize_rows(codes, scales, fmt, dtype, stream=None):
     """code * scale of its block, in `dtype`, for residual_norm_quantized's outputs."""
     where = "dequantize_rows"
-    if codes.dim() != 2 or codes.dtype != torch.int8 or not codes.is_cuda or not codes.is_contiguous():
-        _refuse(where, "codes must be a contiguous 2-D int8 CUDA tensor")
+    device = torch._C._cuda_getDevice()
+    if codes.ndim != 2 or codes.dtype != torch.int8 or codes.get_device() != device or not codes.is_contiguous():
+        _refuse(where, "codes must be a contiguous 2-D int8 tensor on the current CUDA device")
     rows, dim = codes.shape
-    if (dtype not in _LP or scales.dtype != torch.float32 or scales.device != codes.device
+    if (dtype not in _LP or scales.dtype != torch.float32 or scales.get_device() != device
             or scales.shape != (rows, -(-dim // A.ZERO_QUANT_BLOCK)) or not scales.is_contiguous()):
         _refuse(where, "scales must be one float32 per block of a row, dtype float16 or bfloat16")
-    with _On(stream):
-        out = torch.empty((rows, dim), dtype=dtype, device=codes.device)
-        A.zero_dequantize_rows(codes, scales, fmt, rows, dim, _LP[dtype], out, dim, stream)
+    with _on(stream):
+        out = codes.new_empty((rows, dim), dtype=dtype)
+        _call("zero_dequantize_rows", codes.data_ptr(), scales.data_ptr(), fmt, rows, dim, _LP[dtype],
+              out.data_ptr(), dim, A._stream(stream))
     return out
 
 
@@ -143,16 +155,17 @@ def residual_norm_backward(total, weight, grad_out, grad_sum, eps, stream=None):
     other uses.  grad_in is the gradient of x and of residual alike."""
     where = "residual_norm_backward"
     rows, dim, ts = _matrix(where, "total", total)
-    _vector(where, "weight", weight, dim, total.dtype, total.device)
-    gs = _matrix(where, "grad_out", grad_out, total, (rows, dim))[2]
-    ss = 0 if grad_sum is None else _matrix(where, "grad_sum", grad_sum, total, (rows, dim))[2]
-    with _On(stream):
-        grad_in = torch.empty((rows, dim), dtype=total.dtype, device=total.device)
-        grad_weight = torch.empty(dim, dtype=total.dtype, device=total.device)
+    _vector(where, "weight", weight, dim, total.dtype)
+    gs = _matrix(where, "grad_out", grad_out, total.dtype, (rows, dim))[2]
+    ss = 0 if grad_sum is None else _matrix(where, "grad_sum", grad_sum, total.dtype, (rows, dim))[2]
+    with _on(stream):
+        grad_in = total.new_empty((rows, dim))
+        grad_weight = total.new_empty(dim)
         need = A.zero_norm_backward_workspace(rows, dim)
-        space = torch.empty(need, dtype=torch.uint8, device=total.device)
-        A.zero_norm_backward(total, ts, weight, grad_out, gs, grad_sum, ss, eps, rows, dim, _LP[total.dtype],
-                             grad_in, dim, grad_weight, space, need, stream)
+        space = total.new_empty(need, dtype=torch.uint8)
+        _call("zero_norm_backward", total.data_ptr(), ts, weight.data_ptr(), grad_out.data_ptr(), gs, _addr(grad_sum),
+              ss, eps, rows, dim, _LP[total.dtype], grad_in.data_ptr(), dim, grad_weight.data_ptr(),
+              space.data_ptr(), need, A._stream(stream))
     return grad_in, grad_weight
 
 
@@ -160,10 +173,10 @@ def residual_norm_backward(total, weight, grad_out, grad_sum, eps, stream=None):
 
 def _loss_inputs(where, hidden, weight, targets):
     tokens, dim, hs = _matrix(where, "hidden", hidden)
-    vocab, _, ws = _matrix(where, "weight", weight, hidden)
-    if weight.shape[1] != dim:
-        _refuse(where, "weight has rows of %d, hidden of %d" % (weight.shape[1], dim))
-    _vector(where, "targets", targets, tokens, torch.int64, hidden.device)
+    vocab, wide, ws = _matrix(where, "weight", weight, hidden.dtype)
+    if wide != dim:
+        _refuse(where, "weight has rows of %d, hidden of %d" % (wide, dim))
+    _vector(where, "targets", targets, tokens, torch.int64)
     return tokens, dim, vocab, hs, ws
 
 
@@ -173,13 +186,15 @@ def linear_loss(hidden, weight, targets, ignore=-100, stream=None):
     backward call takes.  The logits are never stored.  0 where a target is
     `ignore`; see check_losses for targets outside the vocabulary."""
     tokens, dim, vocab, hs, ws = _loss_inputs("linear_loss", hidden, weight, targets)
-    with _On(stream):
-        loss = torch.empty(tokens, dtype=torch.float32, device=hidden.device)
-        lse = torch.empty(tokens, dtype=torch.float32, device=hidden.device)
+    status = _status(hidden.device)
+    with _on(stream):
+        loss = hidden.new_empty(tokens, dtype=torch.float32)
+        lse = hidden.new_empty(tokens, dtype=torch.float32)
         need = A.zero_loss_workspace(tokens, vocab, dim)[0]
-        space = torch.empty(need, dtype=torch.uint8, device=hidden.device)
-        A.zero_loss_forward(hidden, hs, weight, ws, targets, ignore, tokens, vocab, dim, _LP[hidden.dtype], loss,
-                            lse, _status(hidden.device), space, need, stream)
+        space = hidden.new_empty(need, dtype=torch.uint8)
+        _call("zero_loss_forward", hidden.data_ptr(), hs, weight.data_ptr(), ws, targets.data_ptr(), ignore, tokens,
+              vocab, dim, _LP[hidden.dtype], loss.data_ptr(), lse.data_ptr(), status.data_ptr(), space.data_ptr(),
+              need, A._stream(stream))
     return loss, lse
 
 
@@ -189,24 +204,38 @@ def linear_loss_backward(hidden, weight, targets, lse, grad_loss, ignore=-100, g
     tensors if there are any (e.g. views of the flat gradient buffer)."""
     where = "linear_loss_backward"
     tokens, dim, vocab, hs, ws = _loss_inputs(where, hidden, weight, targets)
-    _vector(where, "lse", lse, tokens, torch.float32, hidden.device)
-    _vector(where, "grad_loss", grad_loss, tokens, torch.float32, hidden.device)
-    with _On(stream):
+    _vector(where, "lse", lse, tokens, torch.float32)
+    _vector(where, "grad_loss", grad_loss, tokens, torch.float32)
+    status = _status(hidden.device)
+    with _on(stream):
         if grad_hidden is None:
-            grad_hidden = torch.empty((tokens, dim), dtype=hidden.dtype, device=hidden.device)
+            grad_hidden = hidden.new_empty((tokens, dim))
         if grad_weight is None:
-            grad_weight = torch.empty((vocab, dim), dtype=hidden.dtype, device=hidden.device)
-        ghs = _matrix(where, "grad_hidden", grad_hidden, hidden, (tokens, dim))[2]
-        gws = _matrix(where, "grad_weight", grad_weight, hidden, (vocab, dim))[2]
+            grad_weight = hidden.new_empty((vocab, dim))
+        ghs = _matrix(where, "grad_hidden", grad_hidden, hidden.dtype, (tokens, dim))[2]
+        gws = _matrix(where, "grad_weight", grad_weight, hidden.dtype, (vocab, dim))[2]
         need = A.zero_loss_workspace(tokens, vocab, dim)[1]
-        space = torch.empty(need, dtype=torch.uint8, device=hidden.device)
-        A.zero_loss_backward(hidden, hs, weight, ws, targets, ignore, tokens, vocab, dim, _LP[hidden.dtype], lse,
-                             grad_loss, grad_hidden, ghs, grad_weight, gws, _status(hidden.device), space, need,
-                             stream)
+        space = hidden.new_empty(need, dtype=torch.uint8)
+        _call("zero_loss_backward", hidden.data_ptr(), hs, weight.data_ptr(), ws, targets.data_ptr(), ignore, tokens,
+              vocab, dim, _LP[hidden.dtype], lse.data_ptr(), grad_loss.data_ptr(), grad_hidden.data_ptr(), ghs,
+              grad_weight.data_ptr(), gws, status.data_ptr(), space.data_ptr(), need, A._stream(stream))
     return grad_hidden, grad_weight
 
 
 # ---- global norm, clipping, packing ----------------------------------------------
+
+_T = torch.Tensor
+_DTYPE = attrgetter("dtype")
+
+
+def _gather(where, name, tensors, dtype, device):
+    """(element counts, addresses) of contiguous tensors of one type on the current device."""
+    if (set(map(_DTYPE, tensors)) != {dtype} or set(map(_T.get_device, tensors)) != {device}
+            or not all(map(_T.is_contiguous, tensors))):
+        _refuse(where, "%s must be contiguous tensors of one type (float16, bfloat16 or float32) on the current "
+                       "CUDA device" % name)
+    return array("q", map(_T.numel, tensors)), array("Q", map(_T.data_ptr, tensors))
+
 
 def clip_gradients(grads, out=None, offsets=None, max_norm=0.0, loss_scale=1.0, stream=None):
     """(norm, coef, nonfinite), one-element device tensors: the global L2 norm of
@@ -218,33 +247,37 @@ def clip_gradients(grads, out=None, offsets=None, max_norm=0.0, loss_scale=1.0, 
     where = "clip_gradients"
     if not grads:
         _refuse(where, "no gradients")
-    dtype, device = grads[0].dtype, grads[0].device
-    if dtype not in _CLIP or not grads[0].is_cuda:
-        _refuse(where, "grads must be float16, bfloat16 or float32 CUDA tensors")
-    lens = np.array([g.numel() for g in grads], np.int64)
-    for g in grads:
-        if g.dtype != dtype or g.device != device or not g.is_contiguous():
-            _refuse(where, "grads must be contiguous, of one type and on one device")
-    src = np.array([g.data_ptr() for g in grads], np.uint64)
+    dtype, device = grads[0].dtype, torch._C._cuda_getDevice()
+    if dtype not in _CLIP:
+        _refuse(where, "grads must be float16, bfloat16 or float32")
+    lens, src = _gather(where, "grads", grads, dtype, device)
+    n = len(lens)
     if out is None:
         dst = src
     elif isinstance(out, torch.Tensor):
-        if out.dim() != 1 or out.dtype != dtype or out.device != device or not out.is_contiguous():
+        if out.ndim != 1 or out.dtype != dtype or out.get_device() != device or not out.is_contiguous():
             _refuse(where, "out must be a contiguous 1-D tensor of the gradients' type and device")
-        at = np.cumsum(lens) - lens if offsets is None else np.ascontiguousarray(offsets, np.int64)
-        if at.shape != lens.shape or (at < 0).any() or (at + lens > out.numel()).any():
+        size, first, room = out.element_size(), out.data_ptr(), out.numel()
+        if offsets is None:
+            at = list(accumulate(lens, initial=0))
+            fits = at.pop() <= room
+        else:
+            at = [int(o) for o in offsets]
+            fits = len(at) == n and all(0 <= o <= room - k for o, k in zip(at, lens))
+        if not fits:
             _refuse(where, "a gradient does not fit into out at its offset")
-        dst = at.astype(np.uint64) * np.uint64(out.element_size()) + np.uint64(out.data_ptr())
+        dst = array("Q", [first + size * o for o in at])
     else:
-        if len(out) != len(grads) or any(o.dtype != dtype or o.device != device or o.numel() != n
-                                         or not o.is_contiguous() for o, n in zip(out, lens)):
-            _refuse(where, "out must hold one contiguous tensor of the same length and type per gradient")
-        dst = np.array([o.data_ptr() for o in out], np.uint64)
-    with _On(stream):
-        norm, coef = torch.empty((), dtype=torch.float32, device=device), torch.empty((), dtype=torch.float32, device=device)
-        nonfinite = torch.empty((), dtype=torch.int32, device=device)
-        need = A.zero_clip_workspace(lens)
-        space = torch.empty(need, dtype=torch.uint8, device=device)
-        A.zero_clip_gradients(src, lens, _CLIP[dtype], dst, loss_scale, max_norm, norm, coef, nonfinite, space, need,
-                              stream)
-    return norm, coef, nonfinite
+        into, dst = _gather(where, "out", out, dtype, device)
+        if into != lens:
+            _refuse(where, "out must hold one tensor of the same length per gradient")
+    with _on(stream):
+        at_lens, need = lens.buffer_info()[0], _i64()
+        _call("zero_clip_workspace", n, at_lens, byref(need))
+        found = grads[0].new_empty(3, dtype=torch.float32)
+        space = grads[0].new_empty(need.value, dtype=torch.uint8)
+        at = found.data_ptr()
+        _call("zero_clip_gradients", n, src.buffer_info()[0], at_lens, _CLIP[dtype], dst.buffer_info()[0], loss_scale,
+              max_norm, at, at + 4, at + 8, space.data_ptr(), need.value, A._stream(stream))
+        norm, coef, nonfinite = found.unbind()
+    return norm, coef, nonfinite.view(torch.int32)
