@@ -39,13 +39,12 @@ constexpr int kOperandBytes = kHalf * kTileK * 2;
 constexpr int kStageBytes = 2 * kOperandBytes;
 constexpr int kBoxBytes = 64 * kTileK * 2;  // a 64 x 64 box of an operand whose rows run along K
 constexpr int kStoreBytes = 32 * 128;       // 32 rows of 128 bytes: one warp's store
-// Warps that take a tile's results, and the columns of each: a quarter of the
-// warps on each quarter of the rows.  The statistics keep their columns in
-// registers and have the longer way (1023 tokens x 768: 65 us with eight warps
-// for them, STATS16 us with sixteen); the others need room to store from.
-constexpr int kStatsWarps = 16, kStatsColumns = kTileN / (kStatsWarps / 4);
-constexpr int kStoreWarps = 8, kStoreColumns = kTileN / (kStoreWarps / 4);
-constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kStoreWarps * kStoreBytes;
+// Warps that take a tile's results: two on each quarter of its rows, each half of
+// the columns.  (Sixteen for the statistics: 0.865 ms for 8184 tokens x 1600, with
+// eight 0.849: they take issue slots from the thread that feeds the tensor core.)
+constexpr int kResultWarps = 8, kResultColumns = kTileN / 2;
+constexpr int kProductThreads = 64 + 32 * kResultWarps;
+constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kResultWarps * kStoreBytes;
 // The tensor core's float sum drops the low bits of every step of 16, always
 // towards zero: a logit of 15 over 4096 products came out 6e-5 too small, a
 // relative 4e-6 where float addition has 4e-8.  The losses are float, so the
@@ -249,6 +248,30 @@ __device__ __forceinline__ void tmem_load16(uint32_t addr, float v[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// two floats at once, each rounded to nearest
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("add.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t &>(r))
+        : "l"(reinterpret_cast<const uint64_t &>(a)), "l"(reinterpret_cast<const uint64_t &>(b)));
+    return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t &>(r))
+        : "l"(reinterpret_cast<const uint64_t &>(a)), "l"(reinterpret_cast<const uint64_t &>(b)));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t &>(r))
+        : "l"(reinterpret_cast<const uint64_t &>(a)), "l"(reinterpret_cast<const uint64_t &>(b)),
+          "l"(reinterpret_cast<const uint64_t &>(c)));
+    return r;
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -499,14 +522,8 @@ __device__ __forceinline__ bool any_of(int id, int threads, bool mine) {
     return r != 0;
 }
 
-template <bool STATS>
-struct Block {
-    static constexpr int kWarps = STATS ? kStatsWarps : kStoreWarps;
-    static constexpr int kThreads = 64 + 32 * kWarps;
-};
-
 template <bool BF16, bool STATS>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Block<STATS>::kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
 loss_products(const __grid_constant__ ProductParams p) {
     extern __shared__ unsigned char raw[];
     __shared__ Shared sh;
@@ -523,7 +540,7 @@ loss_products(const __grid_constant__ ProductParams p) {
         }
         for (int b = 0; b < 2; ++b) {
             bar_init(smem_addr(&sh.acc_full[b]), 1);
-            bar_init(smem_addr(&sh.acc_empty[b]), 2 * Block<STATS>::kWarps);
+            bar_init(smem_addr(&sh.acc_empty[b]), 2 * kResultWarps);
         }
         bar_init(smem_addr(&sh.drained), 1);
         sh.dead = 0;
@@ -661,32 +678,37 @@ loss_products(const __grid_constant__ ProductParams p) {
     } else if constexpr (STATS) {  // ------------------------------- statistics
         const int quad = warp & 3;  // the quarter of the lanes this warp may read
         const int group = (warp - 2) >> 2;  // which of the tile's columns it takes
-        float2(*const joined)[kStatsWarps / 4][kHalf] = reinterpret_cast<float2(*)[kStatsWarps / 4][kHalf]>(smem + kStages * kStageBytes);
+        using Joined = float2[kResultWarps / 4][kHalf];
+        Joined *const joined = reinterpret_cast<Joined *>(smem + kStages * kStageBytes);
         int buf = 0;
         uint32_t acc_phase = 0;
         for (int j = 0; work.at(j, t); ++j) {
             const int row = quad * 32 + lane;
             const long long token = (long long)t.m0 + (int)rank * kHalf + row;
             const bool mine = token < p.tokens;
-            const long long v0 = (long long)t.n0 + group * kStatsColumns;
+            const long long v0 = (long long)t.n0 + group * kResultColumns;
             const long long left = p.vocab - v0;  // columns that exist
             const long long at = mine ? p.target[token] - v0 : -1;
-            float z[kStatsColumns];
+            float z[kResultColumns];
 #pragma unroll
-            for (int i = 0; i < kStatsColumns; ++i) z[i] = 0.0f;
+            for (int i = 0; i < kResultColumns; ++i) z[i] = 0.0f;
             bool ok = true;
             for (int c = chunks_of(t); c > 0; --c) {
                 const bool got = wait_for(&sh.acc_full[buf], acc_phase, dead, limit, p.status);
                 ok = __all_sync(0xffffffffu, got);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t acc = tmem + buf * kTileN + group * kStatsColumns + ((uint32_t)(quad * 32) << 16);
+                const uint32_t acc = tmem + buf * kTileN + group * kResultColumns + ((uint32_t)(quad * 32) << 16);
 #pragma unroll
-                for (int i = 0; i < kStatsColumns; i += 16) {
+                for (int i = 0; i < kResultColumns; i += 16) {
                     float part[16];
                     tmem_load16(acc + i, part);
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) z[i + k] = __fadd_rn(z[i + k], part[k]);
+                    for (int k = 0; k < 16; k += 2) {
+                        const float2 two = add2(make_float2(z[i + k], z[i + k + 1]), make_float2(part[k], part[k + 1]));
+                        z[i + k] = two.x;
+                        z[i + k + 1] = two.y;
+                    }
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -696,26 +718,31 @@ loss_products(const __grid_constant__ ProductParams p) {
             }
             float2 part = make_float2(-INFINITY, 0.0f);
             if (ok && left > 0) {
-                if (left < kStatsColumns) {
+                if (left < kResultColumns) {
 #pragma unroll
-                    for (int i = 0; i < kStatsColumns; ++i)
+                    for (int i = 0; i < kResultColumns; ++i)
                         if (i >= left) z[i] = -INFINITY;
                 }
-                if (__any_sync(0xffffffffu, at >= 0 && at < kStatsColumns)) {
+                if (__any_sync(0xffffffffu, at >= 0 && at < kResultColumns)) {
                     float z_y = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < kStatsColumns; ++i) z_y = i == at ? z[i] : z_y;
-                    if (at >= 0 && at < kStatsColumns) p.picked[token] = z_y;
+                    for (int i = 0; i < kResultColumns; ++i) z_y = i == at ? z[i] : z_y;
+                    if (at >= 0 && at < kResultColumns) p.picked[token] = z_y;
                 }
                 float tops[4] = {z[0], z[1], z[2], z[3]}, sums[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int i = 4; i < kStatsColumns; ++i) tops[i & 3] = fmaxf(tops[i & 3], z[i]);
+                for (int i = 4; i < kResultColumns; ++i) tops[i & 3] = fmaxf(tops[i & 3], z[i]);
                 const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
                 // a row of -inf: any finite base leaves its sum at 0
                 const float high = top == -INFINITY ? 0.0f : top;
                 const float base = __fmul_rn(high, kLog2e);
 #pragma unroll
-                for (int i = 0; i < kStatsColumns; ++i) sums[i & 3] += exp2_approx(__fmaf_rn(z[i], kLog2e, -base));
+                for (int i = 0; i < kResultColumns; i += 2) {
+                    const float2 x = fma2(make_float2(z[i], z[i + 1]), make_float2(kLog2e, kLog2e), make_float2(-base, -base));
+                    const float2 e = add2(make_float2(sums[i & 2], sums[(i & 2) + 1]), make_float2(exp2_approx(x.x), exp2_approx(x.y)));
+                    sums[i & 2] = e.x;
+                    sums[(i & 2) + 1] = e.y;
+                }
                 // the sum is relative to 2^base, and base to top log2(e) rounded once
                 const float miss = __fmaf_rn(high, kLog2e, -base);
                 const float sum = (sums[0] + sums[1]) + (sums[2] + sums[3]);
@@ -723,16 +750,16 @@ loss_products(const __grid_constant__ ProductParams p) {
             }
             // the warps of a row join their parts; if one gave up, all stop
             joined[j & 1][group][row] = part;
-            if (any_of(1 + quad, 32 * (kStatsWarps / 4), !ok)) break;
+            if (any_of(1 + quad, 32 * (kResultWarps / 4), !ok)) break;
             if (group == 0 && mine) {
 #pragma unroll
-                for (int g = 1; g < kStatsWarps / 4; ++g) part = join_parts(part, joined[j & 1][g][row]);
+                for (int g = 1; g < kResultWarps / 4; ++g) part = join_parts(part, joined[j & 1][g][row]);
                 p.parts[t.n * p.tokens + token] = part;
             }
         }
     } else {  // ------------------------------------------------------ results
         const int quad = warp & 3;
-        const int first = ((warp - 2) >> 2) * kStoreColumns;  // its columns
+        const int first = ((warp - 2) >> 2) * kResultColumns;  // its columns
         const uint32_t buffer = stage0 + kStages * kStageBytes + (warp - 2) * kStoreBytes;
         const float factor = p.record->factor;
         int buf = 0;
@@ -754,7 +781,11 @@ loss_products(const __grid_constant__ ProductParams p) {
                     float z[32];
                     tmem_load32(acc + col, z);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) z[j] = exp2_approx(__fmaf_rn(z[j], kLog2e, -lse2));
+                    for (int j = 0; j < 32; j += 2) {
+                        const float2 x = fma2(make_float2(z[j], z[j + 1]), make_float2(kLog2e, kLog2e), make_float2(-lse2, -lse2));
+                        z[j] = exp2_approx(x.x);
+                        z[j + 1] = exp2_approx(x.y);
+                    }
                     const uint32_t hit = y >= col && y < col + 32 ? 1u << (y - col) : 0u;
                     if (__any_sync(0xffffffffu, hit != 0u)) {
 #pragma unroll
@@ -766,9 +797,12 @@ loss_products(const __grid_constant__ ProductParams p) {
                         for (int j = 0; j < 32; ++j) z[j] = j < keep ? z[j] : 0.0f;
                     }
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) w[j] = pack_lp<BF16>(z[2 * j] * ratio, z[2 * j + 1] * ratio);
+                    for (int j = 0; j < 16; ++j) {
+                        const float2 x = mul2(make_float2(z[2 * j], z[2 * j + 1]), make_float2(ratio, ratio));
+                        w[j] = pack_lp<BF16>(x.x, x.y);
+                    }
                 };
-                for (int c = first; c < first + kStoreColumns; c += 64) {
+                for (int c = first; c < first + kResultColumns; c += 64) {
                     uint32_t w[32];
                     q_of(c, w);
                     q_of(c + 32, w + 16);
@@ -776,7 +810,7 @@ loss_products(const __grid_constant__ ProductParams p) {
                 }
             } else if (t.kind == kGradHidden) {
                 const bool any = t.k1 > t.k0;  // else the accumulator was never written
-                for (int c = first; c < first + kStoreColumns; c += 32) {
+                for (int c = first; c < first + kResultColumns; c += 32) {
                     float z[32];
                     tmem_load32(acc + c, z);
                     uint32_t w[32];
@@ -794,7 +828,7 @@ loss_products(const __grid_constant__ ProductParams p) {
                     for (int j = 0; j < 16; ++j)
                         w[j] = any ? pack_lp<BF16>(z[2 * j] * factor, z[2 * j + 1] * factor) : 0u;
                 };
-                for (int c = first; c < first + kStoreColumns; c += 64) {
+                for (int c = first; c < first + kResultColumns; c += 64) {
                     uint32_t w[32];
                     scaled(c, w);
                     scaled(c + 32, w + 16);
@@ -1137,7 +1171,7 @@ int pairs_at_once() {
             return 0;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2);
-        cfg.blockDim = dim3(Block<STATS>::kThreads);
+        cfg.blockDim = dim3(kProductThreads);
         cfg.dynamicSmemBytes = kSmemBytes;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1163,7 +1197,7 @@ cudaError_t launch_products(const ProductParams &p, int64_t tiles, cudaStream_t 
     if (pairs < 1) return cudaErrorInvalidConfiguration;
     if (tiles > 0x3fffffff) return cudaErrorInvalidValue;
     const int64_t use = std::max<int64_t>(1, std::min<int64_t>(pairs, tiles));
-    return launch_pdl(loss_products<BF16, STATS>, dim3((unsigned)(2 * use)), dim3(Block<STATS>::kThreads), kSmemBytes, stream, p);
+    return launch_pdl(loss_products<BF16, STATS>, dim3((unsigned)(2 * use)), dim3(kProductThreads), kSmemBytes, stream, p);
 }
 
 // whether the few tokens' hidden states fit into shared memory twice on an SM
