@@ -10,7 +10,9 @@ multiples of 8 and pointers 16-byte aligned.  `stream` is the current stream, a
 torch.cuda.Stream or a raw cudaStream_t; outputs and scratch are allocated for
 that stream, so a caller on several streams orders its own tensors between
 them and nothing else.  Wrong shapes, types or devices raise ZeroError
-(ZERO_EINVAL) before any device work.
+(ZERO_EINVAL) before any device work.  A process's first loss call on a device
+allocates its status word and waits for the device, so it belongs before a graph
+capture; everything else can be captured.
 """
 import contextlib
 from array import array
@@ -52,6 +54,14 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+def _like(t):
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
+def _scratch(n, device):
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
 def _matrix(where, name, t, dtype=None, shape=None):
     """(rows, columns, row stride) of a 2-D tensor with contiguous rows on the current device."""
     if t.ndim != 2 or t.dtype not in _LP or t.get_device() != torch._C._cuda_getDevice():
@@ -86,7 +96,9 @@ def check_losses(device=None):
     """Waits for the device and raises if a linear_loss or linear_loss_backward
     since the last check met a target outside the vocabulary (ZERO_EINVAL) or
     gave up a bounded wait (ZERO_ETIMEOUT: its outputs are not valid)."""
-    device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    device = torch.device("cuda" if device is None else device)
+    if device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
     torch.cuda.synchronize(device)
     word = _status(device)
     bits = int(word[0].item())
@@ -112,8 +124,7 @@ def residual_norm(x, residual, weight, eps, stream=None):
     with rstd = (mean(sum^2) + eps)^(-1/2) over each row."""
     rows, dim, xs, rs = _norm_inputs("residual_norm", x, residual, weight)
     with _on(stream):
-        out = x.new_empty((rows, dim))
-        total = x.new_empty((rows, dim))
+        out, total = _like(x), _like(x)
         _call("zero_norm_forward", x.data_ptr(), xs, _addr(residual), rs, weight.data_ptr(), eps, rows, dim,
               _LP[x.dtype], out.data_ptr(), dim, total.data_ptr(), dim, A._stream(stream))
     return out, total
@@ -124,9 +135,9 @@ def residual_norm_quantized(x, residual, weight, eps, fmt=A.ZERO_QUANT_INT8, str
     each, int8 tensor) with a float scale per block of 128 elements of a row."""
     rows, dim, xs, rs = _norm_inputs("residual_norm_quantized", x, residual, weight)
     with _on(stream):
-        codes = x.new_empty((rows, dim), dtype=torch.int8)
-        scales = x.new_empty((rows, -(-dim // A.ZERO_QUANT_BLOCK)), dtype=torch.float32)
-        total = x.new_empty((rows, dim))
+        codes = torch.empty((rows, dim), dtype=torch.int8, device=x.device)
+        scales = torch.empty((rows, -(-dim // A.ZERO_QUANT_BLOCK)), dtype=torch.float32, device=x.device)
+        total = _like(x)
         _call("zero_norm_forward_quantized", x.data_ptr(), xs, _addr(residual), rs, weight.data_ptr(), eps, rows,
               dim, _LP[x.dtype], fmt, codes.data_ptr(), scales.data_ptr(), total.data_ptr(), dim, A._stream(stream))
     return codes, scales, total
@@ -143,7 +154,7 @@ def dequantize_rows(codes, scales, fmt, dtype, stream=None):
             or scales.shape != (rows, -(-dim // A.ZERO_QUANT_BLOCK)) or not scales.is_contiguous()):
         _refuse(where, "scales must be one float32 per block of a row, dtype float16 or bfloat16")
     with _on(stream):
-        out = codes.new_empty((rows, dim), dtype=dtype)
+        out = torch.empty((rows, dim), dtype=dtype, device=codes.device)
         _call("zero_dequantize_rows", codes.data_ptr(), scales.data_ptr(), fmt, rows, dim, _LP[dtype],
               out.data_ptr(), dim, A._stream(stream))
     return out
@@ -159,10 +170,9 @@ def residual_norm_backward(total, weight, grad_out, grad_sum, eps, stream=None):
     gs = _matrix(where, "grad_out", grad_out, total.dtype, (rows, dim))[2]
     ss = 0 if grad_sum is None else _matrix(where, "grad_sum", grad_sum, total.dtype, (rows, dim))[2]
     with _on(stream):
-        grad_in = total.new_empty((rows, dim))
-        grad_weight = total.new_empty(dim)
+        grad_in, grad_weight = _like(total), _like(weight)
         need = A.zero_norm_backward_workspace(rows, dim)
-        space = total.new_empty(need, dtype=torch.uint8)
+        space = _scratch(need, total.device)
         _call("zero_norm_backward", total.data_ptr(), ts, weight.data_ptr(), grad_out.data_ptr(), gs, _addr(grad_sum),
               ss, eps, rows, dim, _LP[total.dtype], grad_in.data_ptr(), dim, grad_weight.data_ptr(),
               space.data_ptr(), need, A._stream(stream))
@@ -186,12 +196,13 @@ def linear_loss(hidden, weight, targets, ignore=-100, stream=None):
     backward call takes.  The logits are never stored.  0 where a target is
     `ignore`; see check_losses for targets outside the vocabulary."""
     tokens, dim, vocab, hs, ws = _loss_inputs("linear_loss", hidden, weight, targets)
-    status = _status(hidden.device)
+    device = hidden.device
+    status = _status(device)
     with _on(stream):
-        loss = hidden.new_empty(tokens, dtype=torch.float32)
-        lse = hidden.new_empty(tokens, dtype=torch.float32)
+        loss = torch.empty(tokens, dtype=torch.float32, device=device)
+        lse = torch.empty_like(loss)
         need = A.zero_loss_workspace(tokens, vocab, dim)[0]
-        space = hidden.new_empty(need, dtype=torch.uint8)
+        space = _scratch(need, device)
         _call("zero_loss_forward", hidden.data_ptr(), hs, weight.data_ptr(), ws, targets.data_ptr(), ignore, tokens,
               vocab, dim, _LP[hidden.dtype], loss.data_ptr(), lse.data_ptr(), status.data_ptr(), space.data_ptr(),
               need, A._stream(stream))
@@ -209,13 +220,13 @@ def linear_loss_backward(hidden, weight, targets, lse, grad_loss, ignore=-100, g
     status = _status(hidden.device)
     with _on(stream):
         if grad_hidden is None:
-            grad_hidden = hidden.new_empty((tokens, dim))
+            grad_hidden = _like(hidden)
         if grad_weight is None:
-            grad_weight = hidden.new_empty((vocab, dim))
+            grad_weight = _like(weight)
         ghs = _matrix(where, "grad_hidden", grad_hidden, hidden.dtype, (tokens, dim))[2]
         gws = _matrix(where, "grad_weight", grad_weight, hidden.dtype, (vocab, dim))[2]
         need = A.zero_loss_workspace(tokens, vocab, dim)[1]
-        space = hidden.new_empty(need, dtype=torch.uint8)
+        space = _scratch(need, hidden.device)
         _call("zero_loss_backward", hidden.data_ptr(), hs, weight.data_ptr(), ws, targets.data_ptr(), ignore, tokens,
               vocab, dim, _LP[hidden.dtype], lse.data_ptr(), grad_loss.data_ptr(), grad_hidden.data_ptr(), ghs,
               grad_weight.data_ptr(), gws, status.data_ptr(), space.data_ptr(), need, A._stream(stream))
@@ -274,8 +285,8 @@ def clip_gradients(grads, out=None, offsets=None, max_norm=0.0, loss_scale=1.0, 
     with _on(stream):
         at_lens, need = lens.buffer_info()[0], _i64()
         _call("zero_clip_workspace", n, at_lens, byref(need))
-        found = grads[0].new_empty(3, dtype=torch.float32)
-        space = grads[0].new_empty(need.value, dtype=torch.uint8)
+        found = torch.empty(3, dtype=torch.float32, device=grads[0].device)
+        space = _scratch(need.value, grads[0].device)
         at = found.data_ptr()
         _call("zero_clip_gradients", n, src.buffer_info()[0], at_lens, _CLIP[dtype], dst.buffer_info()[0], loss_scale,
               max_norm, at, at + 4, at + 8, space.data_ptr(), need.value, A._stream(stream))
