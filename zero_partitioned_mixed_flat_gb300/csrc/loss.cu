@@ -902,7 +902,11 @@ loss_join(const float2 *__restrict__ parts, const float *__restrict__ picked, in
     pdl_enter();
     __shared__ float2 way[kJoinWays][kJoinTokens + 1];
     const int x = threadIdx.x % kJoinTokens, w = threadIdx.x / kJoinTokens;
-    long long t = (long long)blockIdx.x * kJoinTokens + x;
+    const long long t = (long long)blockIdx.x * kJoinTokens + x;
+    // what the warp that ends with token w needs, asked for with the parts
+    const long long mine = (long long)blockIdx.x * kJoinTokens + w;
+    const long long y = mine < tokens ? target[mine] : ignore;
+    const float z_y = y >= 0 && y < vocab && y != ignore ? picked[mine] : 0.0f;
     float2 acc = make_float2(-INFINITY, 0.0f);
     if (t < tokens) {
         for (int i = w; i < tiles; i += 8 * kJoinWays) {
@@ -928,18 +932,16 @@ loss_join(const float2 *__restrict__ parts, const float *__restrict__ picked, in
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         acc = join_parts(acc, make_float2(__shfl_xor_sync(0xffffffffu, acc.x, o), __shfl_xor_sync(0xffffffffu, acc.y, o)));
-    t = (long long)blockIdx.x * kJoinTokens + w;
-    if (lane != 0 || t >= tokens) return;
+    if (lane != 0 || mine >= tokens) return;
     const float l = acc.x + log2f(acc.y) * kLn2;
-    lse[t] = l;
-    const long long y = target[t];
+    lse[mine] = l;
     if (y == ignore) {
-        loss[t] = 0.0f;
+        loss[mine] = 0.0f;
     } else if (y < 0 || y >= vocab) {
-        loss[t] = __int_as_float(0x7fffffff);
+        loss[mine] = __int_as_float(0x7fffffff);
         atomicOr(status, ZERO_LOSS_BAD_TARGET);
     } else {
-        loss[t] = l - picked[t];
+        loss[mine] = l - z_y;
     }
 }
 
@@ -1074,17 +1076,30 @@ loss_place(const int64_t *__restrict__ target, long long ignore, long long token
     const long long each = (tokens + kPlaceThreads - 1) / kPlaceThreads;
     const long long t0 = threadIdx.x * each < tokens ? threadIdx.x * each : tokens;
     const long long t1 = t0 + each < tokens ? t0 + each : tokens;
+    // the first tokens of a thread (all, up to 4096 tokens) stay in registers
+    constexpr int kKept = 4;
+    long long kept_y[kKept];
+    float kept_g[kKept], kept_lse[kKept];
+#pragma unroll
+    for (int k = 0; k < kKept; ++k) {
+        const bool is = t0 + k < t1;
+        kept_y[k] = is ? target[t0 + k] : ignore;
+        kept_g[k] = is ? grad_loss[t0 + k] : 0.0f;
+        kept_lse[k] = is ? lse[t0 + k] : 0.0f;
+    }
     int mine = 0;
     float top = 0.0f;
     bool bad = false;
-    for (long long t = t0; t < t1; ++t) {
-        const long long y = target[t];
-        const float g = fabsf(grad_loss[t]);
-        const bool counts = y != ignore && y >= 0 && y < vocab;
-        bad |= y != ignore && !counts;
-        mine += counts;
-        if (counts && g <= 3.402823466e38f) top = fmaxf(top, g);
-    }
+    const auto counts = [&](long long y) { return y != ignore && y >= 0 && y < vocab; };
+    const auto look = [&](long long y, float grad) {
+        const float g = fabsf(grad);
+        bad |= y != ignore && !counts(y);
+        mine += counts(y);
+        if (counts(y) && g <= 3.402823466e38f) top = fmaxf(top, g);
+    };
+#pragma unroll
+    for (int k = 0; k < kKept; ++k) look(kept_y[k], kept_g[k]);
+    for (long long t = t0 + kKept; t < t1; ++t) look(target[t], grad_loss[t]);
     if (bad) atomicOr(status, ZERO_LOSS_BAD_TARGET);
     int before = mine;  // inclusive sum over the warp's lanes, then over the warps
     for (int o = 1; o < 32; o <<= 1) {
@@ -1102,16 +1117,18 @@ loss_place(const int64_t *__restrict__ target, long long ignore, long long token
         top = fmaxf(top, tops[w]);
     }
     int at = before - mine;
-    for (long long t = t0; t < t1; ++t) {
-        const long long y = target[t];
-        const bool counts = y != ignore && y >= 0 && y < vocab;
-        place[t] = counts ? at : -1;
-        if (!counts) continue;
+    const auto put = [&](long long t, long long y, float grad, float l) {
+        place[t] = counts(y) ? at : -1;
+        if (!counts(y)) return;
         index[at] = (int)t;
-        lse2[at] = lse[t] * kLog2e;
-        ratio[at] = top > 0.0f ? grad_loss[t] / top * top_operand : grad_loss[t];
+        lse2[at] = l * kLog2e;
+        ratio[at] = top > 0.0f ? grad / top * top_operand : grad;
         place_target[at++] = (int)y;
-    }
+    };
+#pragma unroll
+    for (int k = 0; k < kKept; ++k)
+        if (t0 + k < t1) put(t0 + k, kept_y[k], kept_g[k], kept_lse[k]);
+    for (long long t = t0 + kKept; t < t1; ++t) put(t, target[t], grad_loss[t], lse[t]);
     for (long long i = all + threadIdx.x; i < rows; i += kPlaceThreads) {  // rows that fill the last tile
         lse2[i] = ratio[i] = 0.0f;
         place_target[i] = -1;
