@@ -167,3 +167,15 @@ def test_workspaces():
 
 def test_library_status_names():
     assert (A.ZERO_LOSS_TIMEOUT, A.ZERO_LOSS_BAD_TARGET, A.ZERO_FP32) == (1, 2, 2)
+
+
+def test_the_package_needs_no_torch_until_the_head_is_used():
+    import subprocess
+    import sys
+    program = ("import sys; sys.modules['torch'] = None\n"
+               "import zero_partitioned_mixed_flat_gb300 as Z\n"
+               "Z.load(); Z.zero_memory_report(8, 1)\n"
+               "try:\n    Z.linear_loss\nexcept ImportError:\n    print('late')\n")
+    out = subprocess.run([sys.executable, "-c", program], capture_output=True, text=True, timeout=120)
+    assert out.stdout.strip() == "late", out.stderr
+    assert callable(Z.residual_norm) and not hasattr(Z, "no_such_name")

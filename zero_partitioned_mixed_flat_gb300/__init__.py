@@ -25,8 +25,17 @@ from ._abi import (  # noqa: F401
     zero_clip_workspace, zero_clip_gradients, ZERO_FP32, ZERO_HEAD_MAX_DIM, ZERO_LOSS_TIMEOUT,
     ZERO_LOSS_BAD_TARGET,
 )
-from .head import (  # noqa: F401
-    check_losses, clip_gradients, dequantize_rows, linear_loss, linear_loss_backward, residual_norm,
-    residual_norm_backward, residual_norm_quantized,
-)
 from .plan import ZeroPlan  # noqa: F401
+
+# the training head on torch tensors (head.py), imported at first use: the rest of
+# the package does without torch
+_HEAD = ("check_losses", "clip_gradients", "dequantize_rows", "linear_loss", "linear_loss_backward",
+         "residual_norm", "residual_norm_backward", "residual_norm_quantized")
+
+
+def __getattr__(name):
+    if name in _HEAD:
+        from . import head
+        globals().update((n, getattr(head, n)) for n in _HEAD)
+        return globals()[name]
+    raise AttributeError("module %r has no attribute %r" % (__name__, name))
