@@ -28,14 +28,17 @@ namespace {
 constexpr int kClipThreads = 256;
 constexpr int kClipVecs = 8;      // 16-byte vectors a thread has in flight
 constexpr int kClipChunkBytes = kClipThreads * kClipVecs * 16;
-constexpr int kClipTable = 640;   // tensors of one launch
+// Tensors of one launch: its table is a kernel parameter, 28 bytes a tensor, which
+// the launch copies.  A short list takes the short table.
+constexpr int kClipShort = 64, kClipTable = 640;
 constexpr int kClipBlocks = 608;  // of one launch: four on each of 152 SMs
 
+template <int TABLE>
 struct ClipParams {
-    const void *in[kClipTable];
-    void *out[kClipTable];
-    long long len[kClipTable];
-    int chunk0[kClipTable + 1];  // first chunk of each tensor in this launch
+    const void *in[TABLE];
+    void *out[TABLE];
+    long long len[TABLE];
+    int chunk0[TABLE + 1];  // first chunk of each tensor in this launch
     int n;
     int base;        // sums of the launches before this one
     int total;       // sums of every launch
@@ -91,15 +94,15 @@ struct Element {
 // The chunks of a block: every gridDim-th, so that all blocks together move
 // through the list in order, forwards or from its end.  A chunk is elements
 // [e0, e1) of tensor i.
-template <int TYPE>
+template <int TYPE, int TABLE>
 struct Chunks {
     static constexpr int kElems = kClipChunkBytes / Element<TYPE>::kBytes;
     int at, i;
     long long e0, e1;
 
-    __device__ __forceinline__ explicit Chunks(const ClipParams &p) : at((int)blockIdx.x) {}
+    __device__ __forceinline__ explicit Chunks(const ClipParams<TABLE> &p) : at((int)blockIdx.x) {}
     // false after the last; else finds the chunk's place
-    __device__ __forceinline__ bool here(const ClipParams &p, bool forwards) {
+    __device__ __forceinline__ bool here(const ClipParams<TABLE> &p, bool forwards) {
         const int all = p.chunk0[p.n];
         if (at >= all) return false;
         const int c = forwards ? at : all - 1 - at;
@@ -158,13 +161,13 @@ struct Span {
 // -- the floats' sum not finite, or so small that lost squares could count
 // although an element is not zero -- the thread squares the same elements in
 // double.  So the sum is not finite exactly where an element is not.
-template <int TYPE>
-__global__ void __launch_bounds__(kClipThreads) clip_norm(const __grid_constant__ ClipParams p) {
+template <int TYPE, int TABLE>
+__global__ void __launch_bounds__(kClipThreads) clip_norm(const __grid_constant__ ClipParams<TABLE> p) {
     pdl_enter();
     using E = Element<TYPE>;
     __shared__ double shared[kClipThreads / 32];
     double sum = 0.0;
-    Chunks<TYPE> c(p);
+    Chunks<TYPE, TABLE> c(p);
     for (bool more = c.here(p, true); more;) {
         const Span<TYPE> s(p.in[c.i], c.e0, c.e1);
         const uint4 *vec = reinterpret_cast<const uint4 *>(s.p + s.head);
@@ -209,7 +212,8 @@ __global__ void __launch_bounds__(kClipThreads) clip_norm(const __grid_constant_
 }
 
 // The coefficient from the blocks' sums, by a whole block; `write`: also the results.
-__device__ __forceinline__ float decide(const ClipParams &p, bool write) {
+template <int TABLE>
+__device__ __forceinline__ float decide(const ClipParams<TABLE> &p, bool write) {
     __shared__ double shared[kClipThreads / 32];
     __shared__ float decision;
     double total = 0.0;
@@ -239,7 +243,8 @@ __device__ __forceinline__ float decide(const ClipParams &p, bool write) {
     return decision;
 }
 
-__global__ void __launch_bounds__(kClipThreads) clip_decide(const __grid_constant__ ClipParams p) {
+template <int TABLE>
+__global__ void __launch_bounds__(kClipThreads) clip_decide(const __grid_constant__ ClipParams<TABLE> p) {
     pdl_enter();
     const float coef = decide(p, true);
     if (p.decided && threadIdx.x == 0) *p.decided = coef;
@@ -264,12 +269,12 @@ __device__ __forceinline__ uint4 straddle(const uint4 &lo, const uint4 &hi, int 
 // a vector's elements straddle two of the source's aligned vectors, this lane's and
 // the next lane's; the first and last vector of a chunk are then read element by
 // element, so that nothing outside the tensor is read.
-template <int TYPE>
-__global__ void __launch_bounds__(kClipThreads) clip_scale(const __grid_constant__ ClipParams p) {
+template <int TYPE, int TABLE>
+__global__ void __launch_bounds__(kClipThreads) clip_scale(const __grid_constant__ ClipParams<TABLE> p) {
     pdl_enter();
     using E = Element<TYPE>;
     using Word = typename E::Word;
-    Chunks<TYPE> c(p);
+    Chunks<TYPE, TABLE> c(p);
     c.here(p, false);
     const float coef = p.decided ? *p.decided : decide(p, blockIdx.x == 0 && p.base == 0);
     if (coef == 1.0f && p.in[c.i] == p.out[c.i]) return;  // in place, and nothing to change
@@ -326,13 +331,25 @@ __global__ void __launch_bounds__(kClipThreads) clip_scale(const __grid_constant
 
 template <int TYPE>
 long long chunks_of(int64_t len) {
-    return (len + Chunks<TYPE>::kElems - 1) / Chunks<TYPE>::kElems;
+    constexpr int kElems = kClipChunkBytes / Element<TYPE>::kBytes;
+    return (len + kElems - 1) / kElems;
 }
 
-template <int TYPE>
-cudaError_t clip_impl(int n, const void *const *grads, const int64_t *lens, void *const *out, ClipParams &p,
+template <int TYPE, int TABLE>
+cudaError_t clip_impl(int n, const void *const *grads, const int64_t *lens, void *const *out, float loss_scale,
+                      float max_norm, float *norm, float *coef, int32_t *nonfinite, void *workspace,
                       cudaStream_t stream) {
-    float *decided = p.decided;
+    ClipParams<TABLE> p;
+    p.n = 0;
+    p.base = 0;
+    p.total = 0;
+    float *decided = static_cast<float *>(workspace);  // then, at byte 16, the sums
+    p.sums = static_cast<double *>(workspace) + 2;
+    p.scale = loss_scale;
+    p.max_norm = max_norm;
+    p.norm = norm;
+    p.coef = coef;
+    p.nonfinite = nonfinite;
     long long all = 0;
     for (int i = 0; i < n; ++i) all += chunks_of<TYPE>(lens[i]);
     p.decided = all > kClipBlocks ? decided : nullptr;
@@ -342,7 +359,7 @@ cudaError_t clip_impl(int n, const void *const *grads, const int64_t *lens, void
         for (int i = 0; i < n && e == cudaSuccess;) {
             long long chunks = 0;
             p.n = 0;
-            for (; i < n && p.n < kClipTable; ++i) {
+            for (; i < n && p.n < TABLE; ++i) {
                 if (lens[i] == 0) continue;
                 if (p.n > 0 && chunks + chunks_of<TYPE>(lens[i]) > 0x3fffffffll) break;
                 p.in[p.n] = grads[i];
@@ -354,14 +371,14 @@ cudaError_t clip_impl(int n, const void *const *grads, const int64_t *lens, void
             p.chunk0[p.n] = (int)chunks;
             if (chunks == 0) continue;
             const int sums = (int)(chunks < kClipBlocks ? chunks : kClipBlocks);
-            e = launch_pdl(pass ? clip_scale<TYPE> : clip_norm<TYPE>, dim3((unsigned)(pass ? chunks : sums)),
+            e = launch_pdl(pass ? clip_scale<TYPE, TABLE> : clip_norm<TYPE, TABLE>, dim3((unsigned)(pass ? chunks : sums)),
                            dim3(kClipThreads), 0, stream, p);
             p.base += sums;
         }
         if (pass > 0) break;
         p.total = p.base;
         if (e == cudaSuccess && (p.decided || !out || p.total == 0))
-            e = launch_pdl(clip_decide, dim3(1), dim3(kClipThreads), 0, stream, p);
+            e = launch_pdl(clip_decide<TABLE>, dim3(1), dim3(kClipThreads), 0, stream, p);
     }
     return e;
 }
@@ -379,20 +396,17 @@ int64_t clip_bytes(int n, const int64_t *lens) {
 cudaError_t launch_clip(int n, const void *const *grads, const int64_t *lens, int dtype, void *const *out,
                         float loss_scale, float max_norm, float *norm, float *coef, int32_t *nonfinite,
                         void *workspace, cudaStream_t stream) {
-    ClipParams p;
-    p.n = 0;
-    p.base = 0;
-    p.decided = static_cast<float *>(workspace);  // then, at byte 16, the sums
-    p.sums = static_cast<double *>(workspace) + 2;
-    p.total = 0;
-    p.scale = loss_scale;
-    p.max_norm = max_norm;
-    p.norm = norm;
-    p.coef = coef;
-    p.nonfinite = nonfinite;
-    if (dtype == ZERO_FP16) return clip_impl<ZERO_FP16>(n, grads, lens, out, p, stream);
-    if (dtype == ZERO_BF16) return clip_impl<ZERO_BF16>(n, grads, lens, out, p, stream);
-    return clip_impl<ZERO_FP32>(n, grads, lens, out, p, stream);
+    const auto clip = [&](auto type) {
+        constexpr int kType = decltype(type)::value;
+        if (n <= kClipShort)
+            return clip_impl<kType, kClipShort>(n, grads, lens, out, loss_scale, max_norm, norm, coef, nonfinite, workspace,
+                                                stream);
+        return clip_impl<kType, kClipTable>(n, grads, lens, out, loss_scale, max_norm, norm, coef, nonfinite, workspace,
+                                            stream);
+    };
+    if (dtype == ZERO_FP16) return clip(std::integral_constant<int, ZERO_FP16>());
+    if (dtype == ZERO_BF16) return clip(std::integral_constant<int, ZERO_BF16>());
+    return clip(std::integral_constant<int, ZERO_FP32>());
 }
 
 }  // namespace zk

@@ -20,6 +20,7 @@ from ctypes import byref, c_int64 as _i64
 from itertools import accumulate
 from operator import attrgetter
 
+import numpy as np
 import torch
 
 from . import _abi as A
@@ -269,15 +270,17 @@ def clip_gradients(grads, out=None, offsets=None, max_norm=0.0, loss_scale=1.0, 
         if out.ndim != 1 or out.dtype != dtype or out.get_device() != device or not out.is_contiguous():
             _refuse(where, "out must be a contiguous 1-D tensor of the gradients' type and device")
         size, first, room = out.element_size(), out.data_ptr(), out.numel()
-        if offsets is None:
+        if offsets is None and n <= 64:   # a short list costs less than numpy's calls
             at = list(accumulate(lens, initial=0))
-            fits = at.pop() <= room
+            fits = at[n] <= room
+            dst = array("Q", [first + size * o for o in at])
         else:
-            at = [int(o) for o in offsets]
-            fits = len(at) == n and all(0 <= o <= room - k for o, k in zip(at, lens))
+            sizes = np.frombuffer(lens, np.int64)
+            at = np.cumsum(sizes) - sizes if offsets is None else np.asarray(offsets, np.int64)
+            fits = at.shape == (n,) and at.min() >= 0 and (at + sizes).max() <= room
+            dst = array("Q", (at * size + first).tobytes()) if fits else None
         if not fits:
             _refuse(where, "a gradient does not fit into out at its offset")
-        dst = array("Q", [first + size * o for o in at])
     else:
         into, dst = _gather(where, "out", out, dtype, device)
         if into != lens:
@@ -286,9 +289,10 @@ def clip_gradients(grads, out=None, offsets=None, max_norm=0.0, loss_scale=1.0, 
         at_lens, need = lens.buffer_info()[0], _i64()
         _call("zero_clip_workspace", n, at_lens, byref(need))
         found = torch.empty(3, dtype=torch.float32, device=grads[0].device)
+        norm, coef, nonfinite = found.unbind()
+        nonfinite = nonfinite.view(torch.int32)
         space = _scratch(need.value, grads[0].device)
         at = found.data_ptr()
         _call("zero_clip_gradients", n, src.buffer_info()[0], at_lens, _CLIP[dtype], dst.buffer_info()[0], loss_scale,
               max_norm, at, at + 4, at + 8, space.data_ptr(), need.value, A._stream(stream))
-        norm, coef, nonfinite = found.unbind()
-    return norm, coef, nonfinite.view(torch.int32)
+    return norm, coef, nonfinite
