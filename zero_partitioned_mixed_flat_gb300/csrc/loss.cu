@@ -1074,24 +1074,54 @@ loss_few(const uint4 *__restrict__ hidden, long long hidden_stride, const uint4 
     }
 }
 
+constexpr int kCopyThreads = 128;
+
+// hidden states of the counted tokens, then zeros up to whole blocks of K
+__device__ __forceinline__ void copy_rows(const uint4 *__restrict__ hidden, long long stride, const int *index, long long count,
+                                          long long tokens, int vecs, uint4 *out) {
+    const long long whole = (count + kTileK - 1) / kTileK * kTileK, end = whole < tokens ? whole : tokens;
+    const int each = (int)blockDim.x / kCopyThreads;  // rows of a block at a time
+    for (long long i = (long long)blockIdx.x * each + threadIdx.x / kCopyThreads; i < end; i += (long long)gridDim.x * each) {
+        const uint4 *src = i < count ? hidden + index[i] * stride : nullptr;
+        for (int v = threadIdx.x % kCopyThreads; v < vecs; v += kCopyThreads)
+            out[i * vecs + v] = src ? src[v] : make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
+// the same after loss_place; nothing where every token counts
+__global__ void __launch_bounds__(kCopyThreads)
+loss_compact(const uint4 *__restrict__ hidden, long long stride, const LossRecord *record, const int *__restrict__ index,
+             long long tokens, int vecs, uint4 *out) {
+    pdl_enter();
+    const long long count = record->count;
+    if (count < tokens) copy_rows(hidden, stride, index, count, tokens, vecs, out);
+}
+
 constexpr int kPlaceThreads = 1024;
+
+constexpr int kKept = 4;                            // tokens a thread keeps in registers
+constexpr int kFewPlaces = kKept * kPlaceThreads;  // tokens up to which blocks copy rows too
 
 // The counted tokens in order (index: token of a place; place: place of a token
 // or -1), what the slopes need of each, and the largest finite |grad_loss|.
-// One block; a thread takes consecutive tokens.
+// A thread takes consecutive tokens.  One block; or, up to kFewPlaces tokens, as many
+// as copy the hidden states of the counted ones (out, not NULL; see loss_compact):
+// each finds every place for itself, which saves a launch (1023 tokens x 768: 6.4 us
+// and not 8.6, 4096 x 4096 16 and not 20), and the first writes them down.
 __global__ void __launch_bounds__(kPlaceThreads)
 loss_place(const int64_t *__restrict__ target, long long ignore, long long tokens, long long rows, long long vocab,
            const float *__restrict__ lse, const float *__restrict__ grad_loss, float top_operand, LossRecord *record,
-           int *index, int *place, float *lse2, float *ratio, int *place_target, int *status) {
+           int *index, int *place, float *lse2, float *ratio, int *place_target, int *status,
+           const uint4 *__restrict__ hidden, long long stride, int vecs, uint4 *out) {
     pdl_enter();
     __shared__ int sums[kPlaceThreads / 32];
     __shared__ float tops[kPlaceThreads / 32];
+    __shared__ int listed[kFewPlaces];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long each = (tokens + kPlaceThreads - 1) / kPlaceThreads;
     const long long t0 = threadIdx.x * each < tokens ? threadIdx.x * each : tokens;
     const long long t1 = t0 + each < tokens ? t0 + each : tokens;
-    // the first tokens of a thread (all, up to 4096 tokens) stay in registers
-    constexpr int kKept = 4;
+    const bool writes = blockIdx.x == 0;
     long long kept_y[kKept];
     float kept_g[kKept], kept_lse[kKept];
 #pragma unroll
@@ -1132,43 +1162,34 @@ loss_place(const int64_t *__restrict__ target, long long ignore, long long token
     }
     int at = before - mine;
     const auto put = [&](long long t, long long y, float grad, float l) {
-        place[t] = counts(y) ? at : -1;
+        if (writes) place[t] = counts(y) ? at : -1;
         if (!counts(y)) return;
-        index[at] = (int)t;
-        lse2[at] = l * kLog2e;
-        ratio[at] = top > 0.0f ? grad / top * top_operand : grad;
-        place_target[at++] = (int)y;
+        if (out) listed[at] = (int)t;
+        if (writes) {
+            index[at] = (int)t;
+            lse2[at] = l * kLog2e;
+            ratio[at] = top > 0.0f ? grad / top * top_operand : grad;
+            place_target[at] = (int)y;
+        }
+        ++at;
     };
 #pragma unroll
     for (int k = 0; k < kKept; ++k)
         if (t0 + k < t1) put(t0 + k, kept_y[k], kept_g[k], kept_lse[k]);
     for (long long t = t0 + kKept; t < t1; ++t) put(t, target[t], grad_loss[t], lse[t]);
-    for (long long i = all + threadIdx.x; i < rows; i += kPlaceThreads) {  // rows that fill the last tile
-        lse2[i] = ratio[i] = 0.0f;
-        place_target[i] = -1;
+    if (writes) {
+        for (long long i = all + threadIdx.x; i < rows; i += kPlaceThreads) {  // rows that fill the last tile
+            lse2[i] = ratio[i] = 0.0f;
+            place_target[i] = -1;
+        }
+        if (threadIdx.x == 0) {
+            record->count = all;
+            record->factor = top / top_operand;
+        }
     }
-    if (threadIdx.x == 0) {
-        record->count = all;
-        record->factor = top / top_operand;
-    }
-}
-
-constexpr int kCopyThreads = 128;
-
-// hidden states of the counted tokens, then zeros up to whole blocks of K;
-// nothing where every token counts
-__global__ void __launch_bounds__(kCopyThreads)
-loss_compact(const uint4 *__restrict__ hidden, long long stride, const LossRecord *record, const int *__restrict__ index,
-             long long tokens, int vecs, uint4 *out) {
-    pdl_enter();
-    const long long count = record->count;
-    if (count == tokens) return;
-    const long long end = (count + kTileK - 1) / kTileK * kTileK < tokens ? (count + kTileK - 1) / kTileK * kTileK : tokens;
-    for (long long i = blockIdx.x; i < end; i += gridDim.x) {
-        const uint4 *src = i < count ? hidden + index[i] * stride : nullptr;
-        for (int v = threadIdx.x; v < vecs; v += kCopyThreads)
-            out[i * vecs + v] = src ? src[v] : make_uint4(0u, 0u, 0u, 0u);
-    }
+    if (!out || all == tokens) return;
+    __syncthreads();
+    copy_rows(hidden, stride, listed, all, tokens, vecs, out);
 }
 
 // grad_hidden of a token: the partial sums in order, rounded once
@@ -1353,14 +1374,19 @@ cudaError_t backward_impl(const LossArgs &a, cudaStream_t stream) {
     p.place_target = place_target;
     p.status = a.status;
     p.wait_cycles = g_wait_cycles.load();
-    cudaError_t e = launch_pdl(loss_place, dim3(1), dim3(kPlaceThreads), 0, stream, a.target, (long long)a.ignore,
-                               (long long)a.tokens, (long long)l.rows, (long long)a.vocab, (const float *)a.lse, a.grad_loss,
-                               operand_top(BF16), record, index, place, lse2, ratio, place_target, a.status);
+    const bool joint = a.tokens <= kFewPlaces;
     const int copies = (int)std::min<int64_t>(a.tokens, 8 * sm_count());
-    if (e == cudaSuccess)
-        e = launch_pdl(loss_compact, dim3((unsigned)copies), dim3(kCopyThreads), 0, stream, static_cast<const uint4 *>(a.hidden),
-                       (long long)(a.hidden_stride / 8), (const LossRecord *)record, (const int *)index, (long long)a.tokens,
-                       a.dim / 8, static_cast<uint4 *>(compact));
+    const uint4 *rows = static_cast<const uint4 *>(a.hidden);
+    const long long stride = a.hidden_stride / 8;
+    cudaError_t e = launch_pdl(loss_place, dim3(joint ? (unsigned)std::min<int64_t>(a.tokens, sm_count()) : 1u), dim3(kPlaceThreads),
+                               0, stream, a.target, (long long)a.ignore, (long long)a.tokens, (long long)l.rows,
+                               (long long)a.vocab, (const float *)a.lse, a.grad_loss, operand_top(BF16), record, index, place,
+                               lse2, ratio, place_target, a.status, rows, stride, a.dim / 8,
+                               joint ? static_cast<uint4 *>(compact) : nullptr);
+    if (e == cudaSuccess && !joint)
+        e = launch_pdl(loss_compact, dim3((unsigned)copies), dim3(kCopyThreads), 0, stream, rows, stride,
+                       (const LossRecord *)record, (const int *)index, (long long)a.tokens, a.dim / 8,
+                       static_cast<uint4 *>(compact));
     const int64_t row_tiles = l.rows / kTileM, dim_tiles = up(a.dim, kTileN) / kTileN, piece_tiles = l.piece / kTileN;
     for (int i = 0; i < l.pieces && e == cudaSuccess; ++i) {
         p.piece0 = i * l.piece;
