@@ -358,6 +358,49 @@ def test_loss_ignored_tokens(t, d, v, ignored):
     check_loss(h, w, y2, g, ignore=7)
 
 
+@pytest.mark.parametrize("t", [4095, 4096, 4097, 5121, 9001])
+@pytest.mark.parametrize("ignored", [0.3, 0.999, 0.0])
+def test_loss_many_tokens_some_ignored(t, ignored):
+    """The counted tokens are copied by the launch that finds them up to 4096 tokens, and by another beyond."""
+    check_loss(*case(t, 72, 300, BF, ignored, 8))
+
+
+@pytest.mark.parametrize("t,counted", [(1, 1), (2, 1), (3, 3), (7, 7), (31, 31), (32, 32), (33, 32), (40, 5), (63, 32), (64, 32),
+                                       (65, 2), (300, 9), (4096, 32), (4097, 1), (5000, 30)])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_loss_few_counted_tokens_round_gradients_once(t, counted, dtype):
+    """One slope is most of such a gradient: its rounding to 16 bits must not be the gradient's error.
+
+    The bound: the gradients' relative error (in norm) is that of rounding the exact ones once, e, but for the
+    logits' error.  72 products are five steps of the tensor core, each at most 2^-22 off of sums of magnitudes
+    up to about 2^6 here: 8e-5 at the worst and for all at once, a tenth of it in norm over entries whose errors
+    differ.  So 1.05 e + 1e-5; with slopes rounded to 16 bits one token's error is about 1.4 e.
+    """
+    d, v = 72, 700
+    total = torch.zeros(4, dtype=torch.float64)
+    for key in range(8):
+        gen = seeded(t, counted, key)
+        w = rows_of(gen, v, d, dtype, 0.05)
+        y = torch.randint(0, v, (t,), generator=gen, device="cuda")
+        above = 8.0 * torch.rand(t, 1, generator=gen, device="cuda")   # targets that are likely, to a different extent
+        h = (torch.randn(t, d, generator=gen, device="cuda") + above * w[y].float() / (0.05 ** 2 * d)).to(dtype)
+        g = 0.5 + torch.rand(t, generator=gen, device="cuda")
+        keep = torch.zeros(t, dtype=torch.bool, device="cuda")
+        keep[torch.randperm(t, generator=gen, device="cuda")[:counted]] = True
+        y = torch.where(keep, y, -100)
+        z, lse64, _, counts, at = loss64(h, w, y)
+        q = torch.exp(z - lse64[:, None])
+        q[torch.arange(t, device="cuda"), at] -= 1.0
+        q *= torch.where(counts, g, 0.0).double()[:, None]
+        gh, gw = Z.linear_loss_backward(h, w, y, Z.linear_loss(h, w, y)[1], g)
+        for i, (got, ref) in enumerate(((gh, q @ w.double()), (gw, q.t() @ h.double()))):
+            total[2 * i] += ((got.double() - ref).norm() / ref.norm()).item() / 8
+            total[2 * i + 1] += ((ref.to(dtype).double() - ref).norm() / ref.norm()).item() / 8
+        assert (gh[~keep] == 0).all()
+    Z.check_losses()
+    assert total[0] <= 1.05 * total[1] + 1e-5 and total[2] <= 1.05 * total[3] + 1e-5, total
+
+
 def test_loss_more_than_one_piece():
     """So many tokens that the slopes take the vocabulary in pieces."""
     t, d, v = 3100, 64, 50257

@@ -61,7 +61,7 @@ constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kResultWarps * kStoreB
 // towards zero: a logit of 15 over 4096 products came out 6e-5 too small, a
 // relative 4e-6 where float addition has 4e-8.  The losses are float, so the
 // statistics take the sum off after at most kChunk blocks (512 products) and add it up
-// in registers, rounded to nearest; q is rounded to lp anyway and does without.
+// in registers, rounded to nearest; q, with lp's bits or twice as many, does without.
 constexpr int kChunk = 8;  // whole stages
 constexpr int kTileCost = 4;  // blocks of K that starting and storing a tile cost, about
 constexpr int kTmemColumns = 512;  // two accumulators of 256 columns
@@ -72,8 +72,18 @@ __host__ __device__ constexpr float operand_top(bool bf16) { return bf16 ? 1.0f 
 
 // ------------------------------------------------------------------ workspace
 
+// Rounding q to lp is no matter where many tokens count, but the target's slope of
+// one or a few tokens is most of a gradient, and its rounding then the gradient's
+// error: up to 2.8 times what rounding the result once costs with one token, at most
+// 1.7 with 7 and 1.4 from 17 on (hidden states 392 wide, eight draws each).  So up to
+// this many counted tokens take a second place each, kRest further, whose row holds
+// what the rounding of q in the first left over: twice lp's bits.  The places of both
+// are one block of K and one tile of rows, which fewer tokens would fill as well.
+constexpr int kRest = kTileK / 2;
+
 struct LossRecord {
     int count;     // tokens that count
+    int places;    // rows of the products: as many, or kTileK where each has two
     float factor;  // q in the products' operands times this is q
 };
 
@@ -565,6 +575,18 @@ __device__ __forceinline__ bool any_of(int id, int threads, bool mine) {
     return r != 0;
 }
 
+// what rounding x to the pair w left over: exact; nothing of what is not finite
+template <bool BF16>
+__device__ __forceinline__ float2 left_over(float2 x, uint32_t w) {
+    float2 f;
+    if constexpr (BF16)
+        f = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    else
+        f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    const float2 r = make_float2(x.x - f.x, x.y - f.y);
+    return make_float2(isfinite(r.x) ? r.x : 0.0f, isfinite(r.y) ? r.y : 0.0f);
+}
+
 template <bool BF16, bool STATS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
 loss_products(const __grid_constant__ ProductParams p) {
@@ -604,8 +626,9 @@ loss_products(const __grid_constant__ ProductParams p) {
 
     volatile int *dead = &sh.dead;
     const long long limit = p.wait_cycles;
-    const bool all = p.record == nullptr || p.record->count == p.tokens;
-    const long long count = p.record ? p.record->count : p.tokens;
+    const bool twice = p.record && p.record->places != p.record->count;  // each token has two places
+    const bool all = p.record == nullptr || (p.record->count == p.tokens && !twice);
+    const long long count = p.record ? p.record->places : p.tokens;
     const Work work(p, count);
     Tile t;
 
@@ -819,6 +842,7 @@ loss_products(const __grid_constant__ ProductParams p) {
             const uint32_t acc = tmem + buf * kTileN + ((uint32_t)(quad * 32) << 16);
             if (t.kind == kLogits) {
                 const int place = row0 + lane;
+                const bool rest = twice && row0 == kRest;  // this warp's rows are the second places
                 const float lse2 = p.lse2[place], ratio = p.ratio[place];
                 const bool live = p.place_target[place] >= 0;  // not a row that fills the last tile
                 const int y = p.place_target[place] - (int)p.piece0 - t.n0;
@@ -847,6 +871,10 @@ loss_products(const __grid_constant__ ProductParams p) {
                     for (int j = 0; j < 16; ++j) {
                         const float2 x = mul2(make_float2(z[2 * j], z[2 * j + 1]), make_float2(ratio, ratio));
                         w[j] = pack_lp<BF16>(x.x, x.y);
+                        if (rest) {
+                            const float2 r = left_over<BF16>(x, w[j]);
+                            w[j] = pack_lp<BF16>(r.x, r.y);
+                        }
                     }
                 };
                 for (int c = first; c < first + kResultColumns; c += 64) {
@@ -1076,13 +1104,18 @@ loss_few(const uint4 *__restrict__ hidden, long long hidden_stride, const uint4 
 
 constexpr int kCopyThreads = 128;
 
-// hidden states of the counted tokens, then zeros up to whole blocks of K
+// Hidden states of the counted tokens by place, and zeros up to whole blocks of K: the
+// products' maps of them have this many rows.
+__host__ __device__ constexpr long long compact_rows(long long tokens) { return tokens < kTileK ? kTileK : tokens; }
+
 __device__ __forceinline__ void copy_rows(const uint4 *__restrict__ hidden, long long stride, const int *index, long long count,
-                                          long long tokens, int vecs, uint4 *out) {
-    const long long whole = (count + kTileK - 1) / kTileK * kTileK, end = whole < tokens ? whole : tokens;
+                                          long long places, long long tokens, int vecs, uint4 *out) {
+    const long long whole = (places + kTileK - 1) / kTileK * kTileK, limit = compact_rows(tokens);
+    const long long end = whole < limit ? whole : limit;
     const int each = (int)blockDim.x / kCopyThreads;  // rows of a block at a time
     for (long long i = (long long)blockIdx.x * each + threadIdx.x / kCopyThreads; i < end; i += (long long)gridDim.x * each) {
-        const uint4 *src = i < count ? hidden + index[i] * stride : nullptr;
+        const long long n = places != count && i >= kRest ? i - kRest : i;
+        const uint4 *src = n < count ? hidden + index[n] * stride : nullptr;
         for (int v = threadIdx.x % kCopyThreads; v < vecs; v += kCopyThreads)
             out[i * vecs + v] = src ? src[v] : make_uint4(0u, 0u, 0u, 0u);
     }
@@ -1094,7 +1127,7 @@ loss_compact(const uint4 *__restrict__ hidden, long long stride, const LossRecor
              long long tokens, int vecs, uint4 *out) {
     pdl_enter();
     const long long count = record->count;
-    if (count < tokens) copy_rows(hidden, stride, index, count, tokens, vecs, out);
+    if (count < tokens) copy_rows(hidden, stride, index, count, record->places, tokens, vecs, out);
 }
 
 constexpr int kPlaceThreads = 1024;
@@ -1162,6 +1195,7 @@ loss_place(const int64_t *__restrict__ target, long long ignore, long long token
         all += sums[w];
         top = fmaxf(top, tops[w]);
     }
+    const int places = all > 0 && all <= kRest ? kTileK : all;
     int at = before - mine;
     const auto put = [&](long long t, long long y, float grad, float l) {
         if (writes) place[t] = counts(y) ? at : -1;
@@ -1169,9 +1203,11 @@ loss_place(const int64_t *__restrict__ target, long long ignore, long long token
         if (out) listed[at] = (int)t;
         if (writes) {
             index[at] = (int)t;
-            lse2[at] = l * kLog2e;
-            ratio[at] = top > 0.0f ? grad / top * top_operand : grad;
-            place_target[at] = (int)y;
+            for (int i = at; i < places; i += places == all ? places : kRest) {
+                lse2[i] = l * kLog2e;
+                ratio[i] = top > 0.0f ? grad / top * top_operand : grad;
+                place_target[i] = (int)y;
+            }
         }
         ++at;
     };
@@ -1181,31 +1217,35 @@ loss_place(const int64_t *__restrict__ target, long long ignore, long long token
     for (long long t = t0 + kKept; t < t1; ++t) put(t, target[t], grad_loss[t], lse[t]);
     if (writes) {
         for (long long i = all + threadIdx.x; i < rows; i += kPlaceThreads) {  // rows that fill the last tile
+            if (places != all && i >= kRest && i < kRest + all) continue;
             lse2[i] = ratio[i] = 0.0f;
             place_target[i] = -1;
         }
         if (threadIdx.x == 0) {
             record->count = all;
+            record->places = places;
             record->factor = top / top_operand;
         }
     }
-    if (!out || all == tokens) return;
+    if (!out || (all == tokens && places == all)) return;
     __syncthreads();
-    copy_rows(hidden, stride, listed, all, tokens, vecs, out);
+    copy_rows(hidden, stride, listed, all, places, tokens, vecs, out);
 }
 
-// grad_hidden of a token: the partial sums in order, rounded once
+// grad_hidden of a token: the partial sums of its place, or of both, in order, rounded once
 template <bool BF16>
 __global__ void __launch_bounds__(kCopyThreads)
-loss_finish(const float4 *__restrict__ sums, const int *__restrict__ place, long long tokens, long long rows, int splits,
-            int vecs, uint4 *out, long long stride) {
+loss_finish(const float4 *__restrict__ sums, const int *__restrict__ place, const LossRecord *record, long long tokens,
+            long long rows, int splits, int vecs, uint4 *out, long long stride) {
     pdl_enter();
+    const int each = record->places != record->count ? 2 : 1;
     for (long long t = blockIdx.x; t < tokens; t += gridDim.x) {
         const int i = place[t];
         for (int v = threadIdx.x; v < vecs; v += kCopyThreads) {
             float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
-            for (int s = 0; s < splits && i >= 0; ++s) {
-                const float4 *src = sums + ((s * rows + i) * vecs + v) * 2;
+            for (int n = 0; n < splits * each && i >= 0; ++n) {
+                const int s = n < splits ? n : n - splits;
+                const float4 *src = sums + ((s * rows + (n < splits ? i : i + kRest)) * vecs + v) * 2;
                 const float4 a = src[0], b = src[1];
                 lo.x += a.x; lo.y += a.y; lo.z += a.z; lo.w += a.w;
                 hi.x += b.x; hi.y += b.y; hi.z += b.z; hi.w += b.w;
@@ -1353,11 +1393,11 @@ cudaError_t backward_impl(const LossArgs &a, cudaStream_t stream) {
     float *sums = reinterpret_cast<float *>(ws + l.sums);
     ProductParams p = {};
     if (!encoder() || !make_map(&p.h_k, a.hidden, a.tokens, a.dim, a.hidden_stride, a.lp, false, kHalf) ||
-        !make_map(&p.hc_k, compact, a.tokens, a.dim, a.dim, a.lp, false, kHalf) ||
+        !make_map(&p.hc_k, compact, compact_rows(a.tokens), a.dim, a.dim, a.lp, false, kHalf) ||
         !make_map(&p.w_k, a.weight, a.vocab, a.dim, a.weight_stride, a.lp, false, kHalf) ||
         !make_map(&p.w_mn, a.weight, a.vocab, a.dim, a.weight_stride, a.lp, false, kTileK) ||
         !make_map(&p.h_mn, a.hidden, a.tokens, a.dim, a.hidden_stride, a.lp, false, kTileK) ||
-        !make_map(&p.hc_mn, compact, a.tokens, a.dim, a.dim, a.lp, false, kTileK) ||
+        !make_map(&p.hc_mn, compact, compact_rows(a.tokens), a.dim, a.dim, a.lp, false, kTileK) ||
         !make_map(&p.q_k, slopes, l.rows, l.piece, l.piece, a.lp, false, kHalf) ||
         !make_map(&p.q_mn, slopes, l.rows, l.piece, l.piece, a.lp, false, kTileK) ||
         !make_map(&p.q_out, slopes, l.rows, l.piece, l.piece, a.lp, false, 32) ||
@@ -1380,11 +1420,13 @@ cudaError_t backward_impl(const LossArgs &a, cudaStream_t stream) {
     const int copies = (int)std::min<int64_t>(a.tokens, 8 * sm_count());
     const uint4 *rows = static_cast<const uint4 *>(a.hidden);
     const long long stride = a.hidden_stride / 8;
-    cudaError_t e = launch_pdl(loss_place, dim3(joint ? (unsigned)std::min<int64_t>(a.tokens, sm_count()) : 1u), dim3(kPlaceThreads),
-                               0, stream, a.target, (long long)a.ignore, (long long)a.tokens, (long long)l.rows,
-                               (long long)a.vocab, (const float *)a.lse, a.grad_loss, operand_top(BF16), record, index, place,
-                               lse2, ratio, place_target, a.status, rows, stride, a.dim / 8,
-                               joint ? static_cast<uint4 *>(compact) : nullptr);
+    // each block copies some rows at a time, of a block of K at least
+    const int64_t few_blocks = kTileK / (kPlaceThreads / kCopyThreads);
+    const int64_t blocks = joint ? std::min<int64_t>(std::max(a.tokens, few_blocks), sm_count()) : 1;
+    cudaError_t e = launch_pdl(loss_place, dim3((unsigned)blocks), dim3(kPlaceThreads), 0, stream, a.target, (long long)a.ignore,
+                               (long long)a.tokens, (long long)l.rows, (long long)a.vocab, (const float *)a.lse, a.grad_loss,
+                               operand_top(BF16), record, index, place, lse2, ratio, place_target, a.status, rows, stride,
+                               a.dim / 8, joint ? static_cast<uint4 *>(compact) : nullptr);
     if (e == cudaSuccess && !joint)
         e = launch_pdl(loss_compact, dim3((unsigned)copies), dim3(kCopyThreads), 0, stream, rows, stride,
                        (const LossRecord *)record, (const int *)index, (long long)a.tokens, a.dim / 8,
@@ -1400,7 +1442,7 @@ cudaError_t backward_impl(const LossArgs &a, cudaStream_t stream) {
     }
     if (e == cudaSuccess)
         e = launch_pdl(loss_finish<BF16>, dim3((unsigned)copies), dim3(kCopyThreads), 0, stream, reinterpret_cast<const float4 *>(sums),
-                       (const int *)place, (long long)a.tokens, (long long)l.rows, l.splits, a.dim / 8,
+                       (const int *)place, (const LossRecord *)record, (long long)a.tokens, (long long)l.rows, l.splits, a.dim / 8,
                        static_cast<uint4 *>(a.grad_hidden), (long long)(a.grad_hidden_stride / 8));
     return e;
 }
