@@ -871,10 +871,14 @@ loss_products(const __grid_constant__ ProductParams p) {
                     for (int j = 0; j < 16; ++j) {
                         const float2 x = mul2(make_float2(z[2 * j], z[2 * j + 1]), make_float2(ratio, ratio));
                         w[j] = pack_lp<BF16>(x.x, x.y);
-                        if (rest) {
-                            const float2 r = left_over<BF16>(x, w[j]);
-                            w[j] = pack_lp<BF16>(r.x, r.y);
-                        }
+                        z[2 * j] = x.x;
+                        z[2 * j + 1] = x.y;
+                    }
+                    if (!rest) return;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float2 r = left_over<BF16>(make_float2(z[2 * j], z[2 * j + 1]), w[j]);
+                        w[j] = pack_lp<BF16>(r.x, r.y);
                     }
                 };
                 for (int c = first; c < first + kResultColumns; c += 64) {
