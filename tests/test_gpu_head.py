@@ -401,6 +401,35 @@ def test_loss_few_counted_tokens_round_gradients_once(t, counted, dtype):
     assert total[0] <= 1.05 * total[1] + 1e-5 and total[2] <= 1.05 * total[3] + 1e-5, total
 
 
+@pytest.mark.parametrize("t,d,v", [(1, 4096, 500), (3, 536, 821), (4, 4096, 500), (5, 4096, 500), (40, 4096, 700), (300, 2056, 700)])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_loss_slopes_of_likely_targets(t, d, v, dtype):
+    """A target of probability 0.999 has a slope of 0.001: what its logit and lse are off counts a thousandfold.
+
+    The bound on a slope: up to four tokens float sums in lanes, 2^-22 of the logit for it, lse and their rounding
+    each; beyond, lse comes from parts of up to 512 products, 34 steps of at most 2^-23.  Besides, the rounding of
+    the slopes and of the result, each as large as e, that of the exact gradients.
+    """
+    gen = seeded(t, d, v)
+    w = rows_of(gen, v, d, dtype, 0.05)
+    y = torch.randint(0, v, (t,), generator=gen, device="cuda")
+    high = math.log(v) + 6.9
+    h = (0.2 * torch.randn(t, d, generator=gen, device="cuda") + high * w[y].float() / w[y].float().square().sum(1, keepdim=True)).to(dtype)
+    g = torch.ones(t, device="cuda")
+    z, lse64, _, counts, at = loss64(h, w, y)
+    q = torch.exp(z - lse64[:, None])
+    rows = torch.arange(t, device="cuda")
+    q[rows, y] = torch.expm1(z[rows, y] - lse64)
+    off = (3 * 2.0 ** -22 if t <= 4 else 34 * 2.0 ** -23) * high
+    gh, gw = Z.linear_loss_backward(h, w, y, Z.linear_loss(h, w, y)[1], g)
+    Z.check_losses()
+    for got, ref in ((gh, q @ w.double()), (gw, q.t() @ h.double())):
+        e = ((ref.to(dtype).double() - ref).norm() / ref.norm()).item()
+        room = 2.1 * e + off * t ** 0.5 / q[rows, y].norm().item()
+        err = ((got.double() - ref).norm() / ref.norm()).item()
+        assert err <= room, (err, room)
+
+
 def test_loss_more_than_one_piece():
     """So many tokens that the slopes take the vocabulary in pieces."""
     t, d, v = 3100, 64, 50257

@@ -92,7 +92,7 @@ struct BackwardLayout {
     int64_t piece;     // columns of a piece of the vocabulary (whole tiles)
     int pieces;
     int splits;        // partial sums of grad_hidden
-    int64_t index, place, lse2, ratio, target, hidden, slopes, sums, bytes;  // byte offsets
+    int64_t index, place, lse2, ratio, target, at_target, hidden, slopes, sums, bytes;  // byte offsets
 };
 
 constexpr int kPairs = 76;  // of SMs
@@ -131,6 +131,7 @@ BackwardLayout backward_layout(int64_t tokens, int64_t vocab, int dim) {
     l.lse2 = take(l.rows * 4);
     l.ratio = take(l.rows * 4);
     l.target = take(l.rows * 4);
+    l.at_target = take(l.rows * 4);
     l.hidden = take(l.rows * dim * 2);
     l.slopes = take(l.rows * l.piece * 2);
     l.sums = take(l.splits * l.rows * dim * 4);
@@ -353,7 +354,7 @@ struct ProductParams {
     float2 *parts;  // [tile of the vocabulary][token]
     float *picked;  // the target's logit
     // q, by place among the counted tokens
-    const float *lse2, *ratio;
+    const float *lse2, *ratio, *at_target;
     const int *place_target;
     int *status;
     long long wait_cycles;
@@ -843,7 +844,7 @@ loss_products(const __grid_constant__ ProductParams p) {
             if (t.kind == kLogits) {
                 const int place = row0 + lane;
                 const bool rest = twice && row0 == kRest;  // this warp's rows are the second places
-                const float lse2 = p.lse2[place], ratio = p.ratio[place];
+                const float lse2 = p.lse2[place], ratio = p.ratio[place], at_target = p.at_target[place];
                 const bool live = p.place_target[place] >= 0;  // not a row that fills the last tile
                 const int y = p.place_target[place] - (int)p.piece0 - t.n0;
                 const long long left = p.vocab - p.piece0 - (long long)t.n0;
@@ -860,7 +861,7 @@ loss_products(const __grid_constant__ ProductParams p) {
                     const uint32_t hit = y >= col && y < col + 32 ? 1u << (y - col) : 0u;
                     if (__any_sync(0xffffffffu, hit != 0u)) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) z[j] = hit >> j & 1u ? z[j] - 1.0f : z[j];
+                        for (int j = 0; j < 32; ++j) z[j] = hit >> j & 1u ? at_target : z[j];
                     }
                     const long long keep = live ? left - col : 0;  // columns that exist, in a row that counts
                     if (keep < 32) {
@@ -1110,28 +1111,61 @@ constexpr int kCopyThreads = 128;
 
 // Hidden states of the counted tokens by place, and zeros up to whole blocks of K: the
 // products' maps of them have this many rows.
+struct RowSource {
+    const uint4 *hidden, *weight;
+    long long stride, weight_stride;
+    const int64_t *target;
+    const float *lse;
+    long long tokens;
+    int vecs;
+};
+
 __host__ __device__ constexpr long long compact_rows(long long tokens) { return tokens < kTileK ? kTileK : tokens; }
 
-__device__ __forceinline__ void copy_rows(const uint4 *__restrict__ hidden, long long stride, const int *index, long long count,
-                                          long long places, long long tokens, int vecs, uint4 *out) {
-    const long long whole = (places + kTileK - 1) / kTileK * kTileK, limit = compact_rows(tokens);
-    const long long end = whole < limit ? whole : limit;
-    const int each = (int)blockDim.x / kCopyThreads;  // rows of a block at a time
-    for (long long i = (long long)blockIdx.x * each + threadIdx.x / kCopyThreads; i < end; i += (long long)gridDim.x * each) {
+// A warp takes a place: it copies the hidden state (out, not NULL) and computes the
+// target's slope from the target's logit in float.  The tensor core's logit is low by
+// up to 2^-23 of itself for every 16 products, and exp(z - lse) - 1 of a likely target
+// has nothing left beside that: gradients of targets of probability 0.999 were 3 %
+// off with 40 tokens, 4096 wide, and 12 % with five.  (1 % of the time of both passes:
+// 1023 x 768 240 -> 243 us, 2048 x 1600 934 -> 942, 4096 x 4096 4.32 -> 4.36 ms.)
+template <bool BF16>
+__device__ __forceinline__ void take_rows(const RowSource &r, const int *index, long long count, long long places, uint4 *out,
+                                          float *at_target) {
+    const int lane = threadIdx.x & 31, warps = (int)blockDim.x / 32;
+    const long long whole = (places + kTileK - 1) / kTileK * kTileK, limit = compact_rows(r.tokens);
+    const long long end = !out ? count : whole < limit ? whole : limit;
+    for (long long i = (long long)(threadIdx.x / 32) * gridDim.x + blockIdx.x; i < end; i += (long long)gridDim.x * warps) {
         const long long n = places != count && i >= kRest ? i - kRest : i;
-        const uint4 *src = n < count ? hidden + index[n] * stride : nullptr;
-        for (int v = threadIdx.x % kCopyThreads; v < vecs; v += kCopyThreads)
-            out[i * vecs + v] = src ? src[v] : make_uint4(0u, 0u, 0u, 0u);
+        if (n >= count) {
+            for (int v = lane; v < r.vecs; v += 32) out[i * r.vecs + v] = make_uint4(0u, 0u, 0u, 0u);
+            continue;
+        }
+        const long long t = index[n], y = r.target[t];
+        const uint4 *h = r.hidden + t * r.stride, *w = r.weight + y * r.weight_stride;
+        float sum[2] = {0.0f, 0.0f};
+#pragma unroll 4
+        for (int v = lane; v < r.vecs; v += 32) {
+            const uint4 x = h[v], m = w[v];
+            if (out) out[i * r.vecs + v] = x;
+            float a[8], b[8];
+            widen8<BF16>(x, a);
+            widen8<BF16>(m, b);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sum[k & 1] = __fmaf_rn(a[k], b[k], sum[k & 1]);
+        }
+        float z = sum[0] + sum[1];
+        for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+        if (lane == 0) at_target[i] = expm1f(z - r.lse[t]);
     }
 }
 
-// the same after loss_place; nothing where every token counts
+// the same after loss_place
+template <bool BF16>
 __global__ void __launch_bounds__(kCopyThreads)
-loss_compact(const uint4 *__restrict__ hidden, long long stride, const LossRecord *record, const int *__restrict__ index,
-             long long tokens, int vecs, uint4 *out) {
+loss_rows(const __grid_constant__ RowSource r, const LossRecord *record, const int *__restrict__ index, uint4 *out, float *at_target) {
     pdl_enter();
-    const long long count = record->count;
-    if (count < tokens) copy_rows(hidden, stride, index, count, record->places, tokens, vecs, out);
+    const long long count = record->count, places = record->places;
+    take_rows<BF16>(r, index, count, places, count < r.tokens || places != count ? out : nullptr, at_target);
 }
 
 constexpr int kPlaceThreads = 1024;
@@ -1142,16 +1176,17 @@ constexpr int kFewPlaces = kKept * kPlaceThreads;  // tokens up to which blocks 
 // The counted tokens in order (index: token of a place; place: place of a token
 // or -1), what the slopes need of each, and the largest finite |grad_loss|.
 // A thread takes consecutive tokens.  One block; or, up to kFewPlaces tokens, as many
-// as copy the hidden states of the counted ones (out, not NULL; see loss_compact):
-// each finds every place for itself, which saves a launch (1023 tokens x 768: 6.4 us
-// and not 8.6, 4096 x 4096 16 and not 20), and the first writes them down.  A call by
-// itself gains 3 us of 275 with 1023 tokens x 768 and 17 of 991 with 2048 x 1600; calls
-// that follow one another, whose launches hide behind the products, take the same time.
+// as then take the rows of the counted ones (out, not NULL; see loss_rows): each finds
+// every place for itself, which saves a launch, and the first writes them down.
+template <bool BF16>
 __global__ void __launch_bounds__(kPlaceThreads)
-loss_place(const int64_t *__restrict__ target, long long ignore, long long tokens, long long rows, long long vocab,
-           const float *__restrict__ lse, const float *__restrict__ grad_loss, float top_operand, LossRecord *record,
-           int *index, int *place, float *lse2, float *ratio, int *place_target, int *status,
-           const uint4 *__restrict__ hidden, long long stride, int vecs, uint4 *out) {
+loss_place(const __grid_constant__ RowSource r, long long ignore, long long rows, long long vocab, const float *__restrict__ grad_loss,
+           LossRecord *record, int *index, int *place, float *lse2, float *ratio, int *place_target, int *status, uint4 *out,
+           float *at_target) {
+    constexpr float top_operand = operand_top(BF16);
+    const int64_t *__restrict__ target = r.target;
+    const float *__restrict__ lse = r.lse;
+    const long long tokens = r.tokens;
     pdl_enter();
     __shared__ int sums[kPlaceThreads / 32];
     __shared__ float tops[kPlaceThreads / 32];
@@ -1231,9 +1266,9 @@ loss_place(const int64_t *__restrict__ target, long long ignore, long long token
             record->factor = top / top_operand;
         }
     }
-    if (!out || (all == tokens && places == all)) return;
+    if (!out) return;
     __syncthreads();
-    copy_rows(hidden, stride, listed, all, places, tokens, vecs, out);
+    take_rows<BF16>(r, listed, all, places, all < tokens || places != all ? out : nullptr, at_target);
 }
 
 // grad_hidden of a token: the partial sums of its place, or of both, in order, rounded once
@@ -1393,6 +1428,7 @@ cudaError_t backward_impl(const LossArgs &a, cudaStream_t stream) {
     int *index = reinterpret_cast<int *>(ws + l.index), *place = reinterpret_cast<int *>(ws + l.place);
     float *lse2 = reinterpret_cast<float *>(ws + l.lse2), *ratio = reinterpret_cast<float *>(ws + l.ratio);
     int *place_target = reinterpret_cast<int *>(ws + l.target);
+    float *at_target = reinterpret_cast<float *>(ws + l.at_target);
     void *compact = ws + l.hidden, *slopes = ws + l.slopes;
     float *sums = reinterpret_cast<float *>(ws + l.sums);
     ProductParams p = {};
@@ -1417,24 +1453,29 @@ cudaError_t backward_impl(const LossArgs &a, cudaStream_t stream) {
     p.record = record;
     p.lse2 = lse2;
     p.ratio = ratio;
+    p.at_target = at_target;
     p.place_target = place_target;
     p.status = a.status;
     p.wait_cycles = g_wait_cycles.load();
     const bool joint = a.tokens <= kFewPlaces;
     const int copies = (int)std::min<int64_t>(a.tokens, 8 * sm_count());
-    const uint4 *rows = static_cast<const uint4 *>(a.hidden);
-    const long long stride = a.hidden_stride / 8;
-    // each block copies some rows at a time, of a block of K at least
-    const int64_t few_blocks = kTileK / (kPlaceThreads / kCopyThreads);
-    const int64_t blocks = joint ? std::min<int64_t>(std::max(a.tokens, few_blocks), sm_count()) : 1;
-    cudaError_t e = launch_pdl(loss_place, dim3((unsigned)blocks), dim3(kPlaceThreads), 0, stream, a.target, (long long)a.ignore,
-                               (long long)a.tokens, (long long)l.rows, (long long)a.vocab, (const float *)a.lse, a.grad_loss,
-                               operand_top(BF16), record, index, place, lse2, ratio, place_target, a.status, rows, stride,
-                               a.dim / 8, joint ? static_cast<uint4 *>(compact) : nullptr);
+    RowSource r;
+    r.hidden = static_cast<const uint4 *>(a.hidden);
+    r.weight = static_cast<const uint4 *>(a.weight);
+    r.stride = a.hidden_stride / 8;
+    r.weight_stride = a.weight_stride / 8;
+    r.target = a.target;
+    r.lse = a.lse;
+    r.tokens = a.tokens;
+    r.vecs = a.dim / 8;
+    // a warp for each place, of a block of K at least
+    const int64_t blocks = joint ? std::min<int64_t>(std::max<int64_t>(a.tokens, kTileK), sm_count()) : 1;
+    cudaError_t e = launch_pdl(loss_place<BF16>, dim3((unsigned)blocks), dim3(kPlaceThreads), 0, stream, r, (long long)a.ignore,
+                               (long long)l.rows, (long long)a.vocab, (const float *)a.grad_loss, record, index, place, lse2, ratio,
+                               place_target, a.status, joint ? static_cast<uint4 *>(compact) : nullptr, at_target);
     if (e == cudaSuccess && !joint)
-        e = launch_pdl(loss_compact, dim3((unsigned)copies), dim3(kCopyThreads), 0, stream, rows, stride,
-                       (const LossRecord *)record, (const int *)index, (long long)a.tokens, a.dim / 8,
-                       static_cast<uint4 *>(compact));
+        e = launch_pdl(loss_rows<BF16>, dim3((unsigned)copies), dim3(kCopyThreads), 0, stream, r, (const LossRecord *)record,
+                       (const int *)index, static_cast<uint4 *>(compact), at_target);
     const int64_t row_tiles = l.rows / kTileM, dim_tiles = up(a.dim, kTileN) / kTileN, piece_tiles = l.piece / kTileN;
     for (int i = 0; i < l.pieces && e == cudaSuccess; ++i) {
         p.piece0 = i * l.piece;
