@@ -60,9 +60,14 @@ constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kResultWarps * kStoreB
 // The tensor core's float sum drops the low bits of every step of 16, always
 // towards zero: a logit of 15 over 4096 products came out 6e-5 too small, a
 // relative 4e-6 where float addition has 4e-8.  The losses are float, so the
-// statistics take the sum off after at most kChunk blocks (512 products) and add it up
+// statistics take the sum off after at most 512 products (kChunk blocks) and add it up
 // in registers, rounded to nearest; q, with lp's bits or twice as many, does without.
 constexpr int kChunk = 8;  // whole stages
+// Half as many where no pair has a second tile, whose product the parts' results would
+// hold up: half the error (163 x 328 x 373: lse 1.0e-6 relative, 6e-7 so) for 0 to 14 % of
+// time (200 x 4096 x 5000 25.1 -> 28.6 us, 500 x 1600 x 8000 16.4 -> 17.6, smaller ones the
+// same); with ten tiles a pair (1023 x 768 x 50257) it took 69 us and not 55.
+constexpr int kShortChunk = 4;
 constexpr int kTileCost = 4;  // blocks of K that starting and storing a tile cost, about
 constexpr int kTmemColumns = 512;  // two accumulators of 256 columns
 
@@ -353,6 +358,7 @@ struct ProductParams {
     const int64_t *target;
     float2 *parts;  // [tile of the vocabulary][token]
     float *picked;  // the target's logit
+    int chunk;      // blocks of K that the tensor core adds up, whole stages
     // q, by place among the counted tokens
     const float *lse2, *ratio, *at_target;
     const int *place_target;
@@ -370,9 +376,9 @@ struct Tile {
     int n;        // its number along the columns
 };
 
-// The statistics' sums: parts of at most kChunk blocks of K, as even as can be (a
+// The statistics' sums: parts of at most p.chunk blocks of K, as even as can be (a
 // short last part would have the tensor core wait for its accumulator).
-__device__ __forceinline__ int chunks_of(int k_blocks) { return (k_blocks + kChunk - 1) / kChunk; }
+__device__ __forceinline__ int chunks_of(int k_blocks, int chunk) { return (k_blocks + chunk - 1) / chunk; }
 
 // Division by a number that stays: the product with 2^32 / d rounded up gives the
 // quotient or one more.  (A plain division took the thread that feeds the tensor
@@ -691,7 +697,7 @@ loss_products(const __grid_constant__ ProductParams p) {
             // tile with its descriptors (after, feed).
             bool ok = true, ready = false, vacant = false;
             const int stages = (work.logits.k_blocks + kStageBlocks - 1) / kStageBlocks;  // statistics: of every tile
-            const int chunks = STATS ? chunks_of(work.logits.k_blocks) : 1;
+            const int chunks = STATS ? chunks_of(work.logits.k_blocks, p.chunk) : 1;
             const int each = stages / chunks * kStageBlocks, longer = stages % chunks;
             Tile after;
             bool more = work.at(0, t);
@@ -753,6 +759,7 @@ loss_products(const __grid_constant__ ProductParams p) {
         Joined *const joined = reinterpret_cast<Joined *>(smem + kStages * kStageBytes);
         int buf = 0;
         uint32_t acc_phase = 0;
+        const int chunks = chunks_of(work.logits.k_blocks, p.chunk);
         for (int j = 0; work.at(j, t); ++j) {
             const int row = quad * 32 + lane;
             const long long token = (long long)t.m0 + (int)rank * kHalf + row;
@@ -764,7 +771,7 @@ loss_products(const __grid_constant__ ProductParams p) {
 #pragma unroll
             for (int i = 0; i < kResultColumns; ++i) z[i] = 0.0f;
             bool ok = true;
-            for (int c = chunks_of(t.k1 - t.k0); c > 0; --c) {
+            for (int c = chunks; c > 0; --c) {
                 const bool got = wait_for(&sh.acc_full[buf], acc_phase, dead, limit, p.status);
                 ok = __all_sync(0xffffffffu, got);
                 if (!ok) break;
@@ -1412,7 +1419,9 @@ cudaError_t forward_impl(const LossArgs &a, cudaStream_t stream) {
         p.picked = picked;
         p.status = a.status;
         p.wait_cycles = g_wait_cycles.load();
-        e = launch_products<BF16, true>(p, up(a.tokens, kTileM) / kTileM * (up(a.vocab, kTileN) / kTileN), stream);
+        const int64_t tiles = up(a.tokens, kTileM) / kTileM * (up(a.vocab, kTileN) / kTileN);
+        p.chunk = tiles <= pairs_at_once<BF16, true>() ? kShortChunk : kChunk;
+        e = launch_products<BF16, true>(p, tiles, stream);
     }
     if (e != cudaSuccess) return e;
     return launch_pdl(loss_join, dim3((unsigned)((a.tokens + kJoinTokens - 1) / kJoinTokens)),
