@@ -574,8 +574,10 @@ zero_status zero_loss_forward(const void *hidden, int64_t hidden_stride, const v
  * lse: as zero_loss_forward wrote it.  An ignored token's grad_hidden is zero
  * and it adds nothing to grad_weight, whatever its hidden state holds.  The
  * logits are computed again, a piece of the vocabulary at a time; q is rounded
- * to lp for the two products, relative to the largest finite |grad_loss| (so a
- * gradient of any size fits fp16), whose sums are float. */
+ * to lp for the two products (to twice lp's bits where at most 32 tokens count),
+ * relative to the largest finite |grad_loss| (so a gradient of any size fits
+ * fp16), whose sums are float.  The slope at the target is
+ * expm1(z[t][target[t]] - lse[t]) of a logit summed in float. */
 zero_status zero_loss_backward(const void *hidden, int64_t hidden_stride, const void *weight,
                                int64_t weight_stride, const int64_t *target, int64_t ignore,
                                int64_t n_tokens, int64_t vocab, int32_t dim, zero_lp lp,
