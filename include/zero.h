@@ -510,7 +510,9 @@ zero_status zero_norm_forward(const void *x, int64_t x_stride, const void *resid
  * row may be shorter) the codes and scale that zero_quantize_shard documents,
  * taken from the unrounded values s[i] * rstd * weight[i].  format:
  * ZERO_QUANT_INT8 or ZERO_QUANT_FP8_E4M3.  codes: n_rows * dim bytes, scales:
- * n_rows * ceil(dim / ZERO_QUANT_BLOCK) floats, both without row padding. */
+ * n_rows * ceil(dim / ZERO_QUANT_BLOCK) floats, both without row padding.  A
+ * block with a value that is NaN (a NaN or an infinity in the row makes some) has
+ * a NaN scale and codes 0, so that all of it dequantizes to NaN. */
 zero_status zero_norm_forward_quantized(const void *x, int64_t x_stride, const void *residual,
                                         int64_t residual_stride, const void *weight, float eps,
                                         int64_t n_rows, int32_t dim, zero_lp lp, int32_t format,

@@ -54,6 +54,13 @@ __device__ __forceinline__ float row_sum(float v, int warps, float *shared) {
     return v;
 }
 
+// the larger one; NaN where either is (fmaxf gives the other)
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 struct NormShape {
     int vecs;   // vectors of 8 in a row
     int warps;  // that own a row: 1 (kRowsPerBlock rows a block) or all of a block
@@ -117,12 +124,15 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) norm_rows(const NormArgs a,
         } else {
             float top = 0.0f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) top = fmaxf(top, v < sh.vecs ? fabsf(y[k]) : 0.0f);
+            for (int k = 0; k < 8; ++k) top = max_or_nan(top, v < sh.vecs ? fabsf(y[k]) : 0.0f);
 #pragma unroll
-            for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            for (int off = 8; off > 0; off >>= 1) top = max_or_nan(top, __shfl_xor_sync(0xffffffffu, top, off));
             float scale;
             uint32_t codes[2];
-            if constexpr (OUT == kOutFp8) {
+            if (top != top) {  // codes have no NaN (int8), so the block's scale says it
+                scale = top;
+                codes[0] = codes[1] = 0u;
+            } else if constexpr (OUT == kOutFp8) {
                 quant_codes_fp8<8>(y, top, scale, codes);
             } else {
                 scale = __fdiv_rn(top, 127.0f);

@@ -133,7 +133,8 @@ def residual_norm(x, residual, weight, eps, stream=None):
 
 def residual_norm_quantized(x, residual, weight, eps, fmt=A.ZERO_QUANT_INT8, stream=None):
     """(codes, scales, sum): residual_norm's out as int8 or E4M3 codes (one byte
-    each, int8 tensor) with a float scale per block of 128 elements of a row."""
+    each, int8 tensor) with a float scale per block of 128 elements of a row.
+    The scale is NaN, and so all of the block once dequantized, where out has a NaN."""
     rows, dim, xs, rs = _norm_inputs("residual_norm_quantized", x, residual, weight)
     with _on(stream):
         codes = torch.empty((rows, dim), dtype=torch.int8, device=x.device)
