@@ -499,7 +499,10 @@ zero_status zero_memory_report(int64_t psi, int32_t n_ranks, int32_t align,
  *   out[i] = lp(s[i] * rstd * weight[i]),  rstd = (mean(s^2) + eps)^(-1/2)
  *   sum[i] = lp(s[i])          (sum NULL: not written)
  * out is computed from the unrounded s.  weight: dim elements.  sum may be
- * residual or x itself (in place).  eps >= 0 and finite. */
+ * residual or x itself (in place).  eps >= 0 and finite.  s and rstd are floats;
+ * the sum of squares of a row whose squares leave float's range is a double, here
+ * and in the gradients, so a row of finite s has a finite rstd (unless eps is 0 and
+ * the row zero, or its root mean square below 2^-127). */
 zero_status zero_norm_forward(const void *x, int64_t x_stride, const void *residual,
                               int64_t residual_stride, const void *weight, float eps,
                               int64_t n_rows, int32_t dim, zero_lp lp, void *out,
@@ -528,7 +531,7 @@ zero_status zero_dequantize_rows(const int8_t *codes, const float *scales, int32
 /* Gradients of zero_norm_forward.  sum: its second output (the rounded s; rstd
  * is computed again from it); grad_out: gradient of out; grad_sum (nullable):
  * gradient that reaches s by its other uses.
- *   grad_in[i]     = lp(rstd * (w[i] gy[i] - s[i] rstd^2 mean(w gy s)) + gs[i])
+ *   grad_in[i]     = lp(rstd * (w[i] gy[i] - s[i] rstd mean(w gy s rstd)) + gs[i])
  *   grad_weight[i] = lp(sum over rows of gy[i] s[i] rstd)
  * grad_in is the gradient of x and of residual alike; it may be grad_out or
  * grad_sum itself.  n_rows = 0 writes a zero grad_weight.  workspace: at least

@@ -2,7 +2,7 @@
 // outputs, and its gradients (sm_103a).
 //
 //   s = x + r,  rstd = (mean(s^2) + eps)^(-1/2),  y = s rstd w
-//   gs' = rstd (w gy - s rstd^2 mean(w gy s)) + gs,  gw = sum over rows of gy s rstd
+//   gs' = rstd (w gy - s rstd mean(w gy s rstd)) + gs,  gw = sum over rows of gy s rstd
 //
 // Bound by memory: forward reads x and r and writes y and s once (8 bytes an
 // element in 16 bits), backward reads s, gy, gs and writes gs' (8 bytes).  A row
@@ -41,17 +41,27 @@ __device__ __forceinline__ uint4 narrow(const float v[8]) {
 __device__ __forceinline__ void forget(uint4 &q) { asm volatile("" : "+r"(q.x), "+r"(q.y), "+r"(q.z), "+r"(q.w)); }
 
 // the sum over the warps that own a row, all of a block's unless there is one
-__device__ __forceinline__ float row_sum(float v, int warps, float *shared) {
+template <typename T>
+__device__ __forceinline__ T row_sum(T v, int warps, T *shared) {
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
     if (warps == 1) return v;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (lane == 0) shared[warp] = v;
     __syncthreads();
-    v = lane < warps ? shared[lane] : 0.0f;
+    v = lane < warps ? shared[lane] : T(0);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
     return v;
+}
+
+// Whether a row's sum of squares has left float's range: not finite (from 1.8e19 /
+// sqrt(dim) on, or not finite itself), or so small beside eps that lost squares could
+// count.  The row then adds its squares up again in double.  Only bfloat16 gets there: the
+// least square of fp16 numbers is 2^-48, and the largest sum 3e14.
+template <bool BF16>
+__device__ __forceinline__ bool leaves_float(float sq, float eps, int dim) {
+    return BF16 && !(__fmaf_rn(eps, (float)dim, sq) >= 0x1p-100f && sq <= 1.7e38f);
 }
 
 // the larger one; NaN where either is (fmaxf gives the other)
@@ -75,6 +85,7 @@ template <bool BF16, int VPT, int OUT>
 __global__ void __launch_bounds__(32 * kMaxWarps, 2) norm_rows(const NormArgs a, const NormShape sh) {
     pdl_enter();
     __shared__ float shared[kMaxWarps];
+    __shared__ double shared_wide[kMaxWarps];
     const int threads = sh.warps * 32;
     const int t = sh.warps == 1 ? threadIdx.x & 31 : threadIdx.x;
     const long long row = sh.warps == 1 ? (long long)blockIdx.x * kRowsPerBlock + (threadIdx.x >> 5) : blockIdx.x;
@@ -106,7 +117,16 @@ __global__ void __launch_bounds__(32 * kMaxWarps, 2) norm_rows(const NormArgs a,
         }
     }
     sq = row_sum(sq, sh.warps, shared);
-    const float rstd = rsqrtf(__fadd_rn(__fdiv_rn(sq, (float)a.dim), a.eps));
+    float rstd = rsqrtf(__fadd_rn(__fdiv_rn(sq, (float)a.dim), a.eps));
+    if (leaves_float<BF16>(sq, a.eps, a.dim)) {
+        double wide = 0.0;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+#pragma unroll
+            for (int k = 0; k < 8; ++k) wide = __fma_rn((double)s[j][k], (double)s[j][k], wide);
+        wide = row_sum(wide, sh.warps, shared_wide);
+        rstd = (float)rsqrt(wide / a.dim + (double)a.eps);
+    }
     uint4 *sum = a.sum ? reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.sum) + row * a.sum_stride) : nullptr;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
@@ -196,7 +216,8 @@ dequantize_rows(const int8_t *__restrict__ codes, const float *__restrict__ scal
 
 // The sums v[0], v[1] over the warps that own a row, of several rows a block:
 // `group` is the row's place in the block and its barrier.
-__device__ __forceinline__ void group_sum(float (&v)[2], int warps, int group, float (*shared)[2]) {
+template <typename T>
+__device__ __forceinline__ void group_sum(T (&v)[2], int warps, int group, T (*shared)[2]) {
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -210,7 +231,7 @@ __device__ __forceinline__ void group_sum(float (&v)[2], int warps, int group, f
     asm volatile("barrier.cta.sync %0, %1;" ::"r"(1 + group), "r"(32 * warps) : "memory");
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
-        float t = lane < warps ? shared[group * warps + lane][n] : 0.0f;
+        T t = lane < warps ? shared[group * warps + lane][n] : T(0);
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
         v[n] = t;
@@ -239,6 +260,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps) norm_rows_backward(const NormB
     pdl_enter();
     extern __shared__ uint4 ahead[];  // [two rows][s, gy, gs][vector][thread]
     __shared__ float shared[2][kMaxWarps][2];
+    __shared__ double shared_wide[2][kMaxWarps][2];
     const int threads = sh.warps * 32, groups = (int)blockDim.x / threads;
     const int group = threadIdx.x / threads, t = threadIdx.x - group * threads;
     uint4 w[VPT];
@@ -277,15 +299,18 @@ __global__ void __launch_bounds__(32 * kMaxWarps) norm_rows_backward(const NormB
         fetch(row + step, slot ^ 1);
         copies_wait<1>();
         uint4 qs[VPT], qg[VPT], qe[VPT];
+        auto take = [&] {
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            qs[j] = qg[j] = qe[j] = make_uint4(0u, 0u, 0u, 0u);
-            if (t + j * threads < sh.vecs) {
-                qs[j] = *place(slot, 0, j);
-                qg[j] = *place(slot, 1, j);
-                if (a.grad_sum) qe[j] = *place(slot, 2, j);
+            for (int j = 0; j < VPT; ++j) {
+                qs[j] = qg[j] = qe[j] = make_uint4(0u, 0u, 0u, 0u);
+                if (t + j * threads < sh.vecs) {
+                    qs[j] = *place(slot, 0, j);
+                    qg[j] = *place(slot, 1, j);
+                    if (a.grad_sum) qe[j] = *place(slot, 2, j);
+                }
             }
-        }
+        };
+        take();
         float sums[2] = {0.0f, 0.0f};
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
@@ -300,8 +325,28 @@ __global__ void __launch_bounds__(32 * kMaxWarps) norm_rows_backward(const NormB
             }
         }
         group_sum(sums, sh.warps, group, shared[slot]);
-        const float rstd = rsqrtf(__fadd_rn(__fdiv_rn(sums[0], (float)a.dim), a.eps));
-        const float along = __fmul_rn(__fmul_rn(__fdiv_rn(sums[1], (float)a.dim), rstd), rstd);
+        float rstd = rsqrtf(__fadd_rn(__fdiv_rn(sums[0], (float)a.dim), a.eps));
+        float along = __fmul_rn(__fdiv_rn(sums[1], (float)a.dim), rstd);  // mean(w gy s rstd)
+        if (leaves_float<BF16>(sums[0], a.eps, a.dim) || (BF16 && !(fabsf(sums[1]) <= 1.7e38f))) {
+            double wide[2] = {0.0, 0.0};
+#pragma unroll 1
+            for (int v = t, j = 0; v < sh.vecs; v += threads, ++j) {
+                float fs[8], fg[8], fw[8];
+                widen<BF16>(*place(slot, 0, j), fs);
+                widen<BF16>(*place(slot, 1, j), fg);
+                widen<BF16>(__ldg(static_cast<const uint4 *>(a.weight) + v), fw);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    wide[0] = __fma_rn((double)fs[k], (double)fs[k], wide[0]);
+                    wide[1] = __fma_rn((double)fg[k] * (double)fw[k], (double)fs[k], wide[1]);
+                }
+            }
+            group_sum(wide, sh.warps, group, shared_wide[slot]);
+            const double exact = rsqrt(wide[0] / a.dim + (double)a.eps);
+            rstd = (float)exact;
+            along = (float)(wide[1] / a.dim * exact);
+            take();  // again, so that no register holds the row meanwhile
+        }
         uint4 *out = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.grad_in) + row * a.grad_in_stride);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
@@ -319,7 +364,7 @@ __global__ void __launch_bounds__(32 * kMaxWarps) norm_rows_backward(const NormB
                 const float unit = __fmul_rn(fs[k], rstd);
                 gw[j][k] = __fmaf_rn(fg[k], unit, gw[j][k]);
                 // without grad_sum fe is 0, which leaves the value as it is
-                fe[k] = __fmaf_rn(rstd, __fmaf_rn(-fs[k], along, __fmul_rn(fg[k], fw[k])), fe[k]);
+                fe[k] = __fmaf_rn(rstd, __fmaf_rn(-unit, along, __fmul_rn(fg[k], fw[k])), fe[k]);
             }
             if (v < sh.vecs) out[v] = narrow<BF16>(fe);
         }
