@@ -603,7 +603,9 @@ zero_status zero_loss_backward(const void *hidden, int64_t hidden_stride, const 
  * but must not overlap any grads otherwise; out NULL: norm only.  lens[i] may
  * be 0 (the pointers are then ignored).  The gradients keep their loss scale.
  * norm, coef: one float each, nonfinite: one int32 (1 if any element is not
- * finite), device memory, 4-byte aligned, any may be NULL.  The sum is exact
+ * finite), device memory, 4-byte aligned, any may be NULL.  The norm is that of
+ * this list: where several ranks' gradients are averaged, pack them with max_norm 0
+ * and let zero_adam_step clip the average.  The sum is exact
  * to float rounding over the whole range of the type (partial sums in double).
  * workspace: at least the bytes zero_clip_workspace gives. */
 #define ZERO_FP32 2

@@ -256,7 +256,9 @@ def clip_gradients(grads, out=None, offsets=None, max_norm=0.0, loss_scale=1.0, 
     coefficient, and whether an element is not finite.  The gradients times coef
     go to `out`: None writes them in place; a list takes one tensor each; a 1-D
     tensor is a flat buffer that takes them at `offsets` (elements; default: back
-    to back, as ZeroPlan.tensor_offsets lays them out)."""
+    to back, as ZeroPlan.tensor_offsets lays them out).  Gradients that a step
+    averages over ranks are packed with max_norm 0, as they are: the step clips
+    the average."""
     where = "clip_gradients"
     if not grads:
         _refuse(where, "no gradients")

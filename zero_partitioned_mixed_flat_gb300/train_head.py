@@ -11,8 +11,10 @@ training program does around the library:
     -> clip_gradients into a flat buffer per rank -> reduce, decision, AdamW, cast
 
 Every rank (simulated on one GPU) takes its own batch; its four gradient tensors
-are clipped and packed back to back into its flat buffer, whose partitions are the
-slices that the reduce adds.  The model's weights are views of the parameter
+are packed back to back into its flat buffer, as they are, and the flat buffers'
+partitions are the slices that the reduce averages.  What is clipped is the average,
+by the step's decision from the norm over all partitions: a rank's own norm says
+nothing about it.  The model's weights are views of the parameter
 buffer that the update writes.  Data is synthetic: the next token is the successor
 of the last token or of the one before, with some noise, and some positions are
 masked out of the loss.
@@ -82,7 +84,7 @@ def train(steps=60, ranks=2, vocab=64, dim=128, tokens=2048, lr=2e-2, clip=1.0, 
     slices = {r: [flats[j, r * P:(r + 1) * P] for j in range(ranks)] for r in range(ranks)}
     buffers = StepBuffers(ranks=list(range(ranks)), slices=slices, g=grads, master=master, m=moments[0], v=moments[1],
                           param=params)
-    step = StepSchedule(plan, buffers, Hyper(lr, 0.9, 0.99, 1e-8, 0.0, 1, 0.0), loss_scale=1.0)
+    step = StepSchedule(plan, buffers, Hyper(lr, 0.9, 0.99, 1e-8, 0.0, 1, clip), loss_scale=1.0)
     successors = torch.stack([torch.randperm(vocab, generator=gen, device=device) for _ in range(2)])
     losses = []
     for _ in range(steps):
@@ -90,7 +92,7 @@ def train(steps=60, ranks=2, vocab=64, dim=128, tokens=2048, lr=2e-2, clip=1.0, 
         for j in range(ranks):
             pairs, targets = batch(successors, tokens, gen)
             loss, each = model.gradients(weights, pairs, targets, max(1, int((targets != IGNORE).sum())))
-            clip_gradients(each, flats[j], offsets, max_norm=clip)
+            clip_gradients(each, flats[j], offsets)
             total = total + loss / ranks
         StepSchedule.run(step.calls(torch.cuda.current_stream()))
         losses.append(float(total))
