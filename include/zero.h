@@ -551,7 +551,10 @@ zero_status zero_norm_backward(const void *sum, int64_t sum_stride, const void *
  * hidden: n_tokens rows, weight: vocab rows, of dim lp elements; target:
  * n_tokens int64 (8-byte aligned); loss, lse: n_tokens floats.  The vocabulary
  * is taken in pieces; only each piece's maximum and sum of exponentials are
- * written.  A target outside [0, vocab) that is not `ignore` gives a NaN loss,
+ * written.  Logits are sums in the tensor core's float, at most 512 products at a
+ * time: each 16 products drop what lies below their sum's last place (up to 2^-23 of
+ * it, 2^-22 in fp16), and the sums are then added up rounded to nearest.  Up to four
+ * tokens' logits are rounded to nearest throughout.  A target outside [0, vocab) that is not `ignore` gives a NaN loss,
  * no gradient, and sets bit ZERO_LOSS_BAD_TARGET of *status.
  * status: one int32 of device memory, only ever OR-ed into: bit
  * ZERO_LOSS_TIMEOUT is set by a kernel whose bounded wait for its copies or

@@ -62,20 +62,16 @@ constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kResultWarps * kStoreB
 // relative 4e-6 where float addition has 4e-8.  The losses are float, so the
 // statistics take the sum off after at most 512 products (kChunk blocks) and add it up
 // in registers, rounded to nearest; q, with lp's bits or twice as many, does without.
+// What is still lost depends on the data: nothing where a sum is exact (one nonzero
+// product, small whole numbers), up to 32 steps' last places otherwise.  Where one logit
+// of 18 to 30 is all of lse, 1024 products, vocabulary 40000: bf16 9e-7 low, fp16, whose
+// longer products lose bits too as they are aligned, 2.6e-6.
 constexpr int kChunk = 8;  // whole stages
 // Half as many where no pair has a second tile, whose product the parts' results would
 // hold up: half the error (163 x 328 x 373: lse 1.0e-6 relative, 6e-7 so) for 0 to 14 % of
 // time (200 x 4096 x 5000 25.1 -> 28.6 us, 500 x 1600 x 8000 16.4 -> 17.6, smaller ones the
 // same); with ten tiles a pair (1023 x 768 x 50257) it took 69 us and not 55.
 constexpr int kShortChunk = 4;
-// A sum that grows evenly over n steps of 16 loses half a unit of itself at each, on
-// average 0.72 2^-24 of what it then is (mantissas spread evenly in their logarithm):
-// n 0.18 2^-23 of its end.  Logits are multiplied by 1 + that, where they are added
-// up or scaled anyway (no time at any size).  Measured where one logit of 18 to 30 is
-// all of lse, 1024 products, vocabulary 40000: bf16 9.3e-7 low, 2.1e-7 so; fp16 2.6e-6
-// and 1.9e-6: its longer products lose bits too as they are aligned, how many depends
-// on their sizes, and that is left.
-constexpr float kLostAStep = 0.18033688f * 1.1920929e-7f;  // 1 / (8 ln 2) of 2^-23
 constexpr int kTileCost = 4;  // blocks of K that starting and storing a tile cost, about
 constexpr int kTmemColumns = 512;  // two accumulators of 256 columns
 
@@ -768,7 +764,6 @@ loss_products(const __grid_constant__ ProductParams p) {
         int buf = 0;
         uint32_t acc_phase = 0;
         const int chunks = chunks_of(work.logits.k_blocks, p.chunk);
-        const float whole = 1.0f + kLostAStep * (float)((p.dim + 15) / 16) / (float)chunks;
         for (int j = 0; work.at(j, t); ++j) {
             const int row = quad * 32 + lane;
             const long long token = (long long)t.m0 + (int)rank * kHalf + row;
@@ -792,7 +787,7 @@ loss_products(const __grid_constant__ ProductParams p) {
                     tmem_load16(acc + i, part);
 #pragma unroll
                     for (int k = 0; k < 16; k += 2) {
-                        const float2 two = fma2(make_float2(part[k], part[k + 1]), make_float2(whole, whole), make_float2(z[i + k], z[i + k + 1]));
+                        const float2 two = add2(make_float2(z[i + k], z[i + k + 1]), make_float2(part[k], part[k + 1]));
                         z[i + k] = two.x;
                         z[i + k + 1] = two.y;
                     }
@@ -849,7 +844,6 @@ loss_products(const __grid_constant__ ProductParams p) {
         const int first = ((warp - 2) >> 2) * kResultColumns;  // its columns
         const uint32_t buffer = stage0 + kStages * kStageBytes + (warp - 2) * kStoreBytes;
         const float factor = p.record->factor;
-        const float log2e = kLog2e * (1.0f + kLostAStep * (float)((p.dim + 15) / 16));
         int buf = 0;
         uint32_t acc_phase = 0;
         for (int j = 0; work.at(j, t); ++j) {
@@ -871,7 +865,7 @@ loss_products(const __grid_constant__ ProductParams p) {
                     tmem_load32(acc + col, z);
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
-                        const float2 x = fma2(make_float2(z[j], z[j + 1]), make_float2(log2e, log2e), make_float2(-lse2, -lse2));
+                        const float2 x = fma2(make_float2(z[j], z[j + 1]), make_float2(kLog2e, kLog2e), make_float2(-lse2, -lse2));
                         z[j] = exp2_approx(x.x);
                         z[j + 1] = exp2_approx(x.y);
                     }
