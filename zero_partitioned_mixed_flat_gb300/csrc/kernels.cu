@@ -22,6 +22,7 @@
 // the stream before touching global memory.
 #include "launch.h"
 #include "norm_tree.cuh"
+#include "per_device.h"
 #include "zero_internal.h"
 
 #include <cuda_bf16.h>
@@ -840,12 +841,18 @@ struct DevInfo {
 DevInfo g_dev[64];
 std::mutex g_dev_mu;
 
+// Blocks of `threads` threads and `smem` bytes of dynamic shared memory that an SM of the
+// current device holds at once, that much having been allowed: or an error below zero.
 template <typename K>
-int occupancy(K kernel, int threads, size_t smem) {
-    int blocks = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kernel, threads, smem) != cudaSuccess)
-        blocks = 1;
-    return blocks < 1 ? 1 : blocks;
+int occupancy(PerDevice &kept, K kernel, int threads, size_t smem) {
+    return kept.get([&] {
+        const int set = done_or_error(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+        int blocks = 0;
+        if (set < 0) return set;
+        const int asked = done_or_error(cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kernel, threads, smem));
+        if (asked < 0) return asked;
+        return blocks > 0 ? blocks : -(int)cudaErrorInvalidConfiguration;
+    });
 }
 
 template <int MAXN, bool BF16, bool ACC_LP, int VPT, int THREADS>
@@ -888,11 +895,10 @@ cudaError_t reduce_impl(const void *const *slices, int n_src, int n, const Reduc
 
 template <bool BF16, bool DEFAULT_SPIN>
 cudaError_t adam_tma_impl(const AdamTmaParams &p, cudaStream_t stream) {
-    static const cudaError_t attr = cudaFuncSetAttribute(
-        adam_fused_cast<BF16, DEFAULT_SPIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kAdamTmaSmem);
-    if (attr != cudaSuccess) return attr;
+    static PerDevice kept;
+    const int occ = occupancy(kept, adam_fused_cast<BF16, DEFAULT_SPIN>, kAdamTmaThreads, kAdamTmaSmem);
+    if (occ < 0) return (cudaError_t)-occ;
     const long long tiles = p.n_tiles;
-    static const int occ = occupancy(adam_fused_cast<BF16, DEFAULT_SPIN>, kAdamTmaThreads, kAdamTmaSmem);
     long long grid = (long long)sm_count() * occ;
     if (grid > tiles) grid = tiles;
     if (grid < 1) return cudaSuccess;
@@ -916,10 +922,9 @@ cudaError_t gather_impl(const void *const *shards, int n, int64_t src_off, int64
     p.n = n;
     if (p.n_chunks == 0) return cudaSuccess;
     const size_t smem = (size_t)kGatherStages * kGatherChunk;
-    static const cudaError_t attr = cudaFuncSetAttribute(
-        gather_layer_tma<MAXN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (attr != cudaSuccess) return attr;
-    static const int occ = occupancy(gather_layer_tma<MAXN>, 32, smem);
+    static PerDevice kept;
+    const int occ = occupancy(kept, gather_layer_tma<MAXN>, 32, smem);
+    if (occ < 0) return (cudaError_t)-occ;
     long long grid = (long long)sm_count() * occ;
     if (grid > p.n_chunks) grid = p.n_chunks;
     return launch_pdl(gather_layer_tma<MAXN>, dim3((unsigned)grid), dim3(32), smem, stream, p);

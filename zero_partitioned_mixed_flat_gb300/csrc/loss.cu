@@ -23,6 +23,7 @@
 // being 84-96 % active cold; the smallest by the latency of its loads.
 #include "head_internal.h"
 #include "launch.h"
+#include "per_device.h"
 #include "zero.h"
 #include "zero_internal.h"
 
@@ -1340,12 +1341,15 @@ bool make_map(CUtensorMap *m, const void *p, int64_t rows, int64_t cols, int64_t
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// pairs of CTAs that run at once
+// Pairs of CTAs that run at once on the current device, their shared memory having been
+// allowed: or an error below zero.
 template <bool BF16, bool STATS>
 int pairs_at_once() {
-    static const int n = [] {
-        if (cudaFuncSetAttribute(loss_products<BF16, STATS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes) != cudaSuccess)
-            return 0;
+    static PerDevice kept;
+    return kept.get([] {
+        const int set = done_or_error(
+            cudaFuncSetAttribute(loss_products<BF16, STATS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes));
+        if (set < 0) return set;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2);
         cfg.blockDim = dim3(kProductThreads);
@@ -1357,13 +1361,10 @@ int pairs_at_once() {
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         int clusters = 0;
-        if (cudaOccupancyMaxActiveClusters(&clusters, loss_products<BF16, STATS>, &cfg) != cudaSuccess || clusters < 1) {
-            cudaGetLastError();
-            clusters = sm_count() / 2;
-        }
-        return clusters < 1 ? 1 : clusters;
-    }();
-    return n;
+        const int asked = done_or_error(cudaOccupancyMaxActiveClusters(&clusters, loss_products<BF16, STATS>, &cfg));
+        if (asked < 0) return asked;
+        return clusters > 0 ? clusters : -(int)cudaErrorInvalidConfiguration;
+    });
 }
 
 std::atomic<long long> g_wait_cycles{4000000000ll};  // about two seconds
@@ -1371,7 +1372,7 @@ std::atomic<long long> g_wait_cycles{4000000000ll};  // about two seconds
 template <bool BF16, bool STATS>
 cudaError_t launch_products(const ProductParams &p, int64_t tiles, cudaStream_t stream) {
     const int pairs = pairs_at_once<BF16, STATS>();
-    if (pairs < 1) return cudaErrorInvalidConfiguration;
+    if (pairs < 0) return (cudaError_t)-pairs;
     if (tiles > 0x3fffffff) return cudaErrorInvalidValue;
     const int64_t use = std::max<int64_t>(1, std::min<int64_t>(pairs, tiles));
     return launch_pdl(loss_products<BF16, STATS>, dim3((unsigned)(2 * use)), dim3(kProductThreads), kSmemBytes, stream, p);
@@ -1385,9 +1386,10 @@ bool few(int64_t tokens, int dim) {
 
 template <bool BF16, int T>
 cudaError_t launch_few(const LossArgs &a, float2 *parts, float *picked, cudaStream_t stream) {
-    static const cudaError_t attr =
-        cudaFuncSetAttribute(loss_few<BF16, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem);
-    if (attr != cudaSuccess) return attr;
+    static PerDevice allowed;
+    const int set = allowed.get(
+        [] { return done_or_error(cudaFuncSetAttribute(loss_few<BF16, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem)); });
+    if (set < 0) return (cudaError_t)-set;
     return launch_pdl(loss_few<BF16, T>, dim3(kFewBlocks), dim3(kFewThreads), size_t(T) * a.dim * 4, stream,
                       static_cast<const uint4 *>(a.hidden), (long long)(a.hidden_stride / 8),
                       static_cast<const uint4 *>(a.weight), (long long)(a.weight_stride / 8), a.target, (int)a.tokens,

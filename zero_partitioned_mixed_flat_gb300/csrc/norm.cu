@@ -13,6 +13,7 @@
 // (84 %: a quarter of its lanes has no vector); backward 8191 x 4096 47 us (84 %).
 #include "head_internal.h"
 #include "launch.h"
+#include "per_device.h"
 #include "quant_codes.cuh"
 #include "zero_internal.h"
 
@@ -463,9 +464,12 @@ cudaError_t backward_impl(const NormBackwardArgs &a, const NormShape &s, int vpt
     if (vpt == VPT) {
         // two rows ahead of three tensors; the columns of grad_weight, 4 bytes each, need less
         constexpr int kAhead = 2 * 3 * VPT * (int)sizeof(uint4);
-        static const cudaError_t attr = cudaFuncSetAttribute(
-            norm_rows_backward<BF16, VPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kAhead * 32 * kMaxWarps);
-        if (attr != cudaSuccess) return attr;
+        static PerDevice allowed;
+        const int set = allowed.get([] {
+            return done_or_error(cudaFuncSetAttribute(norm_rows_backward<BF16, VPT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                      kAhead * 32 * kMaxWarps));
+        });
+        if (set < 0) return (cudaError_t)-set;
         const int threads = 32 * s.warps * rows_of_block(a.rows, s);
         return launch_pdl(norm_rows_backward<BF16, VPT>, dim3((unsigned)backward_blocks(a.rows, s)), dim3((unsigned)threads),
                           size_t(kAhead) * threads, stream, a, s);

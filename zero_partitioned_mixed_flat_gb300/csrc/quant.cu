@@ -11,6 +11,7 @@
 // independent loads in flight before it computes, and every warp load and
 // store is one contiguous run.
 #include "launch.h"
+#include "per_device.h"
 #include "quant_codes.cuh"
 #include "zero_internal.h"
 
@@ -157,9 +158,11 @@ gather_dequant(const __grid_constant__ DequantGatherParams<MAXN> p) {
 }
 
 template <typename K>
-int blocks_per_sm(K kernel) {
-    int b = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, kernel, kQuantThreads, 0) != cudaSuccess) b = 1;
+int blocks_per_sm(PerDevice &kept, K kernel) {
+    const int b = kept.get([&] {
+        int n = 0;
+        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kQuantThreads, 0) == cudaSuccess ? n : 0;
+    });
     return b < 1 ? 1 : b;
 }
 
@@ -178,7 +181,8 @@ cudaError_t dequant_gather_impl(const int8_t *const *codes, const float *const *
     p.out = static_cast<uint4 *>(out);
     p.vec_per_shard = shard_len / 8;
     if (p.vec_per_shard == 0 || n == 0) return cudaSuccess;
-    static const int occ = blocks_per_sm(gather_dequant<MAXN, BF16, FP8>);
+    static PerDevice kept;
+    const int occ = blocks_per_sm(kept, gather_dequant<MAXN, BF16, FP8>);
     // about two waves of CTAs over all ranks
     const long long per_rank_need = (p.vec_per_shard + kQuantThreads * kQuantUnroll - 1) /
                                     (kQuantThreads * kQuantUnroll);
@@ -193,7 +197,8 @@ template <bool BF16, bool FP8>
 cudaError_t quantize_impl(const void *shard, int64_t len, int8_t *codes, float *scales, cudaStream_t stream) {
     const long long blocks = len / 128;
     if (blocks == 0) return cudaSuccess;
-    static const int occ = blocks_per_sm(quantize_shard_blocks<BF16, FP8>);
+    static PerDevice kept;
+    const int occ = blocks_per_sm(kept, quantize_shard_blocks<BF16, FP8>);
     long long grid = (long long)sm_count() * occ;
     const long long per_cta = (kQuantThreads / 32) * 4;  // blocks per CTA per iteration
     const long long need = (blocks + per_cta - 1) / per_cta;
