@@ -558,7 +558,7 @@ zero_status zero_norm_backward(const void *sum, int64_t sum_stride, const void *
  * no gradient, and sets bit ZERO_LOSS_BAD_TARGET of *status.
  * status: one int32 of device memory, only ever OR-ed into: bit
  * ZERO_LOSS_TIMEOUT is set by a kernel whose bounded wait for its copies or
- * products gave up (its outputs are then not valid).  The caller clears it.
+ * products gave up (its outputs are then not valid).  zero_loss_take_status clears it.
  * n_tokens in [0, 2^31 - 2^16), vocab in [1, 2^31 - 2^16). */
 #define ZERO_LOSS_TIMEOUT 1
 #define ZERO_LOSS_BAD_TARGET 2
@@ -566,6 +566,9 @@ zero_status zero_norm_backward(const void *sum, int64_t sum_stride, const void *
  * clock cycles (default 4e9, about two seconds); 0 gives up at once where a
  * wait is not already over (used to test that path).  Process-wide.  Host only. */
 zero_status zero_loss_set_wait_limit(int64_t cycles);
+/* *bits = *status and *status = 0 in one exchange (device memory, asynchronous on
+ * `stream`): bits that calls on other streams set meanwhile stay for the next. */
+zero_status zero_loss_take_status(int32_t *status, int32_t *bits, void *stream);
 zero_status zero_loss_workspace(int64_t n_tokens, int64_t vocab, int32_t dim,
                                 int64_t *forward_bytes, int64_t *backward_bytes);
 zero_status zero_loss_forward(const void *hidden, int64_t hidden_stride, const void *weight,

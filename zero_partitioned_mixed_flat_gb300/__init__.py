@@ -21,7 +21,7 @@ from ._abi import (  # noqa: F401
     zero_quantize_shard, zero_gather_layer_quantized, ZERO_QUANT_BLOCK,
     zero_plan_set_gather_quantization, ZERO_QUANT_INT8, ZERO_QUANT_FP8_E4M3,
     zero_norm_forward, zero_norm_forward_quantized, zero_dequantize_rows, zero_norm_backward,
-    zero_norm_backward_workspace, zero_loss_workspace, zero_loss_set_wait_limit, zero_loss_forward, zero_loss_backward,
+    zero_norm_backward_workspace, zero_loss_workspace, zero_loss_set_wait_limit, zero_loss_take_status, zero_loss_forward, zero_loss_backward,
     zero_clip_workspace, zero_clip_gradients, ZERO_FP32, ZERO_HEAD_MAX_DIM, ZERO_LOSS_TIMEOUT,
     ZERO_LOSS_BAD_TARGET,
 )

@@ -67,6 +67,7 @@ SIGNATURES = {
     "zero_norm_backward": (_i32, [_vp, _i64, _vp, _vp, _i64, _vp, _i64, _f32, _i64, _i32, _i32, _vp,
                                   _i64, _vp, _vp, _i64, _vp]),
     "zero_loss_set_wait_limit": (_i32, [_i64]),
+    "zero_loss_take_status": (_i32, [_vp, _vp, _vp]),
     "zero_loss_workspace": (_i32, [_i64, _i64, _i32, _vp, _vp]),
     "zero_loss_forward": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i32, _i32, _vp, _vp,
                                  _vp, _vp, _i64, _vp]),
@@ -391,6 +392,11 @@ def zero_norm_backward(sum_in, sum_stride: int, weight, grad_out, grad_out_strid
 
 def zero_loss_set_wait_limit(cycles: int):
     _check(load().zero_loss_set_wait_limit(cycles), "zero_loss_set_wait_limit")
+
+
+def zero_loss_take_status(status, bits, stream=None):
+    _check(load().zero_loss_take_status(_ptr(status), _ptr(bits), _stream(stream)),
+           "zero_loss_take_status")
 
 
 def zero_loss_workspace(n_tokens: int, vocab: int, dim: int):

@@ -189,6 +189,12 @@ zero_status zero_loss_set_wait_limit(int64_t cycles) {
     return ZERO_OK;
 }
 
+zero_status zero_loss_take_status(int32_t *status, int32_t *bits, void *stream) {
+    if (!status || !bits) return refuse(ZERO_EINVAL, "status or bits is NULL");
+    if (!aligned(status, 4) || !aligned(bits, 4)) return refuse(ZERO_EALIGN, "status or bits is not 4-byte aligned");
+    return launched(zk::launch_take_status(status, bits, static_cast<cudaStream_t>(stream)), "status kernel launch");
+}
+
 zero_status zero_loss_workspace(int64_t n_tokens, int64_t vocab, int32_t dim, int64_t *forward_bytes,
                                 int64_t *backward_bytes) {
     TRY(loss_shape(n_tokens, vocab, dim, ZERO_BF16));

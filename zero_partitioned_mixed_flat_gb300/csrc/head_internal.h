@@ -73,6 +73,7 @@ struct LossArgs {
     void *workspace;
 };
 void set_loss_wait(int64_t cycles);
+cudaError_t launch_take_status(int32_t *status, int32_t *bits, cudaStream_t stream);
 int64_t loss_forward_bytes(int64_t tokens, int64_t vocab, int dim);
 int64_t loss_backward_bytes(int64_t tokens, int64_t vocab, int dim);
 cudaError_t launch_loss_forward(const LossArgs &a, cudaStream_t stream);

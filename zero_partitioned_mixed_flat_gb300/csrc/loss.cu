@@ -1307,6 +1307,12 @@ loss_finish(const float4 *__restrict__ sums, const int *__restrict__ place, cons
     }
 }
 
+// one exchange, so that no bit is lost that another stream's call sets meanwhile
+__global__ void loss_take_status(int *status, int *bits) {
+    pdl_enter();
+    *bits = atomicExch(status, 0);
+}
+
 // ------------------------------------------------------------------------ host
 
 using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -1510,6 +1516,10 @@ cudaError_t backward_impl(const LossArgs &a, cudaStream_t stream) {
 }  // namespace
 
 void set_loss_wait(int64_t cycles) { g_wait_cycles.store(cycles); }
+
+cudaError_t launch_take_status(int32_t *status, int32_t *bits, cudaStream_t stream) {
+    return launch_pdl(loss_take_status, dim3(1), dim3(1), 0, stream, status, bits);
+}
 
 int64_t loss_forward_bytes(int64_t tokens, int64_t vocab, int dim) {
     return parts_of(tokens, vocab, dim) * tokens * 8 + up(tokens * 4, 16);

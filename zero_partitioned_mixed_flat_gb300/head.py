@@ -15,6 +15,7 @@ allocates its status word and waits for the device, so it belongs before a graph
 capture; everything else can be captured.
 """
 import contextlib
+import threading
 from array import array
 from ctypes import byref, c_int64 as _i64
 from itertools import accumulate
@@ -28,6 +29,7 @@ from . import _abi as A
 _LP = {torch.float16: A.ZERO_FP16, torch.bfloat16: A.ZERO_BF16}
 _CLIP = {**_LP, torch.float32: A.ZERO_FP32}
 _STATUS = {}   # device index -> the int32 that every loss call of the process ORs into
+_STATUS_LOCK = threading.Lock()
 _HERE = contextlib.nullcontext()
 
 
@@ -88,23 +90,30 @@ def _vector(where, name, t, n, dtype):
 def _status(device):
     word = _STATUS.get(device.index)
     if word is None:
-        word = _STATUS[device.index] = torch.zeros(4, dtype=torch.int32, device=device)
-        torch.cuda.synchronize(device)   # calls on any stream may use it from here on
+        with _STATUS_LOCK:               # one word, whichever thread calls first
+            word = _STATUS.get(device.index)
+            if word is None:
+                word = torch.zeros(4, dtype=torch.int32, device=device)
+                torch.cuda.synchronize(device)   # calls on any stream may use it from here on
+                _STATUS[device.index] = word
     return word
 
 
 def check_losses(device=None):
     """Waits for the device and raises if a linear_loss or linear_loss_backward
     since the last check met a target outside the vocabulary (ZERO_EINVAL) or
-    gave up a bounded wait (ZERO_ETIMEOUT: its outputs are not valid)."""
+    gave up a bounded wait (ZERO_ETIMEOUT: its outputs are not valid).  All calls of
+    the process on the device report to the same check, whatever their stream or
+    thread; what one sets while a check runs is left for the next."""
     device = torch.device("cuda" if device is None else device)
     if device.index is None:
         device = torch.device("cuda", torch.cuda.current_device())
     torch.cuda.synchronize(device)
     word = _status(device)
-    bits = int(word[0].item())
-    word.zero_()
-    torch.cuda.synchronize(device)
+    with torch.cuda.device(device):
+        taken = torch.empty(1, dtype=torch.int32, device=device)
+        A.zero_loss_take_status(word, taken)
+        bits = int(taken.item())
     if bits & A.ZERO_LOSS_TIMEOUT:
         raise A.ZeroError(A.ZERO_ETIMEOUT, "check_losses", "a bounded device wait gave up")
     if bits & A.ZERO_LOSS_BAD_TARGET:
