@@ -23,6 +23,7 @@
 // being 84-96 % active cold; the smallest by the latency of its loads.
 #include "head_internal.h"
 #include "launch.h"
+#include "loss_drain.h"
 #include "per_device.h"
 #include "zero.h"
 #include "zero_internal.h"
@@ -193,6 +194,17 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank) {
     return r;
 }
 
+// a store to either CTA's shared memory
+__device__ __forceinline__ void store_in_cta(const volatile void *p, uint32_t rank, uint32_t value) {
+    asm volatile("st.relaxed.cluster.shared::cluster.u32 [%0], %1;" ::"r"(in_cta(smem_addr(const_cast<const void *>(p)), rank)), "r"(value)
+                 : "memory");
+}
+
+// bytes counted on `bar` as if a copy had landed
+__device__ __forceinline__ void bar_count(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
 __device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -255,6 +267,11 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
         "h"((uint16_t)3)
         : "memory");
+}
+
+// the same on a barrier of this CTA only
+__device__ __forceinline__ void mma_commit_here(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -503,24 +520,54 @@ struct Work {
 struct Shared {
     uint64_t full[kStages], empty[kStages], acc_full[2], acc_empty[2], drained;
     uint32_t tmem;
-    int dead;  // a wait of this CTA gave up
+    int dead;  // a wait of the pair gave up
+    // what the first CTA has to know to wait for the pair's copies: see loss_drain.h
+    int placed[2], consumed;
+    uint32_t bytes[2][kStages];
 };
 
-// A bounded wait: false once `limit` cycles have passed (or another wait of the
-// CTA has given up); the CTA then stops and the status says so.
+// The longest that a pair which gives up waits for each of its copies and products in
+// flight, in cycles: they end by themselves, in microseconds.
+constexpr long long kDrainCycles = 4000000000ll;
+
+// the pair stops, and the status says so
+__device__ __noinline__ void give_up(volatile int *dead, int *status) {
+    store_in_cta(dead, 0, 1u);
+    store_in_cta(dead, 1, 1u);
+    atomicOr(status, ZERO_LOSS_TIMEOUT);
+}
+
+// A bounded wait: false once `limit` cycles have passed, or another wait of the
+// pair has given up.
 __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatile int *dead, long long limit, int *status) {
     const uint32_t b = smem_addr(bar);
     if (bar_try(b, parity)) return true;
     const long long t0 = clock64();
     while (!bar_try(b, parity)) {
         if (*dead || clock64() - t0 >= limit) {
-            *dead = 1;
-            atomicOr(status, ZERO_LOSS_TIMEOUT);
+            give_up(dead, status);
             return false;
         }
     }
     return true;
 }
+
+// the same, for what ends by itself
+__device__ __forceinline__ bool wait_out(uint64_t *bar, uint32_t parity) {
+    const long long t0 = clock64();
+    while (!bar_try(smem_addr(bar), parity))
+        if (clock64() - t0 >= kDrainCycles) return false;
+    return true;
+}
+
+// drain_copies' barriers
+struct FullBars {
+    uint64_t *full;
+
+    __device__ __forceinline__ void expect(int slot, uint32_t bytes) { bar_expect(smem_addr(full + slot), bytes); }
+    __device__ __forceinline__ void count(int slot, uint32_t bytes) { bar_count(smem_addr(full + slot), bytes); }
+    __device__ __forceinline__ bool wait(int slot, uint32_t parity) { return wait_out(full + slot, parity); }
+};
 
 // 32 rows of 128 bytes, one a lane, to a box of `map`: swizzled into the warp's
 // buffer once its last store has read it, then one store.  (A second buffer a
@@ -646,7 +693,7 @@ loss_products(const __grid_constant__ ProductParams p) {
 
     if (warp == 0) {
         if (lane == 0) {  // ------------------------------------------ loads
-            int stage = 0;
+            int stage = 0, placed = 0;
             uint32_t phase = 0;
             bool ok = true;
             Tile next;
@@ -662,6 +709,7 @@ loss_products(const __grid_constant__ ProductParams p) {
                     if (!ok) break;
                     const int blocks = t.k1 - k < kStageBlocks ? t.k1 - k : kStageBlocks;
                     const uint32_t bar = in_cta(smem_addr(&sh.full[stage]), 0);
+                    sh.bytes[rank][stage] = blocks * bytes;
                     if (rank == 0) bar_expect(smem_addr(&sh.full[stage]), blocks * bytes);
                     for (int i = 0; i < blocks; ++i) {
                         const uint32_t a = stage0 + stage * kStageBytes + i * kBlockBytes, b = a + kOperandBytes;
@@ -681,6 +729,7 @@ loss_products(const __grid_constant__ ProductParams p) {
                             if (two) tma_load(b + kBoxBytes, h, n0 + 64, kk, bar);
                         }
                     }
+                    ++placed;
                     if (++stage == kStages) {
                         stage = 0;
                         phase ^= 1;
@@ -691,10 +740,13 @@ loss_products(const __grid_constant__ ProductParams p) {
                 if (t.k0 >= t.k1) more = work.at(j, next);
                 t = next;
             }
+            store_in_cta(&sh.placed[rank], 0, placed);
+            if (rank == 1)
+                for (int s = 0; s < kStages; ++s) store_in_cta(&sh.bytes[1][s], 0, sh.bytes[1][s]);
         }
     } else if (warp == 1) {
         if (rank == 0 && lane == 0) {  // ------------------------- products
-            int stage = 0, buf = 0;
+            int stage = 0, buf = 0, consumed = 0;
             uint32_t phase = 0, acc_phase = 0;
             // The tensor core takes little ahead of what it computes, so this thread finds out
             // what comes next while a stage is under way: whether the next stage is
@@ -728,6 +780,7 @@ loss_products(const __grid_constant__ ProductParams p) {
                         if (k + 1 < k1) feed.block(acc, a + (kBlockBytes >> 4), b + (kBlockBytes >> 4), 1);
                         mma_commit(smem_addr(&sh.empty[stage]));
                         add = 1;
+                        ++consumed;
                         if (++stage == kStages) {
                             stage = 0;
                             phase ^= 1;
@@ -752,10 +805,10 @@ loss_products(const __grid_constant__ ProductParams p) {
                 t.k1 = after.k1;
                 feed = feed_after;
             }
-            if (!ok) {  // the products already issued still read shared memory
-                mma_commit(smem_addr(&sh.drained));
-                for (int i = 0; i < 4096 && !bar_try(smem_addr(&sh.drained), 0); ++i) __nanosleep(256);
-            }
+            sh.consumed = consumed;
+            // whoever gave up: no product reads shared memory or writes sums any more
+            mma_commit_here(smem_addr(&sh.drained));
+            if (!wait_out(&sh.drained, 0)) give_up(dead, p.status);
         }
     } else if constexpr (STATS) {  // ------------------------------- statistics
         const int quad = warp & 3;  // the quarter of the lanes this warp may read
@@ -938,14 +991,20 @@ loss_products(const __grid_constant__ ProductParams p) {
     }
     __syncwarp();
     __syncthreads();
-    // after a wait that gave up, loads may still be on their way to either CTA's
-    // shared memory: nothing counts them any more, so give them time
-    if (*dead && threadIdx.x == 0)
-        for (int i = 0; i < 4096; ++i) __nanosleep(512);
-    __syncthreads();
     tc_fence_before();
     cluster_sync();
     tc_fence_after();
+    // After a wait that gave up (the flag is the pair's, so both CTAs come here or neither),
+    // copies may still be on their way to either CTA's shared memory.  The other warps'
+    // stores have been waited for, and both loaders have stopped.
+    if (*dead) {
+        if (rank == 0 && threadIdx.x == 0) {
+            FullBars bars{sh.full};
+            if (!drain_copies(sh.placed, sh.bytes, sh.consumed, bars)) atomicOr(p.status, ZERO_LOSS_TIMEOUT);
+        }
+        __syncwarp();
+        cluster_sync();
+    }
     if (warp == 1)
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemColumns) : "memory");
 }
