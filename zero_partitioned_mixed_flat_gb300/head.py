@@ -9,7 +9,10 @@ bfloat16 CUDA tensors whose rows are contiguous; row lengths and strides must be
 multiples of 8 and pointers 16-byte aligned.  `stream` is the current stream, a
 torch.cuda.Stream or a raw cudaStream_t; outputs and scratch are allocated for
 that stream, so a caller on several streams orders its own tensors between
-them and nothing else.  Wrong shapes, types or devices raise ZeroError
+them and nothing else.  No graph is recorded: the *_backward functions are the
+gradients, to be called by hand or from a torch.autograd.Function, and a matrix
+or vector that requires grad is refused while gradients are enabled (clip_gradients
+takes its tensors as numbers).  Wrong shapes, types or devices raise ZeroError
 (ZERO_EINVAL) before any device work.  A process's first loss call on a device
 allocates its status word and waits for the device, so it belongs before a graph
 capture; everything else can be captured.
@@ -65,8 +68,14 @@ def _scratch(n, device):
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
+def _plain(where, name, t):
+    if t.requires_grad and torch.is_grad_enabled():
+        _refuse(where, "%s requires grad, and the call would record no graph: detach it, or call under torch.no_grad()" % name)
+
+
 def _matrix(where, name, t, dtype=None, shape=None):
     """(rows, columns, row stride) of a 2-D tensor with contiguous rows on the current device."""
+    _plain(where, name, t)
     if t.ndim != 2 or t.dtype not in _LP or t.get_device() != torch._C._cuda_getDevice():
         _refuse(where, "%s must be a 2-D float16 or bfloat16 tensor on the current CUDA device" % name)
     if dtype is not None and t.dtype != dtype:
@@ -82,6 +91,7 @@ def _matrix(where, name, t, dtype=None, shape=None):
 
 
 def _vector(where, name, t, n, dtype):
+    _plain(where, name, t)
     if (t.ndim != 1 or t.dtype != dtype or t.get_device() != torch._C._cuda_getDevice() or t.shape[0] != n
             or (n > 1 and t.stride(0) != 1)):
         _refuse(where, "%s must be a contiguous vector of %d %s on the current CUDA device" % (name, n, dtype))
