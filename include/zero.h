@@ -554,7 +554,7 @@ zero_status zero_norm_backward(const void *sum, int64_t sum_stride, const void *
  * written.  Logits are sums in the tensor core's float, at most 512 products at a
  * time: each 16 products drop what lies below their sum's last place (up to 2^-23 of
  * it, 2^-22 in fp16), and the sums are then added up rounded to nearest.  Up to four
- * tokens' logits are rounded to nearest throughout.  A target outside [0, vocab) that is not `ignore` gives a NaN loss,
+ * tokens' logits, and every target's, are rounded to nearest throughout.  A target outside [0, vocab) that is not `ignore` gives a NaN loss,
  * no gradient, and sets bit ZERO_LOSS_BAD_TARGET of *status.
  * status: one int32 of device memory, only ever OR-ed into: bit
  * ZERO_LOSS_TIMEOUT is set by a kernel whose bounded wait for its copies or
@@ -588,7 +588,7 @@ zero_status zero_loss_forward(const void *hidden, int64_t hidden_stride, const v
  * to lp for the two products (to twice lp's bits where at most 32 tokens count),
  * relative to the largest finite |grad_loss| (so a gradient of any size fits
  * fp16), whose sums are float.  The slope at the target is
- * expm1(z[t][target[t]] - lse[t]) of a logit summed in float. */
+ * expm1(z[t][target[t]] - lse[t]), of the same logit as in lse. */
 zero_status zero_loss_backward(const void *hidden, int64_t hidden_stride, const void *weight,
                                int64_t weight_stride, const int64_t *target, int64_t ignore,
                                int64_t n_tokens, int64_t vocab, int32_t dim, zero_lp lp,

@@ -6,7 +6,8 @@
 // until the previous kernel in the stream has completed and its writes are
 // visible (griddepcontrol.wait), then lets the next kernel of the stream begin
 // launching (griddepcontrol.launch_dependents).  No global memory is read or
-// written before the wait, so the stream order of the step is kept exactly;
+// written before the wait, so the stream order of the step is kept exactly
+// (loss_join reads what the kernel before it reads too, and says why it may);
 // what overlaps is the next kernel's launch and CTA start-up with the
 // previous kernel's last CTAs.  A dependent grid launches only after every
 // CTA of the previous grid has started and passed pdl_enter(), so waiting

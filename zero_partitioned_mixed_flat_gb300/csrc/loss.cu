@@ -1011,20 +1011,80 @@ loss_products(const __grid_constant__ ProductParams p) {
 
 // ---------------------------------------------------------- the smaller kernels
 
-constexpr int kJoinTokens = 32, kJoinWays = 32;
+// Tokens of a block, which has a warp for each; a lane for each way.  (32 tokens leave the
+// targets' rows to few SMs: 163 x 328 x 373 10.8 us for both kernels, with 8 10.1.)
+constexpr int kJoinTokens = 8, kJoinWays = 32;
 
-// lse and loss of 32 tokens: 32 ways along the vocabulary, joined in order
+template <bool BF16>
+__device__ __forceinline__ void widen8(uint4 q, float f[8]) {
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if constexpr (BF16) {
+            f[2 * k] = __uint_as_float(w[k] << 16);
+            f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+        } else {
+            const float2 t = __half22float2(*reinterpret_cast<const __half2 *>(&w[k]));
+            f[2 * k] = t.x;
+            f[2 * k + 1] = t.y;
+        }
+    }
+}
+
+// A logit by a warp, in float rounded to nearest, the same bits as loss_few's: each lane's
+// vectors in order, then lanes 16, 8, ... apart.  also(v, x): vector v of h, on its way.
+template <bool BF16, typename Also>
+__device__ __forceinline__ float warp_logit(const uint4 *h, const uint4 *w, int vecs, int lane, Also also) {
+    float z = 0.0f;
+#pragma unroll 4
+    for (int v = lane; v < vecs; v += 32) {
+        const uint4 x = h[v], m = w[v];
+        also(v, x);
+        float a[8], b[8];
+        widen8<BF16>(x, a);
+        widen8<BF16>(m, b);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) z = __fmaf_rn(a[k], b[k], z);
+    }
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    return z;
+}
+
+// Where the hidden states and the matrix are, their rows in vectors.
+struct Operands {
+    const uint4 *hidden, *weight;
+    long long stride, weight_stride;
+    int vecs;
+};
+
+// lse and loss: 32 ways along the vocabulary for each token, joined in order.
+// The target's logit is a float sum rounded to nearest, in lse as in the slope (take_rows):
+// of a target of probability p the loss and the slope are what is left of z - lse, 1 - p,
+// and z off by 1e-5 in one of the two made gradients 1 % off at p = 0.999 and 3 to 17 % at
+// 0.9999.  With the tensor core's logit d below it, lse is higher by log(1 + p (e^d - 1)),
+// and the loss lower by d less that.  (hidden NULL: the logits are such sums already.)
+template <bool BF16>
 __global__ void __launch_bounds__(kJoinTokens *kJoinWays)
-loss_join(const float2 *__restrict__ parts, const float *__restrict__ picked, int tiles, const int64_t *__restrict__ target,
-          long long ignore, long long tokens, long long vocab, float *loss, float *lse, int *status) {
-    pdl_enter();
+loss_join(const __grid_constant__ Operands in, const float2 *__restrict__ parts, const float *__restrict__ picked, int tiles,
+          const int64_t *__restrict__ target, long long ignore, long long tokens, long long vocab, float *loss, float *lse, int *status) {
     __shared__ float2 way[kJoinWays][kJoinTokens + 1];
     const int x = threadIdx.x % kJoinTokens, w = threadIdx.x / kJoinTokens;
     const long long t = (long long)blockIdx.x * kJoinTokens + x;
-    // what the warp that ends with token w needs, asked for with the parts
-    const long long mine = (long long)blockIdx.x * kJoinTokens + w;
+    // the token that this warp ends with
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long mine = (long long)blockIdx.x * kJoinTokens + warp;
     const long long y = mine < tokens ? target[mine] : ignore;
-    const float z_y = y >= 0 && y < vocab && y != ignore ? picked[mine] : 0.0f;
+    const bool counts = y >= 0 && y < vocab && y != ignore;
+    // The target and both rows are read before the wait for the statistics, while their
+    // kernel still runs: it only reads them too, and no block of this one starts before every
+    // block of that one has waited for all that came before.  (After the wait, 256 x 4096 x
+    // 32000 took 64 us for both kernels; so 57, as without these rows.)
+    float z_float = 0.0f;
+    if (counts && in.hidden)
+        z_float = warp_logit<BF16>(in.hidden + mine * in.stride, in.weight + y * in.weight_stride, in.vecs, lane, [](int, uint4) {});
+    pdl_enter();
+    const float z_y = counts ? picked[mine] : 0.0f;
+    const float low = counts && in.hidden ? z_float - z_y : 0.0f;  // what the picked logit is too low by
     float2 acc = make_float2(-INFINITY, 0.0f);
     if (t < tokens) {
         for (int i = w; i < tiles; i += 8 * kJoinWays) {
@@ -1045,22 +1105,26 @@ loss_join(const float2 *__restrict__ parts, const float *__restrict__ picked, in
     way[w][x] = acc;
     __syncthreads();
     // then a warp for each token, a lane for each way
-    const int lane = threadIdx.x & 31;
-    acc = way[lane][w];
+    acc = way[lane][warp];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         acc = join_parts(acc, make_float2(__shfl_xor_sync(0xffffffffu, acc.x, o), __shfl_xor_sync(0xffffffffu, acc.y, o)));
     if (lane != 0 || mine >= tokens) return;
-    const float l = acc.x + log2f(acc.y) * kLn2;
-    lse[mine] = l;
-    if (y == ignore) {
+    const float log_sum = log2f(acc.y) * kLn2;
+    float more = 0.0f;
+    if (counts) {
+        const float off = (acc.x - z_y) + log_sum;  // -log p
+        // (logits of a million and beyond are off by more, and nothing is left of any difference)
+        const bool small = fabsf(low) <= 1.0f && isfinite(off);
+        if (small) more = log1pf(expf(-off) * expm1f(low));
+        loss[mine] = small ? off + (more - low) : off;
+    } else if (y == ignore) {
         loss[mine] = 0.0f;
-    } else if (y < 0 || y >= vocab) {
+    } else {
         loss[mine] = __int_as_float(0x7fffffff);
         atomicOr(status, ZERO_LOSS_BAD_TARGET);
-    } else {
-        loss[mine] = l - z_y;
     }
+    lse[mine] = acc.x + (log_sum + more);
 }
 
 // Statistics of a few tokens, without the tensor cores: a tile of theirs has 256
@@ -1075,22 +1139,6 @@ constexpr int kFewTokens = 4;
 constexpr int kFewThreads = 256;
 constexpr int kFewBlocks = 304;              // two on each SM
 constexpr int kFewSmem = 96 * 1024;          // floats of the hidden states, at most
-
-template <bool BF16>
-__device__ __forceinline__ void widen8(uint4 q, float f[8]) {
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        if constexpr (BF16) {
-            f[2 * k] = __uint_as_float(w[k] << 16);
-            f[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-        } else {
-            const float2 t = __half22float2(*reinterpret_cast<const __half2 *>(&w[k]));
-            f[2 * k] = t.x;
-            f[2 * k + 1] = t.y;
-        }
-    }
-}
 
 template <bool BF16, int T>
 __global__ void __launch_bounds__(kFewThreads, 2)
@@ -1213,19 +1261,9 @@ __device__ __forceinline__ void take_rows(const RowSource &r, const int *index, 
         }
         const long long t = index[n], y = r.target[t];
         const uint4 *h = r.hidden + t * r.stride, *w = r.weight + y * r.weight_stride;
-        float sum[2] = {0.0f, 0.0f};
-#pragma unroll 4
-        for (int v = lane; v < r.vecs; v += 32) {
-            const uint4 x = h[v], m = w[v];
+        const float z = warp_logit<BF16>(h, w, r.vecs, lane, [&](int v, uint4 x) {
             if (out) out[i * r.vecs + v] = x;
-            float a[8], b[8];
-            widen8<BF16>(x, a);
-            widen8<BF16>(m, b);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) sum[k & 1] = __fmaf_rn(a[k], b[k], sum[k & 1]);
-        }
-        float z = sum[0] + sum[1];
-        for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+        });
         if (lane == 0) at_target[i] = expm1f(z - r.lse[t]);
     }
 }
@@ -1495,8 +1533,14 @@ cudaError_t forward_impl(const LossArgs &a, cudaStream_t stream) {
         e = launch_products<BF16, true>(p, tiles, stream);
     }
     if (e != cudaSuccess) return e;
-    return launch_pdl(loss_join, dim3((unsigned)((a.tokens + kJoinTokens - 1) / kJoinTokens)),
-                      dim3(kJoinTokens * kJoinWays), 0, stream, (const float2 *)parts, (const float *)picked, (int)n,
+    Operands in;
+    in.hidden = few(a.tokens, a.dim) ? nullptr : static_cast<const uint4 *>(a.hidden);
+    in.weight = static_cast<const uint4 *>(a.weight);
+    in.stride = a.hidden_stride / 8;
+    in.weight_stride = a.weight_stride / 8;
+    in.vecs = a.dim / 8;
+    return launch_pdl(loss_join<BF16>, dim3((unsigned)((a.tokens + kJoinTokens - 1) / kJoinTokens)),
+                      dim3(kJoinTokens * kJoinWays), 0, stream, in, (const float2 *)parts, (const float *)picked, (int)n,
                       a.target, (long long)a.ignore, (long long)a.tokens, (long long)a.vocab, a.loss, a.lse, a.status);
 }
 
