@@ -233,7 +233,9 @@ def linear_loss(hidden, weight, targets, ignore=-100, stream=None):
 def linear_loss_backward(hidden, weight, targets, lse, grad_loss, ignore=-100, grad_hidden=None,
                          grad_weight=None, stream=None):
     """(grad_hidden, grad_weight) of sum(grad_loss * loss), written into the given
-    tensors if there are any (e.g. views of the flat gradient buffer)."""
+    tensors if there are any.  These need 16-byte aligned rows like every matrix,
+    which a view of a flat buffer has where the tensor's offset and row length are
+    multiples of 8; other gradients go there by clip_gradients."""
     where = "linear_loss_backward"
     tokens, dim, vocab, hs, ws = _loss_inputs(where, hidden, weight, targets)
     _vector(where, "lse", lse, tokens, torch.float32)
