@@ -16,7 +16,7 @@
 // what each SM reads of B; two pairs that share B by multicast were 1-3 % slower
 // (clusters of four fill 144 of 152 SMs).
 //
-// On GB300, vocabulary 50257: forward 8184 x 1600 0.81 ms (1620 TFLOP/s; 0.71 ms
+// On GB300, vocabulary 50257: forward 8184 x 1600 0.81 ms (1620 TFLOP/s; 0.72 ms
 // from a cold start); forward and gradients 4096 x 4096 4.3 ms (8 T D V operations,
 // 1570 TFLOP/s), 2048 x 1600 0.93 ms, 1023 x 768 0.24 ms.  Warm, the larger ones are
 // bound by power (a library's bf16 product sustains 1690 TFLOP/s), the tensor pipe
@@ -47,15 +47,15 @@ constexpr int kTileK = 64;                 // 128 bytes: one swizzle row
 constexpr int kOperandBytes = kHalf * kTileK * 2;
 constexpr int kBlockBytes = 2 * kOperandBytes;  // both operands of a block of K
 // A stage of shared memory holds two blocks of K, so that the thread that feeds
-// the tensor core waits and commits half as often: 8184 tokens x 1600 forward 0.817
-// ms, 0.845 with six stages of one; 4096 x 4096 with gradients 4.38 ms, 4.49.
+// the tensor core waits and commits half as often.  (Six stages of one: 8184 x 1600
+// forward 3 % slower, 4096 x 4096 with gradients 2.5 %.)
 constexpr int kStageBlocks = 2, kStages = 3;
 constexpr int kStageBytes = kStageBlocks * kBlockBytes;
 constexpr int kBoxBytes = 64 * kTileK * 2;  // a 64 x 64 box of an operand whose rows run along K
 constexpr int kStoreBytes = 32 * 128;       // 32 rows of 128 bytes: one warp's store
 // Warps that take a tile's results: two on each quarter of its rows, each half of
-// the columns.  (Sixteen for the statistics: 0.865 ms for 8184 tokens x 1600, with
-// eight 0.849: they take issue slots from the thread that feeds the tensor core.)
+// the columns.  (Sixteen for the statistics: 8184 x 1600 forward 2 % slower: they take
+// issue slots from the thread that feeds the tensor core.)
 constexpr int kResultWarps = 8, kResultColumns = kTileN / 2;
 constexpr int kProductThreads = 64 + 32 * kResultWarps;
 constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kResultWarps * kStoreBytes;
@@ -70,8 +70,8 @@ constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kResultWarps * kStoreB
 // longer products lose bits too as they are aligned, 2.6e-6.
 constexpr int kChunk = 8;  // whole stages
 // Half as many where no pair has a second tile, whose product the parts' results would
-// hold up: half the error (163 x 328 x 373: lse 1.0e-6 relative, 6e-7 so) for 0 to 14 % of
-// time (200 x 4096 x 5000 25.1 -> 28.6 us, 500 x 1600 x 8000 16.4 -> 17.6, smaller ones the
+// hold up: half the error (163 x 328 x 373, the tensor core's logits alone: lse 1.0e-6
+// relative, 6e-7 so) for 0 to 14 % of time (200 x 4096 x 5000 25.1 -> 28.6 us, 500 x 1600 x 8000 16.4 -> 17.6, smaller ones the
 // same); with ten tiles a pair (1023 x 768 x 50257) it took 69 us and not 55.
 constexpr int kShortChunk = 4;
 constexpr int kTileCost = 4;  // blocks of K that starting and storing a tile cost, about
