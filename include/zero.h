@@ -597,6 +597,45 @@ zero_status zero_loss_backward(const void *hidden, int64_t hidden_stride, const 
                                int64_t grad_weight_stride, int32_t *status, void *workspace,
                                int64_t workspace_bytes, void *stream);
 
+/* The gated projections that open a feed-forward block, without keeping either:
+ *   g = x . gate^T,  u = x . up^T,  out = lp(act(g) * u)
+ * x: n_tokens rows of dim lp elements; gate, up: wide rows of dim; out: n_tokens rows of
+ * wide.  act: ZERO_ACT_SILU g / (1 + exp(-g)), ZERO_ACT_GELU g Phi(g) with the normal
+ * distribution's Phi, ZERO_ACT_GELU_TANH its usual approximation
+ * g (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) / 2.  g and u are float sums that are
+ * not rounded before the activation.  gate and up may be parts of one matrix (rows of
+ * either that lie apart by more than their length, or one behind the other).
+ * wide: a multiple of 8 in [8, 2^30); n_tokens in [0, 2^31 - 2^16).
+ * status: as for zero_loss_forward; a wait that gives up sets ZERO_LOSS_TIMEOUT, and
+ * zero_loss_set_wait_limit bounds the waits.  workspace: at least the bytes that
+ * zero_gated_workspace gives (0 and NULL where it gives none). */
+#define ZERO_ACT_SILU 0
+#define ZERO_ACT_GELU 1
+#define ZERO_ACT_GELU_TANH 2
+zero_status zero_gated_workspace(int64_t n_tokens, int64_t wide, int32_t dim,
+                                 int64_t *forward_bytes, int64_t *backward_bytes);
+zero_status zero_gated_forward(const void *x, int64_t x_stride, const void *gate,
+                               int64_t gate_stride, const void *up, int64_t up_stride, int32_t act,
+                               int64_t n_tokens, int64_t wide, int32_t dim, zero_lp lp, void *out,
+                               int64_t out_stride, int32_t *status, void *workspace,
+                               int64_t workspace_bytes, void *stream);
+
+/* Gradients of zero_gated_forward for grad_out, the gradient of out:
+ *   dg = grad_out u act'(g),  du = grad_out act(g)
+ *   grad_x = lp(dg . gate + du . up),  grad_gate = lp(dg^T . x),  grad_up = lp(du^T . x)
+ * g and u are computed again from x.  dg and du are rounded to lp for the products, in
+ * fp16 relative to the largest finite |grad_out| (so gradients of any size fit; they
+ * overflow where |u act'(g)| or |act(g)| passes 2^17); the products' sums are float.
+ * n_tokens = 0 writes zero gradients of the matrices. */
+zero_status zero_gated_backward(const void *x, int64_t x_stride, const void *gate,
+                                int64_t gate_stride, const void *up, int64_t up_stride,
+                                int32_t act, const void *grad_out, int64_t grad_out_stride,
+                                int64_t n_tokens, int64_t wide, int32_t dim, zero_lp lp,
+                                void *grad_x, int64_t grad_x_stride, void *grad_gate,
+                                int64_t grad_gate_stride, void *grad_up, int64_t grad_up_stride,
+                                int32_t *status, void *workspace, int64_t workspace_bytes,
+                                void *stream);
+
 /* The global norm over a list of gradient tensors, and the clipped gradients:
  *   norm = sqrt(sum over every element of g^2) / loss_scale
  *   coef = max_norm / (norm + 1e-6) if max_norm > 0 and that is < 1, else 1

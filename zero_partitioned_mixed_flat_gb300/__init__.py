@@ -23,13 +23,14 @@ from ._abi import (  # noqa: F401
     zero_norm_forward, zero_norm_forward_quantized, zero_dequantize_rows, zero_norm_backward,
     zero_norm_backward_workspace, zero_loss_workspace, zero_loss_set_wait_limit, zero_loss_take_status, zero_loss_forward, zero_loss_backward,
     zero_clip_workspace, zero_clip_gradients, ZERO_FP32, ZERO_HEAD_MAX_DIM, ZERO_LOSS_TIMEOUT,
-    ZERO_LOSS_BAD_TARGET,
+    ZERO_LOSS_BAD_TARGET, zero_gated_workspace, zero_gated_forward, zero_gated_backward,
+    ZERO_ACT_SILU, ZERO_ACT_GELU, ZERO_ACT_GELU_TANH,
 )
 from .plan import ZeroPlan  # noqa: F401
 
 # the training head on torch tensors (head.py), imported at first use: the rest of
 # the package does without torch
-_HEAD = ("check_losses", "clip_gradients", "dequantize_rows", "linear_loss", "linear_loss_backward",
+_HEAD = ("check_losses", "clip_gradients", "dequantize_rows", "gated_linear", "gated_linear_backward", "linear_loss", "linear_loss_backward",
          "residual_norm", "residual_norm_backward", "residual_norm_quantized")
 
 

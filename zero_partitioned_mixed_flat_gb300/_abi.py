@@ -25,6 +25,7 @@ ZERO_QUANT_INT8, ZERO_QUANT_FP8_E4M3 = 0, 1
 ZERO_FP32 = 2                     # an element type of zero_clip_gradients only
 ZERO_HEAD_MAX_DIM = 16384
 ZERO_LOSS_TIMEOUT, ZERO_LOSS_BAD_TARGET = 1, 2
+ZERO_ACT_SILU, ZERO_ACT_GELU, ZERO_ACT_GELU_TANH = 0, 1, 2
 
 # every exported entry point of include/zero.h, with its ctypes signature
 _i32, _i64, _f32, _f64, _vp = C.c_int32, C.c_int64, C.c_float, C.c_double, C.c_void_p
@@ -73,6 +74,11 @@ SIGNATURES = {
                                  _vp, _vp, _i64, _vp]),
     "zero_loss_backward": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i32, _i32, _vp, _vp,
                                   _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp]),
+    "zero_gated_workspace": (_i32, [_i64, _i64, _i32, _vp, _vp]),
+    "zero_gated_forward": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _i32, _i64, _i64, _i32, _i32, _vp,
+                                  _i64, _vp, _vp, _i64, _vp]),
+    "zero_gated_backward": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _i32, _vp, _i64, _i64, _i64, _i32,
+                                   _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp]),
     "zero_clip_workspace": (_i32, [_i32, _vp, _vp]),
     "zero_clip_gradients": (_i32, [_i32, _vp, _vp, _i32, _vp, _f32, _f32, _vp, _vp, _vp, _vp, _i64,
                                    _vp]),
@@ -426,6 +432,35 @@ def zero_loss_backward(hidden, hidden_stride: int, weight, weight_stride: int, t
                                      _ptr(grad_weight), grad_weight_stride, _ptr(status),
                                      _ptr(workspace), workspace_bytes, _stream(stream)),
            "zero_loss_backward")
+
+
+def zero_gated_workspace(n_tokens: int, wide: int, dim: int):
+    """(forward bytes, backward bytes)."""
+    fwd, bwd = _i64(), _i64()
+    _check(load().zero_gated_workspace(n_tokens, wide, dim, C.byref(fwd), C.byref(bwd)),
+           "zero_gated_workspace")
+    return fwd.value, bwd.value
+
+
+def zero_gated_forward(x, x_stride: int, gate, gate_stride: int, up, up_stride: int, act: int,
+                       n_tokens: int, wide: int, dim: int, lp: int, out, out_stride: int, status,
+                       workspace, workspace_bytes: int, stream=None):
+    _check(load().zero_gated_forward(_ptr(x), x_stride, _ptr(gate), gate_stride, _ptr(up), up_stride,
+                                     act, n_tokens, wide, dim, lp, _ptr(out), out_stride,
+                                     _ptr(status), _ptr(workspace), workspace_bytes,
+                                     _stream(stream)), "zero_gated_forward")
+
+
+def zero_gated_backward(x, x_stride: int, gate, gate_stride: int, up, up_stride: int, act: int,
+                        grad_out, grad_out_stride: int, n_tokens: int, wide: int, dim: int, lp: int,
+                        grad_x, grad_x_stride: int, grad_gate, grad_gate_stride: int, grad_up,
+                        grad_up_stride: int, status, workspace, workspace_bytes: int, stream=None):
+    _check(load().zero_gated_backward(_ptr(x), x_stride, _ptr(gate), gate_stride, _ptr(up), up_stride,
+                                      act, _ptr(grad_out), grad_out_stride, n_tokens, wide, dim, lp,
+                                      _ptr(grad_x), grad_x_stride, _ptr(grad_gate),
+                                      grad_gate_stride, _ptr(grad_up), grad_up_stride, _ptr(status),
+                                      _ptr(workspace), workspace_bytes, _stream(stream)),
+           "zero_gated_backward")
 
 
 def zero_clip_workspace(lens) -> int:

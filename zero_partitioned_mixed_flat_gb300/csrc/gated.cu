@@ -1,0 +1,667 @@
+// gated.cu -- the gated projections of a feed-forward block and their gradients (sm_103a).
+//
+// With x [T, D], the matrices Wg and Wu [F, D], and p = act(g):
+//   g = x Wg^T,  u = x Wu^T,  out = act(g) u
+//   dg = go u act'(g),  du = go act(g)
+//   gx = dg Wg + du Wu,  gWg = dg^T x,  gWu = du^T x
+// Forward is one product whose tiles hold 128 columns of g and the same 128 of u: CTA 0 of
+// a pair loads the rows of Wg and CTA 1 those of Wu, which is how a pair's B operand
+// is split anyhow, so both sums of an element are in one row of tensor memory and neither g
+// nor u is ever stored.  Backward keeps nothing of the forward pass but x: it computes g
+// and u again (4 T D F operations beside the 8 of the gradients), writes dg and du in lp
+// and takes the three products in one launch: gx's sum runs over dg's columns and then du's.
+#include "head_internal.h"
+#include "launch.h"
+#include "per_device.h"
+#include "tile_product.cuh"
+#include "zero.h"
+#include "zero_internal.h"
+
+#include <algorithm>
+
+namespace zk {
+namespace {
+
+constexpr int kTileCost = 4;  // blocks of K that starting and storing a tile cost, about
+
+enum Mode { kForward = 0, kSlopes = 1, kGradients = 2 };
+enum Kind { kGates = 0, kGradX = 1, kGradGate = 2, kGradUp = 3 };
+
+// Blocks that look for the largest |grad_out|, two on each SM.
+constexpr int kTopBlocks = 304, kTopThreads = 256;
+
+struct GatedLayout {
+    int64_t rows;   // tokens rounded up to whole tiles
+    int splits;     // partial sums of grad_x
+    int64_t slope_gate, slope_up, sums, bytes;  // byte offsets
+};
+
+GatedLayout gated_layout(int64_t tokens, int64_t wide, int dim) {
+    GatedLayout l;
+    l.rows = up(std::max<int64_t>(tokens, 1), kTileM);
+    // grad_x has few tiles and long sums: cut its sums until no part is longer than a
+    // pair's share of all three gradients (at most 16 ways, 8 blocks of K each)
+    const int64_t dim_tiles = up(dim, kTileN) / kTileN, row_tiles = l.rows / kTileM;
+    const int64_t long_sum = 2 * (up(wide, kTileK) / kTileK), short_sum = up(tokens, kTileK) / kTileK;
+    const int64_t share = (row_tiles * dim_tiles * long_sum + 2 * (up(wide, kTileM) / kTileM) * dim_tiles * short_sum) / kPairs;
+    l.splits = 1;
+    while (l.splits < 16 && long_sum / l.splits > share && long_sum / (l.splits + 1) >= 8) ++l.splits;
+    int64_t at = up(kTopBlocks * 4, 1024);
+    auto take = [&](int64_t bytes) {
+        const int64_t here = at;
+        at = up(at + bytes, 1024);
+        return here;
+    };
+    l.slope_gate = take(tokens * wide * 2);
+    l.slope_up = take(tokens * wide * 2);
+    l.sums = take(l.splits > 1 ? l.splits * l.rows * dim * 4 : 0);
+    l.bytes = at;
+    return l;
+}
+
+// ----------------------------------------------------------------- activations
+
+__device__ __forceinline__ float rcp_approx(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// 1 / (1 + exp(-x)); 0 and 1 far out
+__device__ __forceinline__ float sigmoid(float x) { return rcp_approx(1.0f + exp2_approx(-x * kLog2e)); }
+
+constexpr float kTanhScale = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+constexpr float kTanhCube = 0.044715f;
+
+// Each activation is g P(g), its derivative P + g P'.
+//   silu       P = 1 / (1 + exp(-g))
+//   gelu       P = erfc(-g / sqrt(2)) / 2
+//   gelu_tanh  P = (1 + tanh(y)) / 2 = 1 / (1 + exp(-2 y)),  2 y = kTanhScale (g + kTanhCube g^3)
+template <int ACT>
+__device__ __forceinline__ float share_of(float g) {
+    if constexpr (ACT == ZERO_ACT_SILU) return sigmoid(g);
+    if constexpr (ACT == ZERO_ACT_GELU) return 0.5f * erfcf(g * -0.70710678118654752f);
+    return sigmoid(kTanhScale * __fmaf_rn(kTanhCube * g, g * g, g));
+}
+
+// P' by P
+template <int ACT>
+__device__ __forceinline__ float share_slope(float g, float p) {
+    if constexpr (ACT == ZERO_ACT_SILU) return p * (1.0f - p);
+    if constexpr (ACT == ZERO_ACT_GELU) return 0.3989422804014327f * exp2_approx(g * g * (-0.5f * kLog2e));
+    return p * (1.0f - p) * (kTanhScale * __fmaf_rn(3.0f * kTanhCube * g, g, 1.0f));
+}
+
+// out of n columns, g and u in place
+template <int ACT, int N>
+__device__ __forceinline__ void outs_of(const float (&g)[N], float (&u)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) u[i] = g[i] * share_of<ACT>(g[i]) * u[i];
+}
+
+// dg and du of n columns, in g's and u's place
+template <int ACT, int N>
+__device__ __forceinline__ void slopes_of(const float (&go)[N], float (&g)[N], float (&u)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float p = share_of<ACT>(g[i]);
+        const float slope = __fmaf_rn(g[i], share_slope<ACT>(g[i], p), p);
+        const float du = go[i] * (g[i] * p);
+        g[i] = go[i] * u[i] * slope;
+        u[i] = du;
+    }
+}
+
+// --------------------------------------------------------------------- products
+
+struct GatedParams {
+    CUtensorMap x_k;             // x: boxes 64 of D x 128 tokens
+    CUtensorMap gate_k, up_k;    // matrices: 64 of D x 128 of F
+    CUtensorMap out;             // out: 64 of F x 32 tokens
+    CUtensorMap x_mn;            // x: 64 of D x 64 tokens
+    CUtensorMap gate_mn, up_mn;  // matrices: 64 of D x 64 of F
+    CUtensorMap dg_out, du_out;  // slopes: 64 of F x 32 tokens
+    CUtensorMap dg_k, du_k;      // slopes: 64 of F x 128 tokens
+    CUtensorMap dg_mn, du_mn;    // slopes: 64 of F x 64 tokens
+    CUtensorMap gx_out;          // grad_x: 64 of D x 32 tokens, or the partial sums: 32 of D x 32 rows, float
+    CUtensorMap ggate_out, gup_out;  // 64 of D x 32 of F
+    long long tokens, rows;
+    int wide, dim, splits;
+    int act;
+    const uint4 *grad_out;
+    long long grad_stride;  // vectors
+    const float *tops;      // NULL: the slopes are not scaled
+    int *status;
+    long long wait_cycles;
+};
+
+// The work of one launch, and which of it each pair does, in order: every pair-th tile,
+// gradients first the tiles of grad_x, few and long; the pairs that get one fewer of
+// them then take `catch_up` tiles of the matrices' gradients each, about as long
+// together as one of the others; the rest of those goes round all pairs.
+template <int MODE>
+struct GatedWork {
+    Tiles gates, x, weight;
+    int pair, pairs, n_x, n_weight, weight_m;
+    int fuller, catch_up, mine;
+
+    __device__ __forceinline__ explicit GatedWork(const GatedParams &p) {
+        const int row_tiles = (int)((p.tokens + kTileM - 1) / kTileM);
+        pair = blockIdx.x >> 1;
+        pairs = gridDim.x >> 1;
+        if constexpr (MODE != kGradients) {
+            const int wide_tiles = (2 * p.wide + kTileN - 1) / kTileN;
+            gates.set(row_tiles, wide_tiles, 2 * p.wide, (p.dim + kTileK - 1) / kTileK, 1);
+        } else {
+            const int dim_tiles = (p.dim + kTileN - 1) / kTileN;
+            weight_m = (p.wide + kTileM - 1) / kTileM;
+            x.set(row_tiles, dim_tiles, p.dim, 2 * ((p.wide + kTileK - 1) / kTileK), p.splits);
+            weight.set(2 * weight_m, dim_tiles, p.dim, (int)((p.tokens + kTileK - 1) / kTileK), 1);
+            n_x = x.size();
+            n_weight = weight.size();
+            fuller = n_x % pairs;
+            const int long_tile = x.k_blocks / x.splits + kTileCost, short_tile = weight.k_blocks + kTileCost;
+            catch_up = fuller ? (long_tile + short_tile / 2) / short_tile : 0;
+            const int most = fuller ? n_weight / (pairs - fuller) : 0;
+            if (catch_up > most) catch_up = most;
+            mine = n_x > pair ? (n_x - pair + pairs - 1) / pairs : 0;
+        }
+    }
+
+    __device__ __forceinline__ bool at(int j, Tile &t) const {
+        if constexpr (MODE != kGradients) {
+            const int i = pair + j * pairs;
+            if (i >= gates.size()) return false;
+            t = gates.at(i, kGates);
+            return true;
+        }
+        if (j < mine) {
+            t = x.at(pair + j * pairs, kGradX);
+            return true;
+        }
+        j -= mine;
+        const int others = pairs - fuller;
+        int i;
+        if (catch_up && pair >= fuller && j < catch_up) {
+            i = pair - fuller + j * others;
+        } else {
+            if (catch_up && pair >= fuller) j -= catch_up;
+            i = catch_up * others + pair + j * pairs;
+        }
+        if (i >= n_weight) return false;
+        t = weight.at(i, kGradGate);
+        if (t.m0 >= weight_m * kTileM) {
+            t.m0 -= weight_m * kTileM;
+            t.kind = kGradUp;
+        }
+        return true;
+    }
+};
+
+template <bool BF16, int MODE>
+__device__ __forceinline__ Feed feed_of(const Tile &t, uint32_t stage0) {
+    return Feed(t.width, MODE == kGradients && t.kind != kGradX, MODE == kGradients, stage0, BF16);
+}
+
+// fp16 slopes are scaled by a power of two that puts the largest finite |grad_out| into
+// [1/4, 1/2): u act'(g) and act(g) may be 2^17 before a slope overflows, and what is
+// 2^-12 of the largest still has all its bits.  (bf16 has float's range.)  By a whole warp.
+__device__ __forceinline__ float scale_of(const float *tops) {
+    if (!tops) return 1.0f;
+    float top = 0.0f;
+    for (int i = threadIdx.x & 31; i < kTopBlocks; i += 32) top = fmaxf(top, tops[i]);
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    // top is 0 or an fp16 number: 2^-24 at least
+    return top > 0.0f ? __uint_as_float((252u - (__float_as_uint(top) >> 23)) << 23) : 1.0f;
+}
+
+template <bool BF16, int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kProductThreads, 1)
+gated_products(const __grid_constant__ GatedParams p) {
+    extern __shared__ unsigned char raw[];
+    __shared__ Shared sh;
+    unsigned char *smem = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t stage0 = smem_addr(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t rank;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            bar_init(smem_addr(&sh.full[s]), 1);
+            bar_init(smem_addr(&sh.empty[s]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            bar_init(smem_addr(&sh.acc_full[b]), 1);
+            bar_init(smem_addr(&sh.acc_empty[b]), 2 * kResultWarps);
+        }
+        bar_init(smem_addr(&sh.drained), 1);
+        sh.dead = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sh.tmem)),
+                     "r"(kTmemColumns)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    pdl_enter();
+
+    volatile int *dead = &sh.dead;
+    const long long limit = p.wait_cycles;
+    const GatedWork<MODE> work(p);
+    Tile t;
+
+    if (warp == 0) {
+        if (lane == 0) {  // ------------------------------------------ loads
+            int stage = 0, placed = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            Tile next;
+            bool more = work.at(0, t);
+            for (int j = 1; ok && more; ++j) {
+                more = false;
+                // this CTA's rows of A, and its half of the columns of B
+                const int m0 = t.m0 + (int)rank * kHalf, n0 = t.n0 + (int)rank * (t.width / 2);
+                const bool two = MODE != kGradients || t.width > kTileN / 2;  // boxes of 64 columns that hold its half
+                const uint32_t bytes = 2 * (two ? kBlockBytes : kBlockBytes - kBoxBytes);
+                const int half_k = MODE == kGradients ? (p.wide + kTileK - 1) / kTileK : 0;
+                for (int k = t.k0; k < t.k1; k += kStageBlocks) {
+                    ok = wait_for(&sh.empty[stage], phase ^ 1, dead, limit, p.status);
+                    if (!ok) break;
+                    const int blocks = t.k1 - k < kStageBlocks ? t.k1 - k : kStageBlocks;
+                    const uint32_t bar = in_cta(smem_addr(&sh.full[stage]), 0);
+                    sh.bytes[rank][stage] = blocks * bytes;
+                    if (rank == 0) bar_expect(smem_addr(&sh.full[stage]), blocks * bytes);
+                    for (int i = 0; i < blocks; ++i) {
+                        const uint32_t a = stage0 + stage * kStageBytes + i * kBlockBytes, b = a + kOperandBytes;
+                        if constexpr (MODE != kGradients) {
+                            const int kk = (k + i) * kTileK;
+                            tma_load(a, &p.x_k, kk, m0, bar);
+                            tma_load(b, rank == 0 ? &p.gate_k : &p.up_k, kk, t.n0 / 2, bar);
+                        } else if (t.kind == kGradX) {
+                            const bool second = k + i >= half_k;
+                            const int kk = (k + i - (second ? half_k : 0)) * kTileK;
+                            const CUtensorMap *w = second ? &p.up_mn : &p.gate_mn;
+                            tma_load(a, second ? &p.du_k : &p.dg_k, kk, m0, bar);
+                            tma_load(b, w, n0, kk, bar);
+                            if (two) tma_load(b + kBoxBytes, w, n0 + 64, kk, bar);
+                        } else {
+                            const int kk = (k + i) * kTileK;
+                            const CUtensorMap *s = t.kind == kGradGate ? &p.dg_mn : &p.du_mn;
+                            tma_load(a, s, m0, kk, bar);
+                            tma_load(a + kBoxBytes, s, m0 + 64, kk, bar);
+                            tma_load(b, &p.x_mn, n0, kk, bar);
+                            if (two) tma_load(b + kBoxBytes, &p.x_mn, n0 + 64, kk, bar);
+                        }
+                    }
+                    ++placed;
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                    // the divisions of the next tile's place, while loads are on their way
+                    if (k == t.k0) more = work.at(j, next);
+                }
+                t = next;
+            }
+            store_in_cta(&sh.placed[rank], 0, placed);
+            if (rank == 1)
+                for (int s = 0; s < kStages; ++s) store_in_cta(&sh.bytes[1][s], 0, sh.bytes[1][s]);
+        }
+    } else if (warp == 1) {
+        if (rank == 0 && lane == 0) {  // ------------------------- products
+            int stage = 0, buf = 0, consumed = 0;
+            uint32_t phase = 0, acc_phase = 0;
+            // as in loss.cu: this thread finds out what comes next while a stage is under way
+            bool ok = true, ready = false, vacant = false;
+            Tile after;
+            bool more = work.at(0, t);
+            Feed feed = feed_of<BF16, MODE>(t, stage0), feed_after;
+            for (int j = 1; ok && more; ++j) {
+                more = false;
+                if (!vacant) ok = wait_for(&sh.acc_empty[buf], acc_phase ^ 1, dead, limit, p.status);
+                if (!ok) break;
+                const uint32_t acc = tmem + buf * kTileN;
+                const uint32_t next_acc_phase = buf ? acc_phase ^ 1 : acc_phase;
+                vacant = false;
+                uint32_t add = 0;
+                for (int k = t.k0; k < t.k1; k += kStageBlocks) {
+                    if (!ready) ok = wait_for(&sh.full[stage], phase, dead, limit, p.status);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t a = feed.a + (uint32_t)stage * (kStageBytes >> 4), b = feed.b + (uint32_t)stage * (kStageBytes >> 4);
+                    feed.block(acc, a, b, add);
+                    if (k + 1 < t.k1) feed.block(acc, a + (kBlockBytes >> 4), b + (kBlockBytes >> 4), 1);
+                    mma_commit(smem_addr(&sh.empty[stage]));
+                    add = 1;
+                    ++consumed;
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1;
+                    }
+                    ready = bar_test(smem_addr(&sh.full[stage]), phase);
+                    if (k + kStageBlocks >= t.k1) vacant = bar_test(smem_addr(&sh.acc_empty[buf ^ 1]), next_acc_phase ^ 1);
+                    if (k == t.k0) {
+                        more = work.at(j, after);
+                        feed_after = feed_of<BF16, MODE>(after, stage0);
+                    }
+                }
+                if (!ok) break;
+                mma_commit(smem_addr(&sh.acc_full[buf]));
+                buf ^= 1;
+                acc_phase = next_acc_phase;
+                t.k0 = after.k0;
+                t.k1 = after.k1;
+                feed = feed_after;
+            }
+            sh.consumed = consumed;
+            // whoever gave up: no product reads shared memory or writes sums any more
+            mma_commit_here(smem_addr(&sh.drained));
+            if (!wait_out(&sh.drained, 0)) give_up(dead, p.status);
+        }
+    } else {  // ------------------------------------------------------ results
+        const int quad = warp & 3;              // the quarter of the lanes this warp may read
+        const int group = (warp - 2) >> 2;      // which half of the columns it takes
+        const uint32_t buffer = stage0 + kStages * kStageBytes + (warp - 2) * kStoreBytes;
+        const float scale = MODE == kForward ? 1.0f : scale_of(p.tops);
+        const float factor = 1.0f / scale;      // powers of two
+        int buf = 0;
+        uint32_t acc_phase = 0;
+        for (int j = 0; work.at(j, t); ++j) {
+            const int row0 = t.m0 + (int)rank * kHalf + quad * 32;  // this warp's first row of M
+            const bool got = wait_for(&sh.acc_full[buf], acc_phase, dead, limit, p.status);
+            if (!__all_sync(0xffffffffu, got)) break;
+            tc_fence_after();
+            const uint32_t acc = tmem + buf * kTileN + ((uint32_t)(quad * 32) << 16);
+            if constexpr (MODE == kForward) {
+                const int first = group * (kTileN / 4), f0 = t.n0 / 2 + first;  // 64 elements of each row
+                if (f0 < p.wide) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int c = 0; c < 64; c += 32) {
+                        float g[32], u[32];
+                        tmem_load32(acc + first + c, g);
+                        tmem_load32(acc + t.width / 2 + first + c, u);
+                        if (p.act == ZERO_ACT_SILU) outs_of<ZERO_ACT_SILU>(g, u);
+                        else if (p.act == ZERO_ACT_GELU) outs_of<ZERO_ACT_GELU>(g, u);
+                        else outs_of<ZERO_ACT_GELU_TANH>(g, u);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) w[c / 2 + i] = pack_lp<BF16>(u[2 * i], u[2 * i + 1]);
+                    }
+                    put_rows(w, buffer, lane, &p.out, f0, row0, false, row0 >= p.tokens);
+                }
+            } else if constexpr (MODE == kSlopes) {
+                const int first = group * (kTileN / 4), f0 = t.n0 / 2 + first;
+                const long long row = row0 + lane;
+                if (f0 < p.wide) {
+                    uint32_t w[32], z[32];
+#pragma unroll
+                    for (int c = 0; c < 64; c += 32) {
+                        float g[32], u[32], go[32];
+                        uint4 q[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int f = f0 + c + 8 * i;
+                            q[i] = row < p.tokens && f < p.wide ? __ldg(p.grad_out + row * p.grad_stride + f / 8) : make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        tmem_load32(acc + first + c, g);
+                        tmem_load32(acc + t.width / 2 + first + c, u);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float f[8];
+                            widen8<BF16>(q[i], f);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) go[8 * i + k] = f[k] * scale;
+                        }
+                        if (p.act == ZERO_ACT_SILU) slopes_of<ZERO_ACT_SILU>(go, g, u);
+                        else if (p.act == ZERO_ACT_GELU) slopes_of<ZERO_ACT_GELU>(go, g, u);
+                        else slopes_of<ZERO_ACT_GELU_TANH>(go, g, u);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            w[c / 2 + i] = pack_lp<BF16>(g[2 * i], g[2 * i + 1]);
+                            z[c / 2 + i] = pack_lp<BF16>(u[2 * i], u[2 * i + 1]);
+                        }
+                    }
+                    put_rows(w, buffer, lane, &p.dg_out, f0, row0, false, row0 >= p.tokens);
+                    put_rows(z, buffer, lane, &p.du_out, f0, row0, false, row0 >= p.tokens);
+                }
+            } else {
+                const int first = group * kResultColumns;
+                if (t.kind == kGradX && p.splits > 1) {
+                    for (int c = first; c < first + kResultColumns; c += 32) {
+                        float z[32];
+                        tmem_load32(acc + c, z);
+                        uint32_t w[32];
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(z[i] * factor);
+                        put_rows(w, buffer, lane, &p.gx_out, t.n0 + c, (int)(t.split * p.rows) + row0, false, t.n0 + c >= p.dim);
+                    }
+                } else {
+                    const CUtensorMap *to = t.kind == kGradX ? &p.gx_out : t.kind == kGradGate ? &p.ggate_out : &p.gup_out;
+                    const bool skip = row0 >= (t.kind == kGradX ? p.tokens : (long long)p.wide);
+                    for (int c = first; c < first + kResultColumns; c += 64) {
+                        uint32_t w[32];
+#pragma unroll
+                        for (int h = 0; h < 64; h += 32) {
+                            float z[32];
+                            tmem_load32(acc + c + h, z);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) w[h / 2 + i] = pack_lp<BF16>(z[2 * i] * factor, z[2 * i + 1] * factor);
+                        }
+                        put_rows(w, buffer, lane, to, t.n0 + c, row0, false, skip || t.n0 + c >= p.dim);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive_cluster(in_cta(smem_addr(&sh.acc_empty[buf]), 0));
+            buf ^= 1;
+            if (buf == 0) acc_phase ^= 1;
+        }
+        if (lane == 0) store_wait_all();
+    }
+    __syncwarp();
+    __syncthreads();
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    // as in loss.cu: after a wait that gave up, copies may still be on their way to either
+    // CTA's shared memory
+    if (*dead) {
+        if (rank == 0 && threadIdx.x == 0) {
+            FullBars bars{sh.full};
+            if (!drain_copies(sh.placed, sh.bytes, sh.consumed, bars)) atomicOr(p.status, ZERO_LOSS_TIMEOUT);
+        }
+        __syncwarp();
+        cluster_sync();
+    }
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemColumns) : "memory");
+}
+
+// ---------------------------------------------------------- the smaller kernels
+
+// The largest finite |grad_out| of a block's share of the rows, fp16.
+__global__ void __launch_bounds__(kTopThreads)
+gated_top(const uint4 *__restrict__ grad, long long stride, long long tokens, int vecs, float *tops) {
+    pdl_enter();
+    __shared__ uint32_t warp_top[kTopThreads / 32];
+    uint32_t top = 0u;
+    const auto look = [&](uint32_t w) {
+        const uint32_t lo = w & 0x7fffu, hi = w >> 16 & 0x7fffu;
+        top = max(top, max(lo < 0x7c00u ? lo : 0u, hi < 0x7c00u ? hi : 0u));
+    };
+    // a warp takes a row's stretch of 32 x 4 vectors at a time
+    const long long parts = (vecs + 127) / 128, all = parts * tokens;
+    const int lane = threadIdx.x & 31;
+    for (long long i = (long long)blockIdx.x * (kTopThreads / 32) + threadIdx.x / 32; i < all; i += (long long)gridDim.x * (kTopThreads / 32)) {
+        const long long t = i / parts;
+        const int v0 = (int)(i - t * parts) * 128 + lane;
+        uint4 q[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) q[k] = v0 + 32 * k < vecs ? grad[t * stride + v0 + 32 * k] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            look(q[k].x);
+            look(q[k].y);
+            look(q[k].z);
+            look(q[k].w);
+        }
+    }
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) warp_top[threadIdx.x / 32] = top;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < kTopThreads / 32; ++w) top = max(top, warp_top[w]);
+        tops[blockIdx.x] = __half2float(__ushort_as_half((unsigned short)top));
+    }
+}
+
+constexpr int kFinishThreads = 128;
+
+// grad_x of a token: its partial sums in order, rounded once
+template <bool BF16>
+__global__ void __launch_bounds__(kFinishThreads)
+gated_finish(const float4 *__restrict__ sums, long long tokens, long long rows, int splits, int vecs, uint4 *out, long long stride) {
+    pdl_enter();
+    for (long long t = blockIdx.x; t < tokens; t += gridDim.x)
+        for (int v = threadIdx.x; v < vecs; v += kFinishThreads) {
+            float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
+            for (int s = 0; s < splits; ++s) {
+                const float4 *src = sums + ((s * rows + t) * vecs + v) * 2;
+                const float4 a = src[0], b = src[1];
+                lo.x += a.x; lo.y += a.y; lo.z += a.z; lo.w += a.w;
+                hi.x += b.x; hi.y += b.y; hi.z += b.z; hi.w += b.w;
+            }
+            out[t * stride + v] = make_uint4(pack_lp<BF16>(lo.x, lo.y), pack_lp<BF16>(lo.z, lo.w), pack_lp<BF16>(hi.x, hi.y),
+                                             pack_lp<BF16>(hi.z, hi.w));
+        }
+}
+
+// ------------------------------------------------------------------------ host
+
+// Pairs of CTAs that run at once on the current device, their shared memory having been
+// allowed: or an error below zero.
+template <bool BF16, int MODE>
+int pairs_at_once() {
+    static PerDevice kept;
+    return kept.get([] {
+        const int set = done_or_error(
+            cudaFuncSetAttribute(gated_products<BF16, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes));
+        if (set < 0) return set;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2);
+        cfg.blockDim = dim3(kProductThreads);
+        cfg.dynamicSmemBytes = kSmemBytes;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int clusters = 0;
+        const int asked = done_or_error(cudaOccupancyMaxActiveClusters(&clusters, gated_products<BF16, MODE>, &cfg));
+        if (asked < 0) return asked;
+        return clusters > 0 ? clusters : -(int)cudaErrorInvalidConfiguration;
+    });
+}
+
+template <bool BF16, int MODE>
+cudaError_t launch_products(const GatedParams &p, int64_t tiles, cudaStream_t stream) {
+    const int pairs = pairs_at_once<BF16, MODE>();
+    if (pairs < 0) return (cudaError_t)-pairs;
+    if (tiles > 0x3fffffff) return cudaErrorInvalidValue;
+    const int64_t use = std::max<int64_t>(1, std::min<int64_t>(pairs, tiles));
+    return launch_pdl(gated_products<BF16, MODE>, dim3((unsigned)(2 * use)), dim3(kProductThreads), kSmemBytes, stream, p);
+}
+
+template <bool BF16>
+cudaError_t forward_impl(const GatedArgs &a, cudaStream_t stream) {
+    GatedParams p = {};
+    if (!encoder() || !make_map(&p.x_k, a.x, a.tokens, a.dim, a.x_stride, a.lp, false, kHalf) ||
+        !make_map(&p.gate_k, a.gate, a.wide, a.dim, a.gate_stride, a.lp, false, kHalf) ||
+        !make_map(&p.up_k, a.up, a.wide, a.dim, a.up_stride, a.lp, false, kHalf) ||
+        !make_map(&p.out, a.out, a.tokens, a.wide, a.out_stride, a.lp, false, 32))
+        return cudaErrorNotSupported;
+    p.tokens = a.tokens;
+    p.wide = a.wide;
+    p.dim = a.dim;
+    p.act = a.act;
+    p.splits = 1;
+    p.status = a.status;
+    p.wait_cycles = loss_wait();
+    return launch_products<BF16, kForward>(p, up(a.tokens, kTileM) / kTileM * (up(2 * a.wide, kTileN) / kTileN), stream);
+}
+
+template <bool BF16>
+cudaError_t backward_impl(const GatedArgs &a, cudaStream_t stream) {
+    const GatedLayout l = gated_layout(a.tokens, a.wide, a.dim);
+    char *ws = static_cast<char *>(a.workspace);
+    float *tops = reinterpret_cast<float *>(ws), *sums = reinterpret_cast<float *>(ws + l.sums);
+    void *dg = ws + l.slope_gate, *du = ws + l.slope_up;
+    GatedParams p = {};
+    const auto map = [&](CUtensorMap *m, const void *at, int64_t rows, int64_t cols, int64_t stride, int box) {
+        return make_map(m, at, rows, cols, stride, a.lp, false, box);
+    };
+    if (!encoder() || !map(&p.x_k, a.x, a.tokens, a.dim, a.x_stride, kHalf) || !map(&p.gate_k, a.gate, a.wide, a.dim, a.gate_stride, kHalf) ||
+        !map(&p.up_k, a.up, a.wide, a.dim, a.up_stride, kHalf) || !map(&p.x_mn, a.x, a.tokens, a.dim, a.x_stride, kTileK) ||
+        !map(&p.gate_mn, a.gate, a.wide, a.dim, a.gate_stride, kTileK) || !map(&p.up_mn, a.up, a.wide, a.dim, a.up_stride, kTileK) ||
+        !map(&p.dg_out, dg, a.tokens, a.wide, a.wide, 32) || !map(&p.du_out, du, a.tokens, a.wide, a.wide, 32) ||
+        !map(&p.dg_k, dg, a.tokens, a.wide, a.wide, kHalf) || !map(&p.du_k, du, a.tokens, a.wide, a.wide, kHalf) ||
+        !map(&p.dg_mn, dg, a.tokens, a.wide, a.wide, kTileK) || !map(&p.du_mn, du, a.tokens, a.wide, a.wide, kTileK) ||
+        !map(&p.ggate_out, a.grad_gate, a.wide, a.dim, a.grad_gate_stride, 32) ||
+        !map(&p.gup_out, a.grad_up, a.wide, a.dim, a.grad_up_stride, 32) ||
+        !(l.splits > 1 ? make_map(&p.gx_out, sums, l.splits * l.rows, a.dim, a.dim, a.lp, true, 32)
+                       : map(&p.gx_out, a.grad_x, a.tokens, a.dim, a.grad_x_stride, 32)))
+        return cudaErrorNotSupported;
+    p.tokens = a.tokens;
+    p.rows = l.rows;
+    p.wide = a.wide;
+    p.dim = a.dim;
+    p.splits = l.splits;
+    p.act = a.act;
+    p.grad_out = static_cast<const uint4 *>(a.grad_out);
+    p.grad_stride = a.grad_out_stride / 8;
+    p.tops = BF16 ? nullptr : tops;
+    p.status = a.status;
+    p.wait_cycles = loss_wait();
+    const int64_t row_tiles = l.rows / kTileM, dim_tiles = up(a.dim, kTileN) / kTileN;
+    cudaError_t e = cudaSuccess;
+    if (!BF16)
+        e = launch_pdl(gated_top, dim3(kTopBlocks), dim3(kTopThreads), 0, stream, p.grad_out, p.grad_stride, (long long)a.tokens, a.wide / 8, tops);
+    if (e == cudaSuccess) e = launch_products<BF16, kSlopes>(p, row_tiles * (up(2 * a.wide, kTileN) / kTileN), stream);
+    if (e == cudaSuccess)
+        e = launch_products<BF16, kGradients>(p, row_tiles * dim_tiles * l.splits + 2 * (up(a.wide, kTileM) / kTileM) * dim_tiles, stream);
+    if (e == cudaSuccess && l.splits > 1)
+        e = launch_pdl(gated_finish<BF16>, dim3((unsigned)std::min<int64_t>(a.tokens, 8 * sm_count())), dim3(kFinishThreads), 0, stream,
+                       reinterpret_cast<const float4 *>(sums), (long long)a.tokens, (long long)l.rows, l.splits, a.dim / 8,
+                       static_cast<uint4 *>(a.grad_x), (long long)(a.grad_x_stride / 8));
+    return e;
+}
+
+}  // namespace
+
+int64_t gated_forward_bytes(int64_t, int64_t, int) { return 0; }
+
+int64_t gated_backward_bytes(int64_t tokens, int64_t wide, int dim) { return gated_layout(tokens, wide, dim).bytes; }
+
+cudaError_t launch_gated_forward(const GatedArgs &a, cudaStream_t stream) {
+    return a.lp ? forward_impl<true>(a, stream) : forward_impl<false>(a, stream);
+}
+
+cudaError_t launch_gated_backward(const GatedArgs &a, cudaStream_t stream) {
+    if (a.tokens == 0) {  // no token: zero gradients of the matrices
+        const cudaError_t e = cudaMemset2DAsync(a.grad_gate, size_t(a.grad_gate_stride) * 2, 0, size_t(a.dim) * 2, size_t(a.wide), stream);
+        if (e != cudaSuccess) return e;
+        return cudaMemset2DAsync(a.grad_up, size_t(a.grad_up_stride) * 2, 0, size_t(a.dim) * 2, size_t(a.wide), stream);
+    }
+    return a.lp ? backward_impl<true>(a, stream) : backward_impl<false>(a, stream);
+}
+
+}  // namespace zk

@@ -108,6 +108,26 @@ zero_status loss_arguments(const void *hidden, int64_t hidden_stride, const void
     return ZERO_OK;
 }
 
+zero_status gated_shape(int64_t n_tokens, int64_t wide, int32_t dim, zero_lp lp) {
+    TRY(shape(n_tokens, dim, lp));
+    if (wide < 8 || wide >= (int64_t(1) << 30)) return refuse(ZERO_EINVAL, "wide %lld outside [8, 2^30)", (long long)wide);
+    if (wide % 8 != 0) return refuse(ZERO_EALIGN, "wide %lld is not a multiple of 8", (long long)wide);
+    return ZERO_OK;
+}
+
+zero_status gated_arguments(const void *x, int64_t x_stride, const void *gate, int64_t gate_stride, const void *up,
+                            int64_t up_stride, int32_t act, int64_t n_tokens, int64_t wide, int32_t dim, zero_lp lp,
+                            const int32_t *status) {
+    TRY(gated_shape(n_tokens, wide, dim, lp));
+    if (act != ZERO_ACT_SILU && act != ZERO_ACT_GELU && act != ZERO_ACT_GELU_TANH) return refuse(ZERO_EINVAL, "unknown act %d", act);
+    TRY(matrix("x", x, n_tokens, dim, x_stride));
+    TRY(matrix("gate", gate, wide, dim, gate_stride));
+    TRY(matrix("up", up, wide, dim, up_stride));
+    if (!status) return refuse(ZERO_EINVAL, "status is NULL");
+    if (!aligned(status, 4)) return refuse(ZERO_EALIGN, "status is not 4-byte aligned");
+    return ZERO_OK;
+}
+
 zero_status clip_lengths(int32_t n_tensors, const int64_t *lens) {
     if (n_tensors < 0 || (n_tensors > 0 && !lens)) return refuse(ZERO_EINVAL, "n_tensors < 0 or lens is NULL");
     for (int32_t i = 0; i < n_tensors; ++i)
@@ -232,6 +252,46 @@ zero_status zero_loss_backward(const void *hidden, int64_t hidden_stride, const 
                             nullptr, const_cast<float *>(lse), grad_loss, grad_hidden, grad_hidden_stride,
                             grad_weight, grad_weight_stride, status, workspace};
     return launched(zk::launch_loss_backward(a, static_cast<cudaStream_t>(stream)), "loss backward kernel launch");
+}
+
+zero_status zero_gated_workspace(int64_t n_tokens, int64_t wide, int32_t dim, int64_t *forward_bytes,
+                                 int64_t *backward_bytes) {
+    TRY(gated_shape(n_tokens, wide, dim, ZERO_BF16));
+    if (forward_bytes) *forward_bytes = zk::gated_forward_bytes(n_tokens, wide, dim);
+    if (backward_bytes) *backward_bytes = zk::gated_backward_bytes(n_tokens, wide, dim);
+    return ZERO_OK;
+}
+
+zero_status zero_gated_forward(const void *x, int64_t x_stride, const void *gate, int64_t gate_stride, const void *up,
+                               int64_t up_stride, int32_t act, int64_t n_tokens, int64_t wide, int32_t dim, zero_lp lp,
+                               void *out, int64_t out_stride, int32_t *status, void *workspace, int64_t workspace_bytes,
+                               void *stream) {
+    TRY(gated_arguments(x, x_stride, gate, gate_stride, up, up_stride, act, n_tokens, wide, dim, lp, status));
+    TRY(matrix("out", out, n_tokens, wide, out_stride));
+    TRY(scratch(workspace, workspace_bytes, zk::gated_forward_bytes(n_tokens, wide, dim)));
+    if (n_tokens == 0) return ZERO_OK;
+    zk::GatedArgs a = {x, x_stride, gate, gate_stride, up, up_stride, act, n_tokens, (int)wide, dim, lp, out, out_stride};
+    a.status = status;
+    a.workspace = workspace;
+    return launched(zk::launch_gated_forward(a, static_cast<cudaStream_t>(stream)), "gated kernel launch");
+}
+
+zero_status zero_gated_backward(const void *x, int64_t x_stride, const void *gate, int64_t gate_stride, const void *up,
+                                int64_t up_stride, int32_t act, const void *grad_out, int64_t grad_out_stride,
+                                int64_t n_tokens, int64_t wide, int32_t dim, zero_lp lp, void *grad_x,
+                                int64_t grad_x_stride, void *grad_gate, int64_t grad_gate_stride, void *grad_up,
+                                int64_t grad_up_stride, int32_t *status, void *workspace, int64_t workspace_bytes,
+                                void *stream) {
+    TRY(gated_arguments(x, x_stride, gate, gate_stride, up, up_stride, act, n_tokens, wide, dim, lp, status));
+    TRY(matrix("grad_out", grad_out, n_tokens, wide, grad_out_stride));
+    TRY(matrix("grad_x", grad_x, n_tokens, dim, grad_x_stride));
+    TRY(matrix("grad_gate", grad_gate, wide, dim, grad_gate_stride));
+    TRY(matrix("grad_up", grad_up, wide, dim, grad_up_stride));
+    TRY(scratch(workspace, workspace_bytes, zk::gated_backward_bytes(n_tokens, wide, dim)));
+    const zk::GatedArgs a = {x, x_stride, gate, gate_stride, up, up_stride, act, n_tokens, (int)wide, dim, lp, nullptr, 0,
+                             grad_out, grad_out_stride, grad_x, grad_x_stride, grad_gate, grad_gate_stride, grad_up,
+                             grad_up_stride, status, workspace};
+    return launched(zk::launch_gated_backward(a, static_cast<cudaStream_t>(stream)), "gated backward kernel launch");
 }
 
 zero_status zero_clip_workspace(int32_t n_tensors, const int64_t *lens, int64_t *bytes) {

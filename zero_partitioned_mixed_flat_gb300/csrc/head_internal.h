@@ -1,5 +1,5 @@
 // head_internal.h -- what the host side of the training-head calls (head.cpp)
-// passes to their kernels (norm.cu, loss.cu, clip.cu).  Every launch function
+// passes to their kernels (norm.cu, loss.cu, gated.cu, clip.cu).  Every launch function
 // gets checked arguments: pointers aligned as include/zero.h asks, strides and
 // dims multiples of 8 where it asks so.
 #pragma once
@@ -73,11 +73,41 @@ struct LossArgs {
     void *workspace;
 };
 void set_loss_wait(int64_t cycles);
+int64_t loss_wait();  // of every product's bounded waits
 cudaError_t launch_take_status(int32_t *status, int32_t *bits, cudaStream_t stream);
 int64_t loss_forward_bytes(int64_t tokens, int64_t vocab, int dim);
 int64_t loss_backward_bytes(int64_t tokens, int64_t vocab, int dim);
 cudaError_t launch_loss_forward(const LossArgs &a, cudaStream_t stream);
 cudaError_t launch_loss_backward(const LossArgs &a, cudaStream_t stream);
+
+struct GatedArgs {
+    const void *x;
+    int64_t x_stride;
+    const void *gate;
+    int64_t gate_stride;
+    const void *up;
+    int64_t up_stride;
+    int act;  // ZERO_ACT_*
+    int64_t tokens;
+    int wide, dim;
+    int lp;
+    void *out;  // forward
+    int64_t out_stride;
+    const void *grad_out;  // backward, with all that follows
+    int64_t grad_out_stride;
+    void *grad_x;
+    int64_t grad_x_stride;
+    void *grad_gate;
+    int64_t grad_gate_stride;
+    void *grad_up;
+    int64_t grad_up_stride;
+    int32_t *status;
+    void *workspace;
+};
+int64_t gated_forward_bytes(int64_t tokens, int64_t wide, int dim);
+int64_t gated_backward_bytes(int64_t tokens, int64_t wide, int dim);
+cudaError_t launch_gated_forward(const GatedArgs &a, cudaStream_t stream);
+cudaError_t launch_gated_backward(const GatedArgs &a, cudaStream_t stream);
 
 int64_t clip_bytes(int n, const int64_t *lens);
 cudaError_t launch_clip(int n, const void *const *grads, const int64_t *lens, int dtype, void *const *out,

@@ -31,6 +31,7 @@ from . import _abi as A
 
 _LP = {torch.float16: A.ZERO_FP16, torch.bfloat16: A.ZERO_BF16}
 _CLIP = {**_LP, torch.float32: A.ZERO_FP32}
+_ACTS = {"silu": A.ZERO_ACT_SILU, "gelu": A.ZERO_ACT_GELU, "gelu_tanh": A.ZERO_ACT_GELU_TANH}
 _STATUS = {}   # device index -> the int32 that every loss call of the process ORs into
 _STATUS_LOCK = threading.Lock()
 _HERE = contextlib.nullcontext()
@@ -111,8 +112,9 @@ def _status(device):
 
 def check_losses(device=None):
     """Waits for the device and raises if a linear_loss or linear_loss_backward
-    since the last check met a target outside the vocabulary (ZERO_EINVAL) or
-    gave up a bounded wait (ZERO_ETIMEOUT: its outputs are not valid).  All calls of
+    since the last check met a target outside the vocabulary (ZERO_EINVAL), or if one of
+    them or a gated_linear or gated_linear_backward gave up a bounded wait (ZERO_ETIMEOUT:
+    its outputs are not valid).  All calls of
     the process on the device report to the same check, whatever their stream or
     thread; what one sets while a check runs is left for the next."""
     device = torch.device("cuda" if device is None else device)
@@ -254,6 +256,56 @@ def linear_loss_backward(hidden, weight, targets, lse, grad_loss, ignore=-100, g
               vocab, dim, _LP[hidden.dtype], lse.data_ptr(), grad_loss.data_ptr(), grad_hidden.data_ptr(), ghs,
               grad_weight.data_ptr(), gws, status.data_ptr(), space.data_ptr(), need, A._stream(stream))
     return grad_hidden, grad_weight
+
+
+# ---- gated projections --------------------------------------------------------------
+
+def _gated_inputs(where, x, gate, up, activation):
+    if activation not in _ACTS:
+        _refuse(where, "activation is %r, expected one of %s" % (activation, ", ".join(_ACTS)))
+    tokens, dim, xs = _matrix(where, "x", x)
+    wide, across, gs = _matrix(where, "gate", gate, x.dtype)
+    if across != dim:
+        _refuse(where, "gate has rows of %d, x of %d" % (across, dim))
+    us = _matrix(where, "up", up, x.dtype, (wide, dim))[2]
+    return tokens, dim, wide, xs, gs, us
+
+
+def gated_linear(x, gate, up, activation="silu", stream=None):
+    """activation(x @ gate.T) * (x @ up.T), rounded once: the projections that open a
+    gated feed-forward block (gate, up: [wide, dim]; they may be halves of one matrix).
+    activation: "silu", "gelu" or "gelu_tanh".  Neither projection is stored; the backward
+    call takes x again.  check_losses also reports a wait that gave up here."""
+    where = "gated_linear"
+    tokens, dim, wide, xs, gs, us = _gated_inputs(where, x, gate, up, activation)
+    status = _status(x.device)
+    with _on(stream):
+        out = torch.empty((tokens, wide), dtype=x.dtype, device=x.device)
+        need = A.zero_gated_workspace(tokens, wide, dim)[0]
+        space = _scratch(need, x.device) if need else None
+        _call("zero_gated_forward", x.data_ptr(), xs, gate.data_ptr(), gs, up.data_ptr(), us, _ACTS[activation], tokens,
+              wide, dim, _LP[x.dtype], out.data_ptr(), wide, status.data_ptr(), _addr(space), need, A._stream(stream))
+    return out
+
+
+def gated_linear_backward(x, gate, up, grad_out, activation="silu", grad_x=None, grad_gate=None, grad_up=None, stream=None):
+    """(grad_x, grad_gate, grad_up) of gated_linear for the gradient of its output,
+    written into the given tensors if there are any (with rows like every matrix's)."""
+    where = "gated_linear_backward"
+    tokens, dim, wide, xs, gs, us = _gated_inputs(where, x, gate, up, activation)
+    gos = _matrix(where, "grad_out", grad_out, x.dtype, (tokens, wide))[2]
+    status = _status(x.device)
+    with _on(stream):
+        grad_x, grad_gate, grad_up = (_like(t) if g is None else g for g, t in ((grad_x, x), (grad_gate, gate), (grad_up, up)))
+        gxs = _matrix(where, "grad_x", grad_x, x.dtype, (tokens, dim))[2]
+        ggs = _matrix(where, "grad_gate", grad_gate, x.dtype, (wide, dim))[2]
+        gus = _matrix(where, "grad_up", grad_up, x.dtype, (wide, dim))[2]
+        need = A.zero_gated_workspace(tokens, wide, dim)[1]
+        space = _scratch(need, x.device)
+        _call("zero_gated_backward", x.data_ptr(), xs, gate.data_ptr(), gs, up.data_ptr(), us, _ACTS[activation],
+              grad_out.data_ptr(), gos, tokens, wide, dim, _LP[x.dtype], grad_x.data_ptr(), gxs, grad_gate.data_ptr(), ggs,
+              grad_up.data_ptr(), gus, status.data_ptr(), space.data_ptr(), need, A._stream(stream))
+    return grad_x, grad_gate, grad_up
 
 
 # ---- global norm, clipping, packing ----------------------------------------------
