@@ -660,6 +660,62 @@ zero_status zero_clip_gradients(int32_t n_tensors, const void *const *grads, con
                                 float *norm, float *coef, int32_t *nonfinite, void *workspace,
                                 int64_t workspace_bytes, void *stream);
 
+/* ----------------------------------------------------------------------
+ * One AdamW step over a list of tensors, without a plan: the update of one process that
+ * holds whole tensors (stage 0), or of a rank's partition as a list of one.  For every
+ * element of params[i], with g' = grads[i] * (coef * (1 / loss_scale)), t the step's number:
+ *   m = beta1 m + (1 - beta1) g',   v = beta2 v + (1 - beta2) g'^2
+ *   p = p * (1 - lr wd) - (lr m / (1 - beta1^t)) / (sqrt(v / (1 - beta2^t)) + eps)
+ *   copies[i] = round(p) in copy_type  (copies NULL: none)
+ * params: float tensors, updated in place; grads: of grad_dtype (ZERO_FP16, ZERO_BF16 or
+ * ZERO_FP32); lens[i] contiguous elements each, aligned to their element only, so any of
+ * them may be parts of flat buffers (clipped gradients as zero_clip_gradients packs them);
+ * lens[i] may be 0 (its pointers are then ignored).  A tensor may not be listed twice,
+ * and nothing may overlap.
+ * The moments of all tensors lie in m and v (16-byte aligned), tensor i's from element
+ * offsets[i] of zero_adamw_layout on: multiples of ZERO_QUANT_BLOCK, offsets[n_tensors]
+ * elements in all.  A new state is all zeros, and what lies between the tensors stays
+ * zero.  moments:
+ *  - ZERO_MOMENTS_FP32: floats.  Every operation is rounded on its own, in the
+ *    order of zero_adam_step: the same bits for the same coefficient, step and
+ *    constants.  m_scales and v_scales are ignored.
+ *  - ZERO_MOMENTS_8BIT: one byte an element, and a float scale (m_scales, v_scales) for every
+ *    ZERO_QUANT_BLOCK elements.  m[i] is an E4M3 code, m its value times the scale, which is the
+ *    block's largest |m| / 448.  v[i] is an unsigned code, the bits 5 to 12 of a binary16
+ *    number, whose value times the scale is the root of v; the scale is the block's largest root /
+ *    (1.96875 / 256).  The step itself uses the new m and root before they are rounded.  Each is
+ *    then rounded to one of its two neighbours at random, in proportion: by
+ *    h(i) = mix((i mod 2^32) ^ mix(mix(mix(seed) + t) + i / 2^32)), where i is the element's
+ *    place in m and mix takes x to x ^ x >> 16, that times 0x9E3779B1, then x ^ x >> 15, that
+ *    times 0xB504F333, then x ^ x >> 16 (all modulo 2^32): up where the fraction that is cut
+ *    off and ((h mod 2^16) + 1/2) / 2^16 (m) or (h / 2^16 + 1/2) / 2^16 (the root) make
+ *    one together.  A root above 0 has a code of at least 1, 2^-12 of the block's largest root.
+ *    A scale below 2^-126 is 0, and so are its codes.  A
+ *    block with a value that is not finite has a NaN scale and codes 0.
+ * record: two int64 of device memory (8-byte aligned), zero at first: record[0] is the
+ * number of steps taken, which the call counts up; record[1] belongs to the call.
+ * coef: a device float (zero_clip_gradients' coef where the gradients are not clipped yet),
+ * NULL: 1.  skip: a device int32 (zero_clip_gradients' nonfinite); where it is not 0
+ * nothing changes, and the step does not count.  NULL: never.
+ * beta1 and beta2 in [0, 1), lr, wd and eps finite, eps >= 0.  1 - beta, 1 - lr wd and the
+ * corrections are computed in double and rounded once.  Asynchronous, capturable (a
+ * replay is the next step), the same bits from run to run; steps of one state follow
+ * each other on a stream. */
+#define ZERO_MOMENTS_FP32 0
+#define ZERO_MOMENTS_8BIT 1
+zero_status zero_adamw_layout(int32_t n_tensors, const int64_t *lens, int64_t *offsets);
+zero_status zero_adamw_step(int32_t n_tensors, float *const *params, const void *const *grads,
+                            int32_t grad_dtype, void *const *copies, zero_lp copy_type,
+                            const int64_t *lens, int32_t moments, void *m, void *v,
+                            float *m_scales, float *v_scales, int64_t *record, double lr,
+                            double beta1, double beta2, double eps, double wd, float loss_scale,
+                            const float *coef, const int32_t *skip, int32_t seed, void *stream);
+/* The values of 8-bit moments, m and v (not its root), n_elems of each (a multiple of
+ * ZERO_QUANT_BLOCK: offsets[n_tensors] of the layout), rounded to dtype. */
+zero_status zero_adamw_values(const int8_t *m, const uint8_t *v, const float *m_scales,
+                              const float *v_scales, int64_t n_elems, int32_t dtype, void *m_out,
+                              void *v_out, void *stream);
+
 /* Frees the plan and its device scratch, after waiting for the plan's own
  * device work (the whole device once one of its calls was captured into a
  * graph).  NULL is allowed. */

@@ -24,19 +24,21 @@ from ._abi import (  # noqa: F401
     zero_norm_backward_workspace, zero_loss_workspace, zero_loss_set_wait_limit, zero_loss_take_status, zero_loss_forward, zero_loss_backward,
     zero_clip_workspace, zero_clip_gradients, ZERO_FP32, ZERO_HEAD_MAX_DIM, ZERO_LOSS_TIMEOUT,
     ZERO_LOSS_BAD_TARGET, zero_gated_workspace, zero_gated_forward, zero_gated_backward,
+    zero_adamw_layout, zero_adamw_step, zero_adamw_values, ZERO_MOMENTS_FP32, ZERO_MOMENTS_8BIT,
     ZERO_ACT_SILU, ZERO_ACT_GELU, ZERO_ACT_GELU_TANH,
 )
 from .plan import ZeroPlan  # noqa: F401
 
-# the training head on torch tensors (head.py), imported at first use: the rest of
-# the package does without torch
-_HEAD = ("check_losses", "clip_gradients", "dequantize_rows", "gated_linear", "gated_linear_backward", "linear_loss", "linear_loss_backward",
-         "residual_norm", "residual_norm_backward", "residual_norm_quantized")
+# the training head (head.py) and the step over tensors (adamw.py) on torch tensors, imported at
+# first use: the rest of the package does without torch
+_HEAD = ("check_losses", "clip_gradients", "dequantize_rows", "gated_linear", "gated_linear_backward", "gradient_norm",
+         "linear_loss", "linear_loss_backward", "residual_norm", "residual_norm_backward", "residual_norm_quantized")
+_ADAMW = ("AdamWState", "adamw_moments", "adamw_offsets", "adamw_state", "adamw_step")
 
 
 def __getattr__(name):
-    if name in _HEAD:
-        from . import head
-        globals().update((n, getattr(head, n)) for n in _HEAD)
+    if name in _HEAD or name in _ADAMW:
+        from . import adamw, head
+        globals().update((n, getattr(module, n)) for module, names in ((head, _HEAD), (adamw, _ADAMW)) for n in names)
         return globals()[name]
     raise AttributeError("module %r has no attribute %r" % (__name__, name))

@@ -25,6 +25,7 @@ ZERO_QUANT_INT8, ZERO_QUANT_FP8_E4M3 = 0, 1
 ZERO_FP32 = 2                     # an element type of zero_clip_gradients only
 ZERO_HEAD_MAX_DIM = 16384
 ZERO_LOSS_TIMEOUT, ZERO_LOSS_BAD_TARGET = 1, 2
+ZERO_MOMENTS_FP32, ZERO_MOMENTS_8BIT = 0, 1
 ZERO_ACT_SILU, ZERO_ACT_GELU, ZERO_ACT_GELU_TANH = 0, 1, 2
 
 # every exported entry point of include/zero.h, with its ctypes signature
@@ -82,6 +83,10 @@ SIGNATURES = {
     "zero_clip_workspace": (_i32, [_i32, _vp, _vp]),
     "zero_clip_gradients": (_i32, [_i32, _vp, _vp, _i32, _vp, _f32, _f32, _vp, _vp, _vp, _vp, _i64,
                                    _vp]),
+    "zero_adamw_layout": (_i32, [_i32, _vp, _vp]),
+    "zero_adamw_step": (_i32, [_i32, _vp, _vp, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp,
+                               _f64, _f64, _f64, _f64, _f64, _f32, _vp, _vp, _i32, _vp]),
+    "zero_adamw_values": (_i32, [_vp, _vp, _vp, _vp, _i64, _i32, _vp, _vp, _vp]),
     "zero_plan_destroy": (None, [_vp]),
     "zero_last_error": (C.c_char_p, []),
 }
@@ -484,3 +489,39 @@ def zero_clip_gradients(grads, lens, dtype: int, out, loss_scale: float, max_nor
                                       max_norm, _ptr(norm), _ptr(coef), _ptr(nonfinite),
                                       _ptr(workspace), workspace_bytes, _stream(stream)),
            "zero_clip_gradients")
+
+
+# ---- AdamW over a list of tensors ----------------------------------------------
+
+def zero_adamw_layout(lens) -> np.ndarray:
+    """The element of the moments where each tensor begins, and their length."""
+    ln = np.ascontiguousarray(lens, np.int64)
+    out = np.zeros(ln.size + 1, np.int64)
+    _check(load().zero_adamw_layout(int(ln.size), _ptr(ln), _ptr(out)), "zero_adamw_layout")
+    return out
+
+
+def _addresses(xs):
+    if xs is None or isinstance(xs, np.ndarray):
+        return xs
+    return np.array([_ptr(x) or 0 for x in xs], np.uint64)
+
+
+def zero_adamw_step(params, grads, grad_dtype: int, copies, copy_type: int, lens, moments: int, m, v,
+                    m_scales, v_scales, record, lr: float, beta1: float, beta2: float, eps: float,
+                    wd: float, loss_scale: float, coef, skip, seed: int = 0, stream=None):
+    """params, grads, copies (or None): one tensor or address per parameter, or uint64
+    arrays of addresses; lens: their element counts."""
+    ln = np.ascontiguousarray(lens, np.int64)
+    p, g, c = _addresses(params), _addresses(grads), _addresses(copies)
+    if p.size != ln.size or g.size != ln.size or (c is not None and c.size != ln.size):
+        raise ValueError("params, grads, copies and lens must have one entry per tensor")
+    _check(load().zero_adamw_step(int(ln.size), _ptr(p), _ptr(g), grad_dtype, _ptr(c), copy_type,
+                                  _ptr(ln), moments, _ptr(m), _ptr(v), _ptr(m_scales), _ptr(v_scales),
+                                  _ptr(record), lr, beta1, beta2, eps, wd, loss_scale, _ptr(coef),
+                                  _ptr(skip), seed, _stream(stream)), "zero_adamw_step")
+
+
+def zero_adamw_values(m, v, m_scales, v_scales, n_elems: int, dtype: int, m_out, v_out, stream=None):
+    _check(load().zero_adamw_values(_ptr(m), _ptr(v), _ptr(m_scales), _ptr(v_scales), n_elems, dtype,
+                                    _ptr(m_out), _ptr(v_out), _stream(stream)), "zero_adamw_values")

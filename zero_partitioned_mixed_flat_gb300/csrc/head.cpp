@@ -324,4 +324,73 @@ zero_status zero_clip_gradients(int32_t n_tensors, const void *const *grads, con
                     "clip kernel launch");
 }
 
+zero_status zero_adamw_layout(int32_t n_tensors, const int64_t *lens, int64_t *offsets) {
+    TRY(clip_lengths(n_tensors, lens));
+    if (!offsets) return refuse(ZERO_EINVAL, "offsets is NULL");
+    int64_t at = 0;
+    for (int32_t i = 0; i <= n_tensors; ++i) {
+        offsets[i] = at;
+        if (i < n_tensors) at += (lens[i] + ZERO_QUANT_BLOCK - 1) / ZERO_QUANT_BLOCK * ZERO_QUANT_BLOCK;
+        if (at > (int64_t(1) << 44)) return refuse(ZERO_EINVAL, "more than 2^44 elements");
+    }
+    return ZERO_OK;
+}
+
+zero_status zero_adamw_step(int32_t n_tensors, float *const *params, const void *const *grads, int32_t grad_dtype,
+                            void *const *copies, zero_lp copy_type, const int64_t *lens, int32_t moments, void *m, void *v,
+                            float *m_scales, float *v_scales, int64_t *record, double lr, double beta1, double beta2,
+                            double eps, double wd, float loss_scale, const float *coef, const int32_t *skip,
+                            int32_t seed, void *stream) {
+    TRY(clip_lengths(n_tensors, lens));
+    if (grad_dtype != ZERO_FP16 && grad_dtype != ZERO_BF16 && grad_dtype != ZERO_FP32)
+        return refuse(ZERO_EINVAL, "unknown grad_dtype %d", grad_dtype);
+    if (copies && copy_type != ZERO_FP16 && copy_type != ZERO_BF16) return refuse(ZERO_EINVAL, "unknown copy_type %d", int(copy_type));
+    if (moments != ZERO_MOMENTS_FP32 && moments != ZERO_MOMENTS_8BIT) return refuse(ZERO_EINVAL, "unknown moments format %d", moments);
+    if (n_tensors > 0 && (!params || !grads)) return refuse(ZERO_EINVAL, "params or grads is NULL");
+    const uintptr_t size = grad_dtype == ZERO_FP32 ? 4 : 2;
+    int64_t total = 0;
+    for (int32_t i = 0; i < n_tensors; ++i) {
+        if (lens[i] == 0) continue;
+        total += lens[i];
+        if (total > (int64_t(1) << 43)) return refuse(ZERO_EINVAL, "more than 2^43 elements");
+        if (!params[i] || !grads[i] || (copies && !copies[i]))
+            return refuse(ZERO_EINVAL, "params[%d], grads[%d] or copies[%d] is NULL", i, i, i);
+        if (!aligned(params[i], 4) || !aligned(grads[i], size) || (copies && !aligned(copies[i], 2)))
+            return refuse(ZERO_EALIGN, "params[%d], grads[%d] or copies[%d] is not aligned to its elements", i, i, i);
+    }
+    TRY(vector("m", m, total));
+    TRY(vector("v", v, total));
+    if (moments == ZERO_MOMENTS_8BIT) {
+        TRY(vector("m_scales", m_scales, total));
+        TRY(vector("v_scales", v_scales, total));
+    }
+    if (!record) return refuse(ZERO_EINVAL, "record is NULL");
+    if (!aligned(record, 8)) return refuse(ZERO_EALIGN, "record is not 8-byte aligned");
+    if (!aligned(coef, 4) || !aligned(skip, 4)) return refuse(ZERO_EALIGN, "coef or skip is not 4-byte aligned");
+    if (!std::isfinite(lr) || !std::isfinite(wd) || !(eps >= 0.0) || !std::isfinite(eps))
+        return refuse(ZERO_EINVAL, "lr, wd and eps must be finite and eps >= 0");
+    if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0)) return refuse(ZERO_EINVAL, "beta1 and beta2 must lie in [0, 1)");
+    if (!(loss_scale > 0.0f) || !std::isfinite(loss_scale)) return refuse(ZERO_EINVAL, "loss_scale must be finite and > 0");
+    const zk::AdamwArgs a = {n_tensors, params, grads, grad_dtype, copies, int(copy_type), lens, moments == ZERO_MOMENTS_8BIT,
+                             m, v, m_scales, v_scales, record, lr, beta1, beta2, eps, wd, loss_scale, coef, skip, (uint32_t)seed};
+    return launched(zk::launch_adamw_step(a, static_cast<cudaStream_t>(stream)), "adamw kernel launch");
+}
+
+zero_status zero_adamw_values(const int8_t *m, const uint8_t *v, const float *m_scales, const float *v_scales,
+                              int64_t n_elems, int32_t dtype, void *m_out, void *v_out, void *stream) {
+    if (n_elems < 0 || n_elems > (int64_t(1) << 44)) return refuse(ZERO_EINVAL, "n_elems outside [0, 2^44]");
+    if (n_elems % ZERO_QUANT_BLOCK != 0) return refuse(ZERO_EALIGN, "n_elems is not a multiple of %d", ZERO_QUANT_BLOCK);
+    if (dtype != ZERO_FP16 && dtype != ZERO_BF16 && dtype != ZERO_FP32) return refuse(ZERO_EINVAL, "unknown dtype %d", dtype);
+    TRY(vector("m", m, n_elems));
+    TRY(vector("v", v, n_elems));
+    TRY(vector("m_scales", m_scales, n_elems));
+    TRY(vector("v_scales", v_scales, n_elems));
+    TRY(vector("m_out", m_out, n_elems));
+    TRY(vector("v_out", v_out, n_elems));
+    if (n_elems == 0) return ZERO_OK;
+    return launched(zk::launch_adamw_values(m, v, m_scales, v_scales, n_elems / ZERO_QUANT_BLOCK, dtype, m_out, v_out,
+                                            static_cast<cudaStream_t>(stream)),
+                    "moments kernel launch");
+}
+
 }  // extern "C"

@@ -1,5 +1,6 @@
 // head_internal.h -- what the host side of the training-head calls (head.cpp)
-// passes to their kernels (norm.cu, loss.cu, gated.cu, clip.cu).  Every launch function
+// passes to their kernels (norm.cu, loss.cu, gated.cu, clip.cu,
+// adamw.cu).  Every launch function
 // gets checked arguments: pointers aligned as include/zero.h asks, strides and
 // dims multiples of 8 where it asks so.
 #pragma once
@@ -113,5 +114,27 @@ int64_t clip_bytes(int n, const int64_t *lens);
 cudaError_t launch_clip(int n, const void *const *grads, const int64_t *lens, int dtype, void *const *out,
                         float loss_scale, float max_norm, float *norm, float *coef, int32_t *nonfinite,
                         void *workspace, cudaStream_t stream);
+
+struct AdamwArgs {
+    int n;
+    float *const *params;
+    const void *const *grads;
+    int grad_dtype;
+    void *const *copies;  // NULL: none
+    int copy_type;
+    const int64_t *lens;
+    bool eight;  // the moments' format
+    void *m, *v;
+    float *m_scales, *v_scales;
+    int64_t *record;
+    double lr, beta1, beta2, eps, wd;
+    float loss_scale;
+    const float *coef;
+    const int32_t *skip;
+    uint32_t seed;
+};
+cudaError_t launch_adamw_step(const AdamwArgs &a, cudaStream_t stream);
+cudaError_t launch_adamw_values(const int8_t *m, const uint8_t *v, const float *m_scales, const float *v_scales,
+                                int64_t blocks, int dtype, void *m_out, void *v_out, cudaStream_t stream);
 
 }  // namespace zk

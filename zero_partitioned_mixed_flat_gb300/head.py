@@ -361,14 +361,31 @@ def clip_gradients(grads, out=None, offsets=None, max_norm=0.0, loss_scale=1.0, 
         into, dst = _gather(where, "out", out, dtype, device)
         if into != lens:
             _refuse(where, "out must hold one tensor of the same length per gradient")
+    return _clip(lens, src, _CLIP[dtype], dst.buffer_info()[0], loss_scale, max_norm, grads[0].device, stream)
+
+
+def gradient_norm(grads, max_norm=0.0, loss_scale=1.0, stream=None):
+    """clip_gradients' (norm, coef, nonfinite) of the gradients, which stay as they are: for a step
+    that takes the coefficient, such as adamw_step."""
+    where = "gradient_norm"
+    if not grads:
+        _refuse(where, "no gradients")
+    dtype = grads[0].dtype
+    if dtype not in _CLIP:
+        _refuse(where, "grads must be float16, bfloat16 or float32")
+    lens, src = _gather(where, "grads", grads, dtype, torch._C._cuda_getDevice())
+    return _clip(lens, src, _CLIP[dtype], None, loss_scale, max_norm, grads[0].device, stream)
+
+
+def _clip(lens, src, dtype, at_out, loss_scale, max_norm, device, stream):
     with _on(stream):
         at_lens, need = lens.buffer_info()[0], _i64()
-        _call("zero_clip_workspace", n, at_lens, byref(need))
-        found = torch.empty(3, dtype=torch.float32, device=grads[0].device)
+        _call("zero_clip_workspace", len(lens), at_lens, byref(need))
+        found = torch.empty(3, dtype=torch.float32, device=device)
         norm, coef, nonfinite = found.unbind()
         nonfinite = nonfinite.view(torch.int32)
-        space = _scratch(need.value, grads[0].device)
+        space = _scratch(need.value, device)
         at = found.data_ptr()
-        _call("zero_clip_gradients", n, src.buffer_info()[0], at_lens, _CLIP[dtype], dst.buffer_info()[0], loss_scale,
+        _call("zero_clip_gradients", len(lens), src.buffer_info()[0], at_lens, dtype, at_out, loss_scale,
               max_norm, at, at + 4, at + 8, space.data_ptr(), need.value, A._stream(stream))
     return norm, coef, nonfinite
