@@ -119,7 +119,8 @@ def test_small(t, d, f, dtype, act):
 
 @pytest.mark.parametrize("t,d,f,dtype,act", [
     (1, 4096, 1000, BF, "silu"), (4, 1600, 4264, FP, "gelu"), (7, 1600, 264, BF, "gelu_tanh"), (48, 1600, 4264, BF, "silu"),
-    (300, 4088, 72, FP, "silu"), (1023, 768, 2048, BF, "gelu"), (2100, 72, 1352, FP, "gelu_tanh"), (513, 264, 5000, BF, "silu"),
+    (300, 4088, 72, FP, "silu"), (64, 4096, 4264, BF, "gelu"), (65, 1600, 136, FP, "silu"), (16, 768, 11000, FP, "gelu_tanh"),
+    (31, 16384, 136, BF, "silu"), (1, 200, 40000, BF, "silu"), (1023, 768, 2048, BF, "gelu"), (2100, 72, 1352, FP, "gelu_tanh"), (513, 264, 5000, BF, "silu"),
 ])
 def test_larger(t, d, f, dtype, act):
     check(*case(t, d, f, dtype, std=0.03), act)
@@ -267,8 +268,9 @@ def test_against_differences(act):
         assert abs(float(slope - (got[k].double() * step).sum())) <= float((off * step.abs()).sum()) + 1e-7
 
 
-def test_a_wait_that_runs_out_is_reported():
-    x, gate, up, grad = case(300, 264, 520, BF)
+@pytest.mark.parametrize("t,d", [(300, 264), (40, 520), (3, 64)])
+def test_a_wait_that_runs_out_is_reported(t, d):
+    x, gate, up, grad = case(t, d, 520, BF)
     want = Z.gated_linear(x, gate, up)
     Z.check_losses()
     Z.zero_loss_set_wait_limit(0)

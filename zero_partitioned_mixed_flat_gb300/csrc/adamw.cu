@@ -30,13 +30,22 @@
 namespace zk {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBlock = ZERO_QUANT_BLOCK;  // a warp's 32 lanes x 4
-// Blocks of 128 that a warp has in flight: 16 or 8 elements a lane.
+// Blocks of 128 that a warp has in flight, 16 or 12 elements a lane, in one block of 16 warps on an
+// SM.  More warps with less in flight each are slower: 117M elements with 32-bit moments 525 us
+// so, 541 and 617 us with two and three blocks of 256 that take 2 at a time, 982 us with
+// eight that take 1; 124M with 8-bit moments and their values 451 us, 465 with two
+// blocks of 256, 481 and 532 where they take 3 and 2 at a time.
 template <int BITS>
-constexpr int kDepth = BITS == 8 ? 4 : 2;
+constexpr int kDepth = BITS == 8 ? 4 : 3;
 template <int BITS>
 constexpr int kChunkBlocks = kWarps * kDepth<BITS>;  // blocks of 128 of a chunk
+// Whether a chunk's lines are asked for while the one before is at work: 8-bit moments, whose
+// arithmetic takes about as long as their copies (124M elements 520 us without it; with
+// 32-bit moments 4 % slower with it).
+template <int BITS>
+constexpr bool kAhead = BITS == 8;
 // Tensors of one launch: the table is a kernel parameter, 44 bytes a tensor.
 constexpr int kShort = 64, kTable = 640;
 
@@ -85,29 +94,35 @@ __host__ __device__ __forceinline__ uint32_t mix(uint32_t x) {
 
 // ------------------------------------------------------------------------ codes
 
-// A code with MANTISSA bits below the leading one, normal from 2^LOW on, of y >= 0 (at
-// most the largest code's value, but for a rounding): the float's bits from the last kept
-// one on, after adding 16 random bits below it.  Below 2^LOW, where steps are
-// equal, y + 2^LOW has the same steps.
+// Codes with MANTISSA bits below the leading one, normal from 2^LOW on, of y >= 0 (at
+// most the largest code's value, but for a rounding), each rounded by 16 random bits.
+// y 2^(-126 - LOW) has float's own subnormal numbers where the code has its: its bits
+// from the last kept one on are the code, after adding the random bits below that.
 template <int MANTISSA, int LOW>
-__device__ __forceinline__ uint32_t random_code(float y, uint32_t random16) {
+__device__ __forceinline__ uint32_t random_code(float y, uint32_t random16, uint32_t most) {
     constexpr int kDrop = 23 - MANTISSA;
-    constexpr uint32_t kFirst = (uint32_t)(127 + LOW) << MANTISSA;  // 2^LOW's kept bits
-    constexpr float kLow = LOW == -6 ? 0x1p-6f : 0x1p-14f;
     static_assert(LOW == -6 || LOW == -14, "");
-    const bool below = y < kLow;
-    const uint32_t bits = __float_as_uint(below ? y + kLow : y);
-    const uint32_t kept = (bits + (random16 << (kDrop - 16)) + (1u << (kDrop - 17))) >> kDrop;
-    return kept - (below ? kFirst : kFirst - (1u << MANTISSA));
+    const float z = y * (LOW == -6 ? 0x1p-120f : 0x1p-112f);
+    return min((__float_as_uint(z) + (random16 << (kDrop - 16)) + (1u << (kDrop - 17))) >> kDrop, most);
+}
+
+__device__ __forceinline__ uint32_t pack_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+
+// the larger of a and |b|; NaN if either is
+__device__ __forceinline__ float larger(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+    return r;
 }
 
 // the scale of a block whose largest magnitude has these bits, and its reciprocal
 __device__ __forceinline__ float scale_of(uint32_t top_bits, float per_top, float &inverse) {
-    const float top = __uint_as_float(top_bits);
-    float s = top * per_top;
-    if (!(s >= kLeastScale)) s = 0.0f;
+    float s = __uint_as_float(top_bits) * per_top;
+    s = s >= kLeastScale ? s : 0.0f;
     if (top_bits >= 0x7f800000u) s = __int_as_float(0x7fffffff);  // an infinity or NaN: all of the block reads as NaN
-    inverse = s >= kLeastScale ? __frcp_rn(s) : 0.0f;
+    inverse = s >= kLeastScale ? rcp_approx(s) : 0.0f;
     return s;
 }
 
@@ -138,40 +153,62 @@ __device__ __forceinline__ float sqrt_approx(float x) {
 
 // --------------------------------------------------------------------- elements
 
+// Four consecutive gradients as loaded, widened only once they are needed.
 template <int TYPE>
 struct Grad {
     static constexpr int kBytes = TYPE == ZERO_FP32 ? 4 : 2;
-    using Four = typename std::conditional<TYPE == ZERO_FP32, uint4, uint2>::type;
+    // 16 bits: two words, or three where the first element is the upper half of a word
+    static constexpr int kWords = TYPE == ZERO_FP32 ? 4 : 3;
+    uint32_t w[kWords];
 
-    // elements [i, len) of up to four, zeros behind them
-    static __device__ __forceinline__ Four few(const void *p, long long i, long long len) {
+    // all four there, aligned together or (16 bits) with another element behind them
+    template <bool TOGETHER>
+    __device__ __forceinline__ void load(const char *p) {
         if constexpr (TYPE == ZERO_FP32) {
-            const uint32_t *w = static_cast<const uint32_t *>(p) + i;
-            return make_uint4(w[0], i + 1 < len ? w[1] : 0u, i + 2 < len ? w[2] : 0u, i + 3 < len ? w[3] : 0u);
+            if constexpr (TOGETHER) {
+                const uint4 q = __ldcs(reinterpret_cast<const uint4 *>(p));
+                w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w[k] = __ldcs(reinterpret_cast<const uint32_t *>(p) + k);
+            }
+        } else if constexpr (TOGETHER) {
+            const uint2 q = __ldcs(reinterpret_cast<const uint2 *>(p));
+            w[0] = q.x; w[1] = q.y; w[2] = 0u;
         } else {
-            const uint16_t *w = static_cast<const uint16_t *>(p) + i;
-            const uint32_t lo = i + 1 < len ? w[1] : 0, mid = i + 2 < len ? w[2] : 0, hi = i + 3 < len ? w[3] : 0;
-            return make_uint2(w[0] | lo << 16, mid | hi << 16);
+            const bool upper = reinterpret_cast<uintptr_t>(p) & 2u;
+            const uint32_t *q = reinterpret_cast<const uint32_t *>(p - (upper ? 2 : 0));
+            w[0] = __ldcs(q);
+            w[1] = __ldcs(q + 1);
+            w[2] = upper ? __ldcs(q + 2) : 0u;
         }
     }
-    static __device__ __forceinline__ Four none() {
-        if constexpr (TYPE == ZERO_FP32) return make_uint4(0u, 0u, 0u, 0u);
-        else return make_uint2(0u, 0u);
-    }
-    static __device__ __forceinline__ void widen(Four q, float f[4]) {
+    // `left` of them there, zeros behind
+    __device__ __forceinline__ void few(const char *p, long long left) {
+        const bool upper = kBytes == 2 && (reinterpret_cast<uintptr_t>(p) & 2u);
         if constexpr (TYPE == ZERO_FP32) {
-            f[0] = __uint_as_float(q.x);
-            f[1] = __uint_as_float(q.y);
-            f[2] = __uint_as_float(q.z);
-            f[3] = __uint_as_float(q.w);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = k < left ? reinterpret_cast<const uint32_t *>(p)[k] : 0u;
         } else {
-            from_lp4<TYPE == ZERO_BF16>(q, f);
+            uint32_t h[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) h[k] = k < left ? reinterpret_cast<const uint16_t *>(p)[k] : 0u;
+            w[0] = upper ? h[0] << 16 : h[0] | h[1] << 16;
+            w[1] = upper ? h[1] | h[2] << 16 : h[2] | h[3] << 16;
+            w[2] = upper ? h[3] : 0u;
+        }
+    }
+    template <bool TOGETHER>
+    __device__ __forceinline__ void widen(const char *p, float f[4]) const {
+        if constexpr (TYPE == ZERO_FP32) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) f[k] = __uint_as_float(w[k]);
+        } else {
+            const uint32_t by = TOGETHER ? 0u : (uint32_t)(reinterpret_cast<uintptr_t>(p) & 2u) * 8u;
+            from_lp4<TYPE == ZERO_BF16>(make_uint2(__funnelshift_r(w[0], w[1], by), __funnelshift_r(w[1], w[2], by)), f);
         }
     }
 };
-
-__device__ __forceinline__ uint4 stream_load(const uint4 *p) { return __ldcs(p); }
-__device__ __forceinline__ uint2 stream_load(const uint2 *p) { return __ldcs(p); }
 
 // One tensor of the table: what a chunk needs of it.
 struct Piece {
@@ -179,7 +216,8 @@ struct Piece {
     const void *g;
     void *copy;
     long long len, block0, first;  // first: the chunk's first block within the tensor
-    bool vectors;                  // p, g and copy are aligned to four elements
+    bool vectors;                  // p and copy are aligned to four elements
+    bool together;                 // and g
 };
 
 // COPY: the copies' type, or -1
@@ -197,41 +235,9 @@ __device__ __forceinline__ Piece piece_of(const AdamwParams<TABLE> &t, int chunk
     q.len = t.len[i];
     q.block0 = t.block0[i];
     q.first = (long long)(chunk - t.chunk0[i]) * chunk_blocks;
-    q.vectors = ((reinterpret_cast<uintptr_t>(q.p) & 15u) | (reinterpret_cast<uintptr_t>(q.g) & (4 * Grad<GRAD>::kBytes - 1)) |
-                 (reinterpret_cast<uintptr_t>(q.copy) & 7u)) == 0;
+    q.vectors = ((reinterpret_cast<uintptr_t>(q.p) & 15u) | (reinterpret_cast<uintptr_t>(q.copy) & 7u)) == 0;
+    q.together = (reinterpret_cast<uintptr_t>(q.g) & (4 * Grad<GRAD>::kBytes - 1)) == 0;
     return q;
-}
-
-// A thread's four elements of a block, as loaded.
-template <int GRAD>
-__device__ __forceinline__ void take(const Piece &q, long long e, float4 &p, typename Grad<GRAD>::Four &g) {
-    if (q.vectors && e + 4 <= q.len) {
-        p = __ldcs(reinterpret_cast<const float4 *>(q.p + e));
-        g = stream_load(reinterpret_cast<const typename Grad<GRAD>::Four *>(static_cast<const char *>(q.g) + e * Grad<GRAD>::kBytes));
-    } else if (e < q.len) {
-        p = make_float4(q.p[e], e + 1 < q.len ? q.p[e + 1] : 0.0f, e + 2 < q.len ? q.p[e + 2] : 0.0f, e + 3 < q.len ? q.p[e + 3] : 0.0f);
-        g = Grad<GRAD>::few(q.g, e, q.len);
-    } else {
-        p = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        g = Grad<GRAD>::none();
-    }
-}
-
-template <int COPY>
-__device__ __forceinline__ void put(const Piece &q, long long e, const float p[4]) {
-    if (q.vectors && e + 4 <= q.len) {
-        __stcs(reinterpret_cast<float4 *>(q.p + e), make_float4(p[0], p[1], p[2], p[3]));
-        if constexpr (COPY >= 0)
-            __stcs(reinterpret_cast<uint2 *>(static_cast<uint16_t *>(q.copy) + e),
-                   make_uint2(to_lp2_packed<COPY == ZERO_BF16>(p[0], p[1]), to_lp2_packed<COPY == ZERO_BF16>(p[2], p[3])));
-    } else {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (e + k >= q.len) break;
-            q.p[e + k] = p[k];
-            if constexpr (COPY >= 0) static_cast<uint16_t *>(q.copy)[e + k] = (uint16_t)to_lp2_packed<COPY == ZERO_BF16>(p[k], 0.0f);
-        }
-    }
 }
 
 // What one step needs of its number and the device's decisions.
@@ -241,8 +247,176 @@ struct StepScalars {
     int skip;
 };
 
+// A warp's N blocks of 128 of one tensor, a lane four elements of each: loaded all at
+// once, then updated and stored one after the other.  FORM: kWhole, all of them exist and
+// are whole, parameters and copies are aligned, and no 2^32 lies between their places;
+// kTogether, the gradients are aligned too, else another element stands behind them; kAny,
+// whatever there is.
+enum Form { kAny, kWhole, kTogether };
+
+template <int BITS, int GRAD, int COPY, int FORM>
+struct Span {
+    static constexpr int N = kDepth<BITS>;
+    static constexpr bool FULL = FORM != kAny;
+    float *p;          // this lane's first element, and the same place in the others
+    const char *g;
+    uint16_t *copy;
+    long long e, len;  // elements of the tensor before it, and in all
+    long long block;   // the first block's place in the state
+    int blocks;        // that exist
+    bool vectors;
+    float4 p4[N];
+    Grad<GRAD> g4[N];
+    float4 m4[BITS == 32 ? N : 1], v4[BITS == 32 ? N : 1];
+    uint32_t mc[BITS == 8 ? N : 1], vc[BITS == 8 ? N : 1];
+    float ms[BITS == 8 ? N : 1], vs[BITS == 8 ? N : 1];
+
+    __device__ __forceinline__ Span(const Piece &q, long long b0, int lane) {
+        e = b0 * kBlock + lane * 4;
+        p = q.p + e;
+        g = static_cast<const char *>(q.g) + e * Grad<GRAD>::kBytes;
+        copy = COPY >= 0 ? static_cast<uint16_t *>(q.copy) + e : nullptr;
+        len = q.len;
+        block = q.block0 + b0;
+        const long long left = (q.len + kBlock - 1) / kBlock - b0;
+        blocks = FULL || left > N ? N : (int)left;
+        vectors = q.vectors;
+    }
+
+    __device__ __forceinline__ void load(const Moments &s, int lane) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (!FULL && i >= blocks) break;
+            if constexpr (BITS == 32) {
+                m4[i] = __ldcs(static_cast<const float4 *>(s.m) + block * 32 + lane + i * 32);
+                v4[i] = __ldcs(static_cast<const float4 *>(s.v) + block * 32 + lane + i * 32);
+            } else {
+                mc[i] = __ldcs(static_cast<const uint32_t *>(s.m) + block * 32 + lane + i * 32);
+                vc[i] = __ldcs(static_cast<const uint32_t *>(s.v) + block * 32 + lane + i * 32);
+                ms[i] = s.m_scales[block + i];
+                vs[i] = s.v_scales[block + i];
+            }
+            const long long at = e + i * kBlock;
+            const float *from = p + i * kBlock;
+            const char *grad = g + i * kBlock * Grad<GRAD>::kBytes;
+            if (FULL || (vectors && at + 4 <= len))
+                p4[i] = __ldcs(reinterpret_cast<const float4 *>(from));
+            else
+                p4[i] = make_float4(at < len ? from[0] : 0.0f, at + 1 < len ? from[1] : 0.0f, at + 2 < len ? from[2] : 0.0f,
+                                    at + 3 < len ? from[3] : 0.0f);
+            if (FULL || at + 5 <= len)
+                g4[i].template load<FORM == kTogether>(grad);
+            else
+                g4[i].few(grad, len - at);
+        }
+    }
+
+    __device__ __forceinline__ void put(int i, const float (&w)[4]) const {
+        const long long at = e + i * kBlock;
+        float *to = p + i * kBlock;
+        if (FULL || (vectors && at + 4 <= len)) {
+            __stcs(reinterpret_cast<float4 *>(to), make_float4(w[0], w[1], w[2], w[3]));
+            if constexpr (COPY >= 0)
+                __stcs(reinterpret_cast<uint2 *>(copy) + i * 32,
+                       make_uint2(to_lp2_packed<COPY == ZERO_BF16>(w[0], w[1]), to_lp2_packed<COPY == ZERO_BF16>(w[2], w[3])));
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (at + k >= len) break;
+                to[k] = w[k];
+                if constexpr (COPY >= 0) copy[i * kBlock + k] = (uint16_t)to_lp2_packed<COPY == ZERO_BF16>(w[k], 0.0f);
+            }
+        }
+    }
+
+    __device__ __forceinline__ void step(const Moments &st, const AdamwScalars &c, const StepScalars &s, float lr1, float rs2, int lane) {
+        uint32_t key = BITS == 8 ? mix(s.key + (uint32_t)((unsigned long long)block * kBlock >> 32)) : 0u;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (!FULL && i >= blocks) break;
+            float w[4] = {p4[i].x, p4[i].y, p4[i].z, p4[i].w}, grad[4];
+            g4[i].template widen<FORM == kTogether>(g, grad);
+            if constexpr (BITS == 32) {
+                float m[4] = {m4[i].x, m4[i].y, m4[i].z, m4[i].w}, v[4] = {v4[i].x, v4[i].y, v4[i].z, v4[i].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    // every operation rounded on its own, in zero_adam_step's order
+                    const float f = __fmul_rn(grad[k], s.factor);
+                    m[k] = __fadd_rn(__fmul_rn(c.beta1, m[k]), __fmul_rn(c.omb1, f));
+                    v[k] = __fadd_rn(__fmul_rn(c.beta2, v[k]), __fmul_rn(c.omb2, __fmul_rn(f, f)));
+                    const float denom = __fadd_rn(__fsqrt_rn(__fdiv_rn(v[k], s.bc2)), c.eps);
+                    const float update = __fdiv_rn(__fmul_rn(c.lr, __fdiv_rn(m[k], s.bc1)), denom);
+                    w[k] = __fsub_rn(__fmul_rn(w[k], c.decay), update);
+                }
+                __stcs(static_cast<float4 *>(st.m) + block * 32 + lane + i * 32, make_float4(m[0], m[1], m[2], m[3]));
+                __stcs(static_cast<float4 *>(st.v) + block * 32 + lane + i * 32, make_float4(v[0], v[1], v[2], v[3]));
+                put(i, w);
+            } else {
+                // What lies behind a tensor's end has gradient and codes 0, and keeps them.
+                float m[4], r[4], top_m = 0.0f, top_r = 0.0f;
+                m_values(mc[i], m);
+                root_values(vc[i], r);
+                const float old_m = c.beta1 * ms[i];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float f = grad[k] * s.factor, root = r[k] * vs[i];
+                    m[k] = __fmaf_rn(old_m, m[k], c.omb1 * f);
+                    r[k] = sqrt_approx(__fmaf_rn(c.beta2, root * root, c.omb2 * (f * f)));
+                    w[k] = __fmaf_rn(w[k], c.decay, -(lr1 * m[k] * rcp_approx(__fmaf_rn(r[k], rs2, c.eps))));
+                    top_m = larger(top_m, m[k]);
+                    top_r = larger(top_r, r[k]);
+                }
+                put(i, w);
+                const uint32_t bits_m = __reduce_max_sync(0xffffffffu, __float_as_uint(top_m));
+                const uint32_t bits_r = __reduce_max_sync(0xffffffffu, __float_as_uint(top_r));
+                float inv_m, inv_r;
+                const float scale_m = scale_of(bits_m, 1.0f / kTopM, inv_m), scale_r = scale_of(bits_r, 1.0f / kTopR, inv_r);
+                const unsigned long long place = (unsigned long long)(block + i) * kBlock;
+                if (!FULL && i > 0 && (uint32_t)place == 0u) key = mix(s.key + (uint32_t)(place >> 32));
+                uint32_t cm[4], cr[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t random = mix(((uint32_t)place + lane * 4 + k) ^ key);
+                    cm[k] = random_code<3, -6>(fabsf(m[k]) * inv_m, random & 0xffffu, 126u);
+                    cr[k] = random_code<5, -14>(r[k] * inv_r, random >> 16, 255u);
+                    cr[k] = max(cr[k], r[k] > 0.0f ? 1u : 0u);
+                }
+                uint32_t new_m = pack_bytes(cm[0], cm[1], cm[2], cm[3]), new_r = pack_bytes(cr[0], cr[1], cr[2], cr[3]);
+                const uint32_t signs = __byte_perm(__byte_perm(__float_as_uint(m[0]), __float_as_uint(m[1]), 0x0073),
+                                                   __byte_perm(__float_as_uint(m[2]), __float_as_uint(m[3]), 0x0073), 0x5410);
+                new_m |= signs & 0x80808080u;
+                if (!(scale_m > 0.0f)) new_m = 0u;
+                if (!(scale_r > 0.0f)) new_r = 0u;
+                __stcs(static_cast<uint32_t *>(st.m) + block * 32 + lane + i * 32, new_m);
+                __stcs(static_cast<uint32_t *>(st.v) + block * 32 + lane + i * 32, new_r);
+                if (lane == 0) {
+                    st.m_scales[block + i] = scale_m;
+                    st.v_scales[block + i] = scale_r;
+                }
+            }
+        }
+    }
+};
+
+// Asks L2 for the lines of a warp's N blocks: the next chunk's, while this one's are at work.
+template <int BITS, int GRAD, int N>
+__device__ __forceinline__ void ask_ahead(const Piece &q, long long b0, const Moments &s, int lane) {
+    constexpr int kP = 4, kG = Grad<GRAD>::kBytes, kM = BITS / 8, kLines = kP + kG + 2 * kM;  // of 128 bytes, of a block
+#pragma unroll
+    for (int j = 0; j < (N * kLines + 31) / 32; ++j) {
+        const int l = lane + 32 * j, i = l / kLines, line = l % kLines;
+        if (i >= N || (b0 + i + 1) * kBlock > q.len) break;
+        const char *at;
+        if (line < kP) at = reinterpret_cast<const char *>(q.p + (b0 + i) * kBlock) + line * 128;
+        else if (line < kP + kG) at = static_cast<const char *>(q.g) + (b0 + i) * kBlock * kG + (line - kP) * 128;
+        else if (line < kP + kG + kM) at = static_cast<const char *>(s.m) + (q.block0 + b0 + i) * kBlock * kM + (line - kP - kG) * 128;
+        else at = static_cast<const char *>(s.v) + (q.block0 + b0 + i) * kBlock * kM + (line - kP - kG - kM) * 128;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+    }
+}
+
 template <int BITS, int GRAD, int COPY, int TABLE>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 1)
 adamw_step(const __grid_constant__ AdamwParams<TABLE> t) {
     pdl_enter();
     __shared__ StepScalars shared;
@@ -261,103 +435,39 @@ adamw_step(const __grid_constant__ AdamwParams<TABLE> t) {
     bool first = true;
     StepScalars s;
     float lr1 = 0.0f, rs2 = 0.0f;
+    Piece q;
+    if ((int)blockIdx.x < chunks) q = piece_of<GRAD, COPY>(t, blockIdx.x, kChunkBlocks<BITS>);
     for (int chunk = blockIdx.x; chunk < chunks; chunk += gridDim.x) {
-        const Piece q = piece_of<GRAD, COPY>(t, chunk, kChunkBlocks<BITS>);
         const long long b0 = q.first + warp * N;  // this warp's blocks within the tensor
-        const long long blocks = (q.len + kBlock - 1) / kBlock;
-        float4 p4[N];
-        typename Grad<GRAD>::Four g4[N];
-        float4 m4[BITS == 32 ? N : 1], v4[BITS == 32 ? N : 1];
-        uint32_t mc[BITS == 8 ? N : 1], vc[BITS == 8 ? N : 1];
-        float ms[BITS == 8 ? N : 1], vs[BITS == 8 ? N : 1];
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            if (b0 + i >= blocks) break;
-            const long long at = (q.block0 + b0 + i) * (kBlock / 4) + lane;  // four elements of the state
-            if constexpr (BITS == 32) {
-                m4[i] = __ldcs(static_cast<const float4 *>(t.s.m) + at);
-                v4[i] = __ldcs(static_cast<const float4 *>(t.s.v) + at);
-            } else {
-                mc[i] = __ldcs(static_cast<const uint32_t *>(t.s.m) + at);
-                vc[i] = __ldcs(static_cast<const uint32_t *>(t.s.v) + at);
-                ms[i] = t.s.m_scales[q.block0 + b0 + i];
-                vs[i] = t.s.v_scales[q.block0 + b0 + i];
+        Piece next;
+        const auto meanwhile = [&] {  // the loads being on their way
+            if (chunk + (int)gridDim.x < chunks) {
+                next = piece_of<GRAD, COPY>(t, chunk + gridDim.x, kChunkBlocks<BITS>);
+                if (kAhead<BITS>) ask_ahead<BITS, GRAD, N>(next, next.first + warp * N, t.s, lane);
             }
-            take<GRAD>(q, (b0 + i) * kBlock + lane * 4, p4[i], g4[i]);
-        }
-        if (first) {
+            if (!first) return;
             first = false;
             __syncthreads();
             s = shared;
             lr1 = __fdiv_rn(c.lr, s.bc1);
             rs2 = __frcp_rn(__fsqrt_rn(s.bc2));
-            if (s.skip) break;
-        }
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            if (b0 + i >= blocks) break;
-            const long long e = (b0 + i) * kBlock + lane * 4;
-            const long long at = (q.block0 + b0 + i) * (kBlock / 4) + lane;
-            float p[4] = {p4[i].x, p4[i].y, p4[i].z, p4[i].w}, grad[4];
-            Grad<GRAD>::widen(g4[i], grad);
-            if constexpr (BITS == 32) {
-                float m[4] = {m4[i].x, m4[i].y, m4[i].z, m4[i].w}, v[4] = {v4[i].x, v4[i].y, v4[i].z, v4[i].w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    // every operation rounded on its own, in zero_adam_step's order
-                    const float g = __fmul_rn(grad[k], s.factor);
-                    m[k] = __fadd_rn(__fmul_rn(c.beta1, m[k]), __fmul_rn(c.omb1, g));
-                    v[k] = __fadd_rn(__fmul_rn(c.beta2, v[k]), __fmul_rn(c.omb2, __fmul_rn(g, g)));
-                    const float denom = __fadd_rn(__fsqrt_rn(__fdiv_rn(v[k], s.bc2)), c.eps);
-                    const float update = __fdiv_rn(__fmul_rn(c.lr, __fdiv_rn(m[k], s.bc1)), denom);
-                    p[k] = __fsub_rn(__fmul_rn(p[k], c.decay), update);
-                }
-                __stcs(static_cast<float4 *>(t.s.m) + at, make_float4(m[0], m[1], m[2], m[3]));
-                __stcs(static_cast<float4 *>(t.s.v) + at, make_float4(v[0], v[1], v[2], v[3]));
-                put<COPY>(q, e, p);
-            } else {
-                float m[4], r[4];
-                m_values(mc[i], m);
-                root_values(vc[i], r);
-                uint32_t top_m = 0u, top_r = 0u;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float g = grad[k] * s.factor;
-                    const float root = r[k] * vs[i];
-                    m[k] = __fmaf_rn(c.beta1, m[k] * ms[i], c.omb1 * g);
-                    const float v = __fmaf_rn(c.beta2 * root, root, c.omb2 * g * g);
-                    r[k] = sqrt_approx(v);
-                    if (e + k >= q.len) m[k] = r[k] = 0.0f;  // behind the tensor's end
-                    p[k] = __fmaf_rn(p[k], c.decay, -__fdividef(lr1 * m[k], __fmaf_rn(r[k], rs2, c.eps)));
-                    top_m = max(top_m, __float_as_uint(m[k]) & 0x7fffffffu);
-                    top_r = max(top_r, __float_as_uint(r[k]) & 0x7fffffffu);
-                }
-                put<COPY>(q, e, p);
-                top_m = __reduce_max_sync(0xffffffffu, top_m);
-                top_r = __reduce_max_sync(0xffffffffu, top_r);
-                float inv_m, inv_r;
-                const float scale_m = scale_of(top_m, 1.0f / kTopM, inv_m), scale_r = scale_of(top_r, 1.0f / kTopR, inv_r);
-                const unsigned long long place = (unsigned long long)at * 4;
-                const uint32_t key = mix(s.key + (uint32_t)(place >> 32));
-                uint32_t new_m = 0u, new_r = 0u;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const uint32_t random = mix(((uint32_t)place + k) ^ key);
-                    uint32_t code = random_code<3, -6>(fabsf(m[k]) * inv_m, random & 0xffffu);
-                    code = min(code, 126u) | (__float_as_uint(m[k]) >> 31 << 7);
-                    new_m |= (inv_m > 0.0f ? code : 0u) << (8 * k);
-                    uint32_t root = random_code<5, -14>(r[k] * inv_r, random >> 16);
-                    root = min(max(root, r[k] > 0.0f ? 1u : 0u), 255u);
-                    new_r |= (inv_r > 0.0f ? root : 0u) << (8 * k);
-                }
-                __stcs(static_cast<uint32_t *>(t.s.m) + at, new_m);
-                __stcs(static_cast<uint32_t *>(t.s.v) + at, new_r);
-                if (lane == 0) {
-                    t.s.m_scales[q.block0 + b0 + i] = scale_m;
-                    t.s.v_scales[q.block0 + b0 + i] = scale_r;
-                }
-            }
-        }
+        };
+        const unsigned long long place = (unsigned long long)(q.block0 + b0) * kBlock;
+        const auto update = [&](auto form) {
+            Span<BITS, GRAD, COPY, decltype(form)::value> a(q, b0, lane);
+            a.load(t.s, lane);
+            meanwhile();
+            if (!s.skip) a.step(t.s, c, s, lr1, rs2, lane);
+        };
+        const bool full = q.vectors && (BITS == 32 || (uint32_t)place <= 0xffffffffu - (N - 1) * kBlock);
+        if (full && q.together && (b0 + N) * kBlock <= q.len)
+            update(std::integral_constant<int, kTogether>());
+        else if (full && (b0 + N) * kBlock < q.len)
+            update(std::integral_constant<int, kWhole>());
+        else
+            update(std::integral_constant<int, kAny>());
+        if (s.skip) break;
+        q = next;
     }
     // The step counts once everyone has read its number.
     if (!c.last) return;

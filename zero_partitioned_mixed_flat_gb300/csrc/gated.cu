@@ -250,6 +250,20 @@ gated_products(const __grid_constant__ GatedParams p) {
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
+    if (threadIdx.x == 0) {  // the maps of the operands, while the kernel before this one ends
+        if constexpr (MODE != kGradients) {
+            ask_for(&p.x_k);
+            ask_for(rank == 0 ? &p.gate_k : &p.up_k);
+        } else {
+            ask_for(&p.x_mn);
+            ask_for(&p.dg_k);
+            ask_for(&p.du_k);
+            ask_for(&p.gate_mn);
+            ask_for(&p.up_mn);
+            ask_for(&p.dg_mn);
+            ask_for(&p.du_mn);
+        }
+    }
     pdl_enter();
 
     volatile int *dead = &sh.dead;
@@ -485,6 +499,263 @@ gated_products(const __grid_constant__ GatedParams p) {
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemColumns) : "memory");
 }
 
+// ------------------------------------------------------------------- few tokens
+
+// Up to kNarrow tokens the matrices are what takes time, read once, and a tile of 256 tokens
+// would hold few.  Here the matrices are the A operand: a CTA takes 128 rows of both, x is B,
+// and a row of tensor memory holds one f's sums for every token, g's columns before u's.
+// A cluster of CTAs shares a tile's K between them, so that as many CTAs as run at once
+// load at the same time; each then adds up its share of the elements from all of them.
+constexpr int kNarrow = 64;
+constexpr int kNarrowThreads = 192;          // loads, products, and a warp for each quarter of the lanes
+constexpr int kNarrowSmem = 112 * 1024;      // two CTAs on an SM
+constexpr int kNarrowWays = 8;               // CTAs of a cluster, at most
+constexpr int kNarrowStages = 3;
+
+struct NarrowPlan {
+    int columns;  // tokens rounded up to what a product takes
+    int stages, stage_bytes, ways, tmem;
+};
+
+NarrowPlan narrow_plan(int64_t tokens, int64_t wide, int dim) {
+    NarrowPlan n;
+    n.columns = (int)up(tokens, 16);
+    n.stage_bytes = 2 * kOperandBytes + n.columns * 128;
+    n.stages = std::min(kNarrowStages, (kNarrowSmem - 1024) / n.stage_bytes);
+    n.tmem = 32;
+    while (n.tmem < 2 * n.columns) n.tmem *= 2;
+    const int64_t tiles = up(wide, kHalf) / kHalf, blocks = up(dim, kTileK) / kTileK;
+    n.ways = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(kNarrowWays, 4 * kPairs / tiles), blocks / 2));
+    return n;
+}
+
+struct NarrowParams {
+    CUtensorMap gate_k, up_k;  // 64 of D x 128 of F
+    CUtensorMap x_k;           // 64 of D x all tokens' columns
+    int tokens, wide, k_blocks, act;
+    int columns, stages, stage_bytes, ways, tmem;
+    uint16_t *out;             // forward
+    long long out_stride;
+    const uint16_t *grad_out;  // slopes
+    long long grad_stride;
+    uint16_t *dg, *du;         // rows of `wide`
+    const float *tops;
+    int *status;
+    long long wait_cycles;
+};
+
+__device__ __forceinline__ void tma_load_here(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_one(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+
+__device__ __forceinline__ void commit_one(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+
+__device__ __forceinline__ float4 load_in_cta(uint32_t addr, uint32_t rank) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(in_cta(addr, rank)) : "memory");
+    return v;
+}
+
+// A bounded wait of this CTA's: false once `limit` cycles have passed, or another wait of it has given up.
+__device__ __forceinline__ bool narrow_wait(uint64_t *bar, uint32_t parity, volatile int *dead, long long limit, int *status) {
+    const uint32_t b = smem_addr(bar);
+    if (bar_try(b, parity)) return true;
+    const long long t0 = clock64();
+    while (!bar_try(b, parity)) {
+        if (*dead || clock64() - t0 >= limit) {
+            *dead = 1;
+            atomicOr(status, ZERO_LOSS_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+
+// the results of four neighbouring elements from their sums
+template <bool BF16, int MODE>
+__device__ __forceinline__ void narrow_results(const NarrowParams &p, long long t, long long f, float scale, float (&g)[4], float (&u)[4]) {
+    if constexpr (MODE == kForward) {
+        if (p.act == ZERO_ACT_SILU) outs_of<ZERO_ACT_SILU>(g, u);
+        else if (p.act == ZERO_ACT_GELU) outs_of<ZERO_ACT_GELU>(g, u);
+        else outs_of<ZERO_ACT_GELU_TANH>(g, u);
+        *reinterpret_cast<uint2 *>(p.out + t * p.out_stride + f) = make_uint2(pack_lp<BF16>(u[0], u[1]), pack_lp<BF16>(u[2], u[3]));
+    } else {
+        const uint2 q = *reinterpret_cast<const uint2 *>(p.grad_out + t * p.grad_stride + f);
+        float w[8];
+        widen8<BF16>(make_uint4(q.x, q.y, 0u, 0u), w);
+        const float go[4] = {w[0] * scale, w[1] * scale, w[2] * scale, w[3] * scale};
+        if (p.act == ZERO_ACT_SILU) slopes_of<ZERO_ACT_SILU>(go, g, u);
+        else if (p.act == ZERO_ACT_GELU) slopes_of<ZERO_ACT_GELU>(go, g, u);
+        else slopes_of<ZERO_ACT_GELU_TANH>(go, g, u);
+        *reinterpret_cast<uint2 *>(p.dg + t * p.wide + f) = make_uint2(pack_lp<BF16>(g[0], g[1]), pack_lp<BF16>(g[2], g[3]));
+        *reinterpret_cast<uint2 *>(p.du + t * p.wide + f) = make_uint2(pack_lp<BF16>(u[0], u[1]), pack_lp<BF16>(u[2], u[3]));
+    }
+}
+
+template <bool BF16, int MODE>
+__global__ void __launch_bounds__(kNarrowThreads)
+gated_narrow(const __grid_constant__ NarrowParams p) {
+    extern __shared__ unsigned char raw[];
+    __shared__ uint64_t full[kNarrowStages], empty[kNarrowStages], done;
+    __shared__ uint32_t tmem_at;
+    __shared__ int dead_flag, placed_count, consumed_count;
+    const uint32_t stage0 = (smem_addr(raw) + 1023u) & ~1023u;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t rank;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.stages; ++s) {
+            bar_init(smem_addr(&full[s]), 1);
+            bar_init(smem_addr(&empty[s]), 1);
+        }
+        bar_init(smem_addr(&done), 1);
+        dead_flag = placed_count = consumed_count = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_at)), "r"(p.tmem) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_at;
+    if (threadIdx.x == 0) {
+        ask_for(&p.gate_k);
+        ask_for(&p.up_k);
+        ask_for(&p.x_k);
+    }
+    pdl_enter();
+
+    volatile int *dead = &dead_flag;
+    const int tile = blockIdx.x / p.ways, f0 = tile * kHalf;
+    const int k0 = p.k_blocks * (int)rank / p.ways, k1 = p.k_blocks * ((int)rank + 1) / p.ways;
+    if (warp == 0) {
+        if (lane == 0) {  // ------------------------------------------ loads
+            int stage = 0, placed = 0;
+            uint32_t phase = 0;
+            for (int k = k0; k < k1; ++k) {
+                if (!narrow_wait(&empty[stage], phase ^ 1, dead, p.wait_cycles, p.status)) break;
+                const uint32_t bar = smem_addr(&full[stage]), a = stage0 + stage * p.stage_bytes;
+                bar_expect(bar, p.stage_bytes);
+                tma_load_here(a, &p.gate_k, k * kTileK, f0, bar);
+                tma_load_here(a + kOperandBytes, &p.up_k, k * kTileK, f0, bar);
+                tma_load_here(a + 2 * kOperandBytes, &p.x_k, k * kTileK, 0, bar);
+                ++placed;
+                if (++stage == p.stages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+            placed_count = placed;
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {  // --------------------------------------- products
+            uint32_t idesc = 1u << 4 | (BF16 ? 1u << 7 | 1u << 10 : 0u);  // float sums
+            idesc |= (uint32_t)(p.columns >> 3) << 17 | (uint32_t)(kHalf >> 4) << 24;
+            int stage = 0, consumed = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int k = k0; k < k1; ++k) {
+                ok = narrow_wait(&full[stage], phase, dead, p.wait_cycles, p.status);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t at = stage0 + stage * p.stage_bytes;
+                const uint64_t g = operand_desc(at, false), u = operand_desc(at + kOperandBytes, false), x = operand_desc(at + 2 * kOperandBytes, false);
+#pragma unroll
+                for (int i = 0; i < kTileK / 16; ++i) {
+                    mma_one(tmem, g + 2 * i, x + 2 * i, idesc, k > k0 || i > 0);
+                    mma_one(tmem + p.columns, u + 2 * i, x + 2 * i, idesc, k > k0 || i > 0);
+                }
+                commit_one(smem_addr(&empty[stage]));
+                ++consumed;
+                if (++stage == p.stages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+            consumed_count = consumed;
+            // also after a wait that gave up: no product reads shared memory any more
+            commit_one(smem_addr(&done));
+            if (!wait_out(&done, 0)) {
+                *dead = 1;
+                atomicOr(p.status, ZERO_LOSS_TIMEOUT);
+            }
+            tc_fence_before();
+        }
+    }
+    __syncwarp();
+    __syncthreads();  // the products are done, and every copy that they waited for has landed
+    tc_fence_after();
+    if (*dead && threadIdx.x == 0) {  // copies on their way would land in what follows
+        for (int n = consumed_count; n < placed_count; ++n)
+            if (!wait_out(&full[n % p.stages], (uint32_t)(n / p.stages) & 1u)) atomicOr(p.status, ZERO_LOSS_TIMEOUT);
+    }
+    const float scale = MODE == kForward ? 1.0f : scale_of(p.tops);
+    __syncthreads();  // thread 0 may have waited for copies
+    // this CTA's sums to its shared memory: [g, then u][token][128 of f]
+    if (warp >= 2) {
+        const int quad = warp & 3;
+        const uint32_t row = tmem + ((uint32_t)(quad * 32) << 16);
+        for (int c = 0; c < 2 * p.columns; c += 16) {
+            float z[16];
+            tmem_load16(row + c, z);
+            const int first = c < p.columns ? c : c - p.columns, left = p.tokens - first;
+            const uint32_t to = stage0 + (((c < p.columns ? 0 : p.tokens) + first) * kHalf + quad * 32 + lane) * 4;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (i < left) asm volatile("st.shared.f32 [%0], %1;" ::"r"(to + i * kHalf * 4), "f"(z[i]) : "memory");
+        }
+    }
+    __syncthreads();
+    if (p.ways > 1) cluster_sync();
+    const int fours = p.tokens * (kHalf / 4);
+    const int i0 = fours * (int)rank / p.ways, i1 = fours * ((int)rank + 1) / p.ways;
+    for (int i = i0 + (int)threadIdx.x; i < i1; i += kNarrowThreads) {
+        const long long f = f0 + i % (kHalf / 4) * 4;
+        if (f >= p.wide) continue;
+        float4 part[2][kNarrowWays];
+#pragma unroll
+        for (int r = 0; r < kNarrowWays; ++r)
+            if (r < p.ways) {
+                part[0][r] = load_in_cta(stage0 + i * 16, r);
+                part[1][r] = load_in_cta(stage0 + (fours + i) * 16, r);
+            }
+        float sum[2][4] = {};
+#pragma unroll
+        for (int r = 0; r < kNarrowWays; ++r)
+            if (r < p.ways)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    sum[h][0] += part[h][r].x;
+                    sum[h][1] += part[h][r].y;
+                    sum[h][2] += part[h][r].z;
+                    sum[h][3] += part[h][r].w;
+                }
+        narrow_results<BF16, MODE>(p, i / (kHalf / 4), f, scale, sum[0], sum[1]);
+    }
+    __syncthreads();
+    if (p.ways > 1) cluster_sync();  // the others have read this CTA's
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(p.tmem) : "memory");
+}
+
 // ---------------------------------------------------------- the smaller kernels
 
 // The largest finite |grad_out| of a block's share of the rows, fp16.
@@ -581,8 +852,56 @@ cudaError_t launch_products(const GatedParams &p, int64_t tiles, cudaStream_t st
     return launch_pdl(gated_products<BF16, MODE>, dim3((unsigned)(2 * use)), dim3(kProductThreads), kSmemBytes, stream, p);
 }
 
+template <bool BF16, int MODE>
+cudaError_t launch_narrow(const GatedArgs &a, uint16_t *dg, uint16_t *du, const float *tops, cudaStream_t stream) {
+    static PerDevice allowed;
+    const int set = allowed.get([] {
+        return done_or_error(cudaFuncSetAttribute(gated_narrow<BF16, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kNarrowSmem));
+    });
+    if (set < 0) return (cudaError_t)-set;
+    const NarrowPlan n = narrow_plan(a.tokens, a.wide, a.dim);
+    NarrowParams p = {};
+    if (!encoder() || !make_map(&p.gate_k, a.gate, a.wide, a.dim, a.gate_stride, a.lp, false, kHalf) ||
+        !make_map(&p.up_k, a.up, a.wide, a.dim, a.up_stride, a.lp, false, kHalf) ||
+        !make_map(&p.x_k, a.x, a.tokens, a.dim, a.x_stride, a.lp, false, n.columns))
+        return cudaErrorNotSupported;
+    p.tokens = (int)a.tokens;
+    p.wide = a.wide;
+    p.k_blocks = (int)(up(a.dim, kTileK) / kTileK);
+    p.act = a.act;
+    p.columns = n.columns;
+    p.stages = n.stages;
+    p.stage_bytes = n.stage_bytes;
+    p.ways = n.ways;
+    p.tmem = n.tmem;
+    p.out = static_cast<uint16_t *>(a.out);
+    p.out_stride = a.out_stride;
+    p.grad_out = static_cast<const uint16_t *>(a.grad_out);
+    p.grad_stride = a.grad_out_stride;
+    p.dg = dg;
+    p.du = du;
+    p.tops = tops;
+    p.status = a.status;
+    p.wait_cycles = loss_wait();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(up(a.wide, kHalf) / kHalf * n.ways));
+    cfg.blockDim = dim3(kNarrowThreads);
+    cfg.dynamicSmemBytes = kNarrowSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)n.ways;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, gated_narrow<BF16, MODE>, p);
+}
+
 template <bool BF16>
 cudaError_t forward_impl(const GatedArgs &a, cudaStream_t stream) {
+    if (a.tokens <= kNarrow) return launch_narrow<BF16, kForward>(a, nullptr, nullptr, nullptr, stream);
     GatedParams p = {};
     if (!encoder() || !make_map(&p.x_k, a.x, a.tokens, a.dim, a.x_stride, a.lp, false, kHalf) ||
         !make_map(&p.gate_k, a.gate, a.wide, a.dim, a.gate_stride, a.lp, false, kHalf) ||
@@ -635,7 +954,10 @@ cudaError_t backward_impl(const GatedArgs &a, cudaStream_t stream) {
     cudaError_t e = cudaSuccess;
     if (!BF16)
         e = launch_pdl(gated_top, dim3(kTopBlocks), dim3(kTopThreads), 0, stream, p.grad_out, p.grad_stride, (long long)a.tokens, a.wide / 8, tops);
-    if (e == cudaSuccess) e = launch_products<BF16, kSlopes>(p, row_tiles * (up(2 * a.wide, kTileN) / kTileN), stream);
+    if (e == cudaSuccess && a.tokens <= kNarrow)
+        e = launch_narrow<BF16, kSlopes>(a, static_cast<uint16_t *>(dg), static_cast<uint16_t *>(du), p.tops, stream);
+    else if (e == cudaSuccess)
+        e = launch_products<BF16, kSlopes>(p, row_tiles * (up(2 * a.wide, kTileN) / kTileN), stream);
     if (e == cudaSuccess)
         e = launch_products<BF16, kGradients>(p, row_tiles * dim_tiles * l.splits + 2 * (up(a.wide, kTileM) / kTileM) * dim_tiles, stream);
     if (e == cudaSuccess && l.splits > 1)
