@@ -116,17 +116,18 @@ __device__ __forceinline__ void slopes_of(const float (&go)[N], float (&g)[N], f
 
 struct GatedParams {
     CUtensorMap x_k;             // x: boxes 64 of D x 128 tokens
-    CUtensorMap gate_k, up_k;    // matrices: 64 of D x 128 of F
-    CUtensorMap out;             // out: 64 of F x 32 tokens
+    CUtensorMap gate_k, up_k;    // matrices: 64 of D x half a tile's columns
+    CUtensorMap out;             // out: 32 of F x 32 tokens
     CUtensorMap x_mn;            // x: 64 of D x 64 tokens
     CUtensorMap gate_mn, up_mn;  // matrices: 64 of D x 64 of F
-    CUtensorMap dg_out, du_out;  // slopes: 64 of F x 32 tokens
+    CUtensorMap dg_out, du_out;  // slopes: 32 of F x 32 tokens
     CUtensorMap dg_k, du_k;      // slopes: 64 of F x 128 tokens
     CUtensorMap dg_mn, du_mn;    // slopes: 64 of F x 64 tokens
     CUtensorMap gx_out;          // grad_x: 64 of D x 32 tokens, or the partial sums: 32 of D x 32 rows, float
     CUtensorMap ggate_out, gup_out;  // 64 of D x 32 of F
     long long tokens, rows;
     int wide, dim, splits;
+    int step;  // columns of a tile of both projections
     int act;
     const uint4 *grad_out;
     long long grad_stride;  // vectors
@@ -135,6 +136,25 @@ struct GatedParams {
     long long wait_cycles;
 };
 
+// 32 rows of 64 bytes, one a lane, to a box of `map`: put_rows with half the columns and two
+// buffers a warp, which stores in turn.
+__device__ __forceinline__ void put_half_rows(const uint32_t (&w)[16], uint32_t buffer, int lane, const CUtensorMap *map, int x, int y, bool skip) {
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+    __syncwarp();
+    const uint32_t row = buffer + lane * 64;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((c ^ (lane >> 1 & 3)) << 4)), "r"(w[4 * c]),
+                     "r"(w[4 * c + 1]), "r"(w[4 * c + 2]), "r"(w[4 * c + 3])
+                     : "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) {
+        if (!skip) tma_store(map, x, y, buffer);
+        store_commit();
+    }
+}
+
 // The work of one launch, and which of it each pair does, in order: every pair-th tile,
 // gradients first the tiles of grad_x, few and long; the pairs that get one fewer of
 // them then take `catch_up` tiles of the matrices' gradients each, about as long
@@ -142,6 +162,7 @@ struct GatedParams {
 template <int MODE>
 struct GatedWork {
     Tiles gates, x, weight;
+    int step;
     int pair, pairs, n_x, n_weight, weight_m;
     int fuller, catch_up, mine;
 
@@ -149,8 +170,9 @@ struct GatedWork {
         const int row_tiles = (int)((p.tokens + kTileM - 1) / kTileM);
         pair = blockIdx.x >> 1;
         pairs = gridDim.x >> 1;
+        step = p.step;
         if constexpr (MODE != kGradients) {
-            const int wide_tiles = (2 * p.wide + kTileN - 1) / kTileN;
+            const int wide_tiles = (2 * p.wide + p.step - 1) / p.step;
             gates.set(row_tiles, wide_tiles, 2 * p.wide, (p.dim + kTileK - 1) / kTileK, 1);
         } else {
             const int dim_tiles = (p.dim + kTileN - 1) / kTileN;
@@ -173,6 +195,9 @@ struct GatedWork {
             const int i = pair + j * pairs;
             if (i >= gates.size()) return false;
             t = gates.at(i, kGates);
+            t.n0 = t.n * step;
+            const int left = (gates.columns - t.n0 + 31) / 32 * 32;
+            t.width = left < step ? left : step;
             return true;
         }
         if (j < mine) {
@@ -283,7 +308,8 @@ gated_products(const __grid_constant__ GatedParams p) {
                 // this CTA's rows of A, and its half of the columns of B
                 const int m0 = t.m0 + (int)rank * kHalf, n0 = t.n0 + (int)rank * (t.width / 2);
                 const bool two = MODE != kGradients || t.width > kTileN / 2;  // boxes of 64 columns that hold its half
-                const uint32_t bytes = 2 * (two ? kBlockBytes : kBlockBytes - kBoxBytes);
+                const uint32_t bytes = MODE != kGradients ? 2 * kOperandBytes + work.step * kTileK * 2
+                                                          : 2 * (two ? kBlockBytes : kBlockBytes - kBoxBytes);
                 const int half_k = MODE == kGradients ? (p.wide + kTileK - 1) / kTileK : 0;
                 for (int k = t.k0; k < t.k1; k += kStageBlocks) {
                     ok = wait_for(&sh.empty[stage], phase ^ 1, dead, limit, p.status);
@@ -385,65 +411,68 @@ gated_products(const __grid_constant__ GatedParams p) {
         const uint32_t buffer = stage0 + kStages * kStageBytes + (warp - 2) * kStoreBytes;
         const float scale = MODE == kForward ? 1.0f : scale_of(p.tops);
         const float factor = 1.0f / scale;      // powers of two
-        int buf = 0;
+        int buf = 0, turn = 0;
         uint32_t acc_phase = 0;
         for (int j = 0; work.at(j, t); ++j) {
             const int row0 = t.m0 + (int)rank * kHalf + quad * 32;  // this warp's first row of M
+            uint4 grad[MODE == kSlopes ? 2 : 1][4];
+            if constexpr (MODE == kSlopes) {  // while the sums are under way
+                const long long row = row0 + lane;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int c = group * 64 + 32 * h, f = t.n0 / 2 + c + 8 * i;
+                        grad[h][i] = row < p.tokens && c < t.width / 2 && f < p.wide ? __ldg(p.grad_out + row * p.grad_stride + f / 8)
+                                                                                    : make_uint4(0u, 0u, 0u, 0u);
+                    }
+            }
             const bool got = wait_for(&sh.acc_full[buf], acc_phase, dead, limit, p.status);
             if (!__all_sync(0xffffffffu, got)) break;
             tc_fence_after();
             const uint32_t acc = tmem + buf * kTileN + ((uint32_t)(quad * 32) << 16);
             if constexpr (MODE == kForward) {
-                const int first = group * (kTileN / 4), f0 = t.n0 / 2 + first;  // 64 elements of each row
-                if (f0 < p.wide) {
-                    uint32_t w[32];
+#pragma unroll 1
+                for (int c = group * 64; c < group * 64 + 64 && c < t.width / 2; c += 32) {
+                    const int f = t.n0 / 2 + c;
+                    float g[32], u[32];
+                    uint32_t w[16];
+                    tmem_load32(acc + c, g);
+                    tmem_load32(acc + t.width / 2 + c, u);
+                    if (p.act == ZERO_ACT_SILU) outs_of<ZERO_ACT_SILU>(g, u);
+                    else if (p.act == ZERO_ACT_GELU) outs_of<ZERO_ACT_GELU>(g, u);
+                    else outs_of<ZERO_ACT_GELU_TANH>(g, u);
 #pragma unroll
-                    for (int c = 0; c < 64; c += 32) {
-                        float g[32], u[32];
-                        tmem_load32(acc + first + c, g);
-                        tmem_load32(acc + t.width / 2 + first + c, u);
-                        if (p.act == ZERO_ACT_SILU) outs_of<ZERO_ACT_SILU>(g, u);
-                        else if (p.act == ZERO_ACT_GELU) outs_of<ZERO_ACT_GELU>(g, u);
-                        else outs_of<ZERO_ACT_GELU_TANH>(g, u);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) w[c / 2 + i] = pack_lp<BF16>(u[2 * i], u[2 * i + 1]);
-                    }
-                    put_rows(w, buffer, lane, &p.out, f0, row0, false, row0 >= p.tokens);
+                    for (int i = 0; i < 16; ++i) w[i] = pack_lp<BF16>(u[2 * i], u[2 * i + 1]);
+                    put_half_rows(w, buffer + turn * (kStoreBytes / 2), lane, &p.out, f, row0, row0 >= p.tokens || f >= p.wide);
+                    turn ^= 1;
                 }
             } else if constexpr (MODE == kSlopes) {
-                const int first = group * (kTileN / 4), f0 = t.n0 / 2 + first;
-                const long long row = row0 + lane;
-                if (f0 < p.wide) {
-                    uint32_t w[32], z[32];
 #pragma unroll
-                    for (int c = 0; c < 64; c += 32) {
-                        float g[32], u[32], go[32];
-                        uint4 q[4];
+                for (int h = 0; h < 2; ++h) {
+                    const int c = group * 64 + 32 * h, f = t.n0 / 2 + c;
+                    if (c >= t.width / 2) break;
+                    float g[32], u[32], go[32];
+                    uint32_t w[16];
+                    tmem_load32(acc + c, g);
+                    tmem_load32(acc + t.width / 2 + c, u);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int f = f0 + c + 8 * i;
-                            q[i] = row < p.tokens && f < p.wide ? __ldg(p.grad_out + row * p.grad_stride + f / 8) : make_uint4(0u, 0u, 0u, 0u);
-                        }
-                        tmem_load32(acc + first + c, g);
-                        tmem_load32(acc + t.width / 2 + first + c, u);
+                    for (int i = 0; i < 4; ++i) {
+                        float x[8];
+                        widen8<BF16>(grad[h][i], x);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float f[8];
-                            widen8<BF16>(q[i], f);
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) go[8 * i + k] = f[k] * scale;
-                        }
-                        if (p.act == ZERO_ACT_SILU) slopes_of<ZERO_ACT_SILU>(go, g, u);
-                        else if (p.act == ZERO_ACT_GELU) slopes_of<ZERO_ACT_GELU>(go, g, u);
-                        else slopes_of<ZERO_ACT_GELU_TANH>(go, g, u);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            w[c / 2 + i] = pack_lp<BF16>(g[2 * i], g[2 * i + 1]);
-                            z[c / 2 + i] = pack_lp<BF16>(u[2 * i], u[2 * i + 1]);
-                        }
+                        for (int k = 0; k < 8; ++k) go[8 * i + k] = BF16 ? x[k] : x[k] * scale;
                     }
-                    put_rows(w, buffer, lane, &p.dg_out, f0, row0, false, row0 >= p.tokens);
-                    put_rows(z, buffer, lane, &p.du_out, f0, row0, false, row0 >= p.tokens);
+                    if (p.act == ZERO_ACT_SILU) slopes_of<ZERO_ACT_SILU>(go, g, u);
+                    else if (p.act == ZERO_ACT_GELU) slopes_of<ZERO_ACT_GELU>(go, g, u);
+                    else slopes_of<ZERO_ACT_GELU_TANH>(go, g, u);
+                    const bool skip = row0 >= p.tokens || f >= p.wide;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) w[i] = pack_lp<BF16>(g[2 * i], g[2 * i + 1]);
+                    put_half_rows(w, buffer, lane, &p.dg_out, f, row0, skip);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) w[i] = pack_lp<BF16>(u[2 * i], u[2 * i + 1]);
+                    put_half_rows(w, buffer + kStoreBytes / 2, lane, &p.du_out, f, row0, skip);
                 }
             } else {
                 const int first = group * kResultColumns;
@@ -508,24 +537,29 @@ gated_products(const __grid_constant__ GatedParams p) {
 // load at the same time; each then adds up its share of the elements from all of them.
 constexpr int kNarrow = 64;
 constexpr int kNarrowThreads = 192;          // loads, products, and a warp for each quarter of the lanes
-constexpr int kNarrowSmem = 112 * 1024;      // two CTAs on an SM
+constexpr int kNarrowSmem = 220 * 1024, kNarrowHalf = 112 * 1024;  // one CTA on an SM, or two
 constexpr int kNarrowWays = 8;               // CTAs of a cluster, at most
-constexpr int kNarrowStages = 3;
+constexpr int kNarrowStages = 5;
 
 struct NarrowPlan {
     int columns;  // tokens rounded up to what a product takes
-    int stages, stage_bytes, ways, tmem;
+    int stages, stage_bytes, ways, tmem, smem;
 };
 
+// Two CTAs on an SM, unless there is more than 16 tokens' worth of sums to exchange and one on
+// each has a way of its own: 48 tokens, 1600 x 4264 12.6 us with two and 10.7 with one, one
+// token 8.6 and 9.2, and 4096 x 10928, whose 86 tiles one on an SM leaves whole, 33.5 and 37.4.
 NarrowPlan narrow_plan(int64_t tokens, int64_t wide, int dim) {
     NarrowPlan n;
     n.columns = (int)up(tokens, 16);
     n.stage_bytes = 2 * kOperandBytes + n.columns * 128;
-    n.stages = std::min(kNarrowStages, (kNarrowSmem - 1024) / n.stage_bytes);
     n.tmem = 32;
     while (n.tmem < 2 * n.columns) n.tmem *= 2;
     const int64_t tiles = up(wide, kHalf) / kHalf, blocks = up(dim, kTileK) / kTileK;
-    n.ways = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(kNarrowWays, 4 * kPairs / tiles), blocks / 2));
+    const bool one = n.columns > 16 && tiles <= kPairs;
+    n.smem = one ? kNarrowSmem : kNarrowHalf;
+    n.stages = std::min(kNarrowStages, (n.smem - 1024) / n.stage_bytes);
+    n.ways = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(kNarrowWays, (one ? 2 : 4) * kPairs / tiles), blocks / 2));
     return n;
 }
 
@@ -843,6 +877,26 @@ int pairs_at_once() {
     });
 }
 
+// Columns of a tile of both projections: those for which the pairs' rounds take the least time.
+// A block of K takes (step + 128) / 384 of what it takes with 256 columns, as measured: 19
+// rounds of 256 and 24 of 192 (4096 x 4096 x 10928) 400 and 432 us, 15 and 19 (8184 x 1600 x
+// 4264) 134.6 and 140.6, but one round of 128 columns and not of 256 (300 x 1000 x 2000) 9.3
+// and 11.4, two of 192 and not of 256 (129 x 4088 x 10920) 53.3 and 58.5.
+int step_of(int64_t tokens, int64_t wide, int dim, int pairs) {
+    const int64_t rows = up(tokens, kTileM) / kTileM, blocks = up(dim, kTileK) / kTileK;
+    int best = kTileN;
+    int64_t least = 0;
+    for (int step = kTileN; step >= kTileN / 2; step -= 64) {
+        const int64_t rounds = up(rows * (up(2 * wide, step) / step), pairs) / pairs;
+        const int64_t cost = rounds * (blocks * (step + 128) + kTileCost * 384);
+        if (least == 0 || cost < least) {
+            least = cost;
+            best = step;
+        }
+    }
+    return best;
+}
+
 template <bool BF16, int MODE>
 cudaError_t launch_products(const GatedParams &p, int64_t tiles, cudaStream_t stream) {
     const int pairs = pairs_at_once<BF16, MODE>();
@@ -886,7 +940,7 @@ cudaError_t launch_narrow(const GatedArgs &a, uint16_t *dg, uint16_t *du, const 
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(up(a.wide, kHalf) / kHalf * n.ways));
     cfg.blockDim = dim3(kNarrowThreads);
-    cfg.dynamicSmemBytes = kNarrowSmem;
+    cfg.dynamicSmemBytes = n.smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -902,11 +956,14 @@ cudaError_t launch_narrow(const GatedArgs &a, uint16_t *dg, uint16_t *du, const 
 template <bool BF16>
 cudaError_t forward_impl(const GatedArgs &a, cudaStream_t stream) {
     if (a.tokens <= kNarrow) return launch_narrow<BF16, kForward>(a, nullptr, nullptr, nullptr, stream);
+    const int pairs = pairs_at_once<BF16, kForward>();
+    if (pairs < 0) return (cudaError_t)-pairs;
     GatedParams p = {};
+    p.step = step_of(a.tokens, a.wide, a.dim, pairs);
     if (!encoder() || !make_map(&p.x_k, a.x, a.tokens, a.dim, a.x_stride, a.lp, false, kHalf) ||
-        !make_map(&p.gate_k, a.gate, a.wide, a.dim, a.gate_stride, a.lp, false, kHalf) ||
-        !make_map(&p.up_k, a.up, a.wide, a.dim, a.up_stride, a.lp, false, kHalf) ||
-        !make_map(&p.out, a.out, a.tokens, a.wide, a.out_stride, a.lp, false, 32))
+        !make_map(&p.gate_k, a.gate, a.wide, a.dim, a.gate_stride, a.lp, false, p.step / 2) ||
+        !make_map(&p.up_k, a.up, a.wide, a.dim, a.up_stride, a.lp, false, p.step / 2) ||
+        !make_map(&p.out, a.out, a.tokens, a.wide, a.out_stride, a.lp, false, 32, true))
         return cudaErrorNotSupported;
     p.tokens = a.tokens;
     p.wide = a.wide;
@@ -915,7 +972,7 @@ cudaError_t forward_impl(const GatedArgs &a, cudaStream_t stream) {
     p.splits = 1;
     p.status = a.status;
     p.wait_cycles = loss_wait();
-    return launch_products<BF16, kForward>(p, up(a.tokens, kTileM) / kTileM * (up(2 * a.wide, kTileN) / kTileN), stream);
+    return launch_products<BF16, kForward>(p, up(a.tokens, kTileM) / kTileM * (up(2 * a.wide, p.step) / p.step), stream);
 }
 
 template <bool BF16>
@@ -924,14 +981,18 @@ cudaError_t backward_impl(const GatedArgs &a, cudaStream_t stream) {
     char *ws = static_cast<char *>(a.workspace);
     float *tops = reinterpret_cast<float *>(ws), *sums = reinterpret_cast<float *>(ws + l.sums);
     void *dg = ws + l.slope_gate, *du = ws + l.slope_up;
+    const int pairs = pairs_at_once<BF16, kSlopes>();
+    if (pairs < 0) return (cudaError_t)-pairs;
     GatedParams p = {};
+    p.step = step_of(a.tokens, a.wide, a.dim, pairs);
     const auto map = [&](CUtensorMap *m, const void *at, int64_t rows, int64_t cols, int64_t stride, int box) {
         return make_map(m, at, rows, cols, stride, a.lp, false, box);
     };
-    if (!encoder() || !map(&p.x_k, a.x, a.tokens, a.dim, a.x_stride, kHalf) || !map(&p.gate_k, a.gate, a.wide, a.dim, a.gate_stride, kHalf) ||
-        !map(&p.up_k, a.up, a.wide, a.dim, a.up_stride, kHalf) || !map(&p.x_mn, a.x, a.tokens, a.dim, a.x_stride, kTileK) ||
+    if (!encoder() || !map(&p.x_k, a.x, a.tokens, a.dim, a.x_stride, kHalf) || !map(&p.gate_k, a.gate, a.wide, a.dim, a.gate_stride, p.step / 2) ||
+        !map(&p.up_k, a.up, a.wide, a.dim, a.up_stride, p.step / 2) || !map(&p.x_mn, a.x, a.tokens, a.dim, a.x_stride, kTileK) ||
         !map(&p.gate_mn, a.gate, a.wide, a.dim, a.gate_stride, kTileK) || !map(&p.up_mn, a.up, a.wide, a.dim, a.up_stride, kTileK) ||
-        !map(&p.dg_out, dg, a.tokens, a.wide, a.wide, 32) || !map(&p.du_out, du, a.tokens, a.wide, a.wide, 32) ||
+        !make_map(&p.dg_out, dg, a.tokens, a.wide, a.wide, a.lp, false, 32, true) ||
+        !make_map(&p.du_out, du, a.tokens, a.wide, a.wide, a.lp, false, 32, true) ||
         !map(&p.dg_k, dg, a.tokens, a.wide, a.wide, kHalf) || !map(&p.du_k, du, a.tokens, a.wide, a.wide, kHalf) ||
         !map(&p.dg_mn, dg, a.tokens, a.wide, a.wide, kTileK) || !map(&p.du_mn, du, a.tokens, a.wide, a.wide, kTileK) ||
         !map(&p.ggate_out, a.grad_gate, a.wide, a.dim, a.grad_gate_stride, 32) ||
@@ -957,7 +1018,7 @@ cudaError_t backward_impl(const GatedArgs &a, cudaStream_t stream) {
     if (e == cudaSuccess && a.tokens <= kNarrow)
         e = launch_narrow<BF16, kSlopes>(a, static_cast<uint16_t *>(dg), static_cast<uint16_t *>(du), p.tops, stream);
     else if (e == cudaSuccess)
-        e = launch_products<BF16, kSlopes>(p, row_tiles * (up(2 * a.wide, kTileN) / kTileN), stream);
+        e = launch_products<BF16, kSlopes>(p, row_tiles * (up(2 * a.wide, p.step) / p.step), stream);
     if (e == cudaSuccess)
         e = launch_products<BF16, kGradients>(p, row_tiles * dim_tiles * l.splits + 2 * (up(a.wide, kTileM) / kTileM) * dim_tiles, stream);
     if (e == cudaSuccess && l.splits > 1)

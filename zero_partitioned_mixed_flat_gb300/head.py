@@ -280,7 +280,7 @@ def gated_linear(x, gate, up, activation="silu", stream=None):
     tokens, dim, wide, xs, gs, us = _gated_inputs(where, x, gate, up, activation)
     status = _status(x.device)
     with _on(stream):
-        out = x.new_empty((tokens, wide))
+        out = torch.empty((tokens, wide), dtype=x.dtype, device=x.device)
         # the forward call needs no workspace
         _call("zero_gated_forward", x.data_ptr(), xs, gate.data_ptr(), gs, up.data_ptr(), us, _ACTS[activation], tokens,
               wide, dim, _LP[x.dtype], out.data_ptr(), wide, status.data_ptr(), None, 0, A._stream(stream))
