@@ -73,30 +73,55 @@ __device__ __forceinline__ float sigmoid(float x) { return rcp_approx(1.0f + exp
 constexpr float kTanhScale = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kTanhCube = 0.044715f;
 
+// P = erfc(-g / sqrt(2)) / 2 from q = erfc(x) / 2 at x = |g| / sqrt(2): (1 + 2 x) exp(x^2) erfc(x)
+// is a smooth function of t = (x - 2.5) / (x + 2.5) over all x >= 0 (Shepherd and Laframboise,
+// "Chebyshev approximation of (1 + 2x) exp(x^2) erfc x in 0 <= x < infinity", Math. Comp. 36,
+// 1981); the coefficients are a Chebyshev fit of degree 9 of half of it, 1.5e-7 off.  With the
+// exponential rounded as it is here q is off by at most 0.4 (g^2 / 2 + 16) 2^-22 of itself.
+// (erfcf took 120 cycles an element, which showed: 8184 x 1600 x 4264 forward 138 us.)
+__device__ __forceinline__ float normal_share(float g, float bell) {
+    const float x = fminf(fabsf(g) * 0.70710678118654752f, 16.0f);
+    const float t = (x - 2.5f) * rcp_approx(x + 2.5f);
+    float h = __fmaf_rn(2.022946865e-04f, t, 1.512481249e-04f);
+    h = __fmaf_rn(h, t, -2.088966779e-03f);
+    h = __fmaf_rn(h, t, 5.443191039e-04f);
+    h = __fmaf_rn(h, t, 1.633777283e-02f);
+    h = __fmaf_rn(h, t, -5.151086301e-02f);
+    h = __fmaf_rn(h, t, 7.882248610e-02f);
+    h = __fmaf_rn(h, t, -4.950888082e-02f);
+    h = __fmaf_rn(h, t, -6.117876619e-02f);
+    h = __fmaf_rn(h, t, 6.324190497e-01f);
+    const float q = bell * (h * rcp_approx(__fmaf_rn(2.0f, x, 1.0f)));
+    return g < 0.0f ? q : 1.0f - q;
+}
+
 // Each activation is g P(g), its derivative P + g P'.
 //   silu       P = 1 / (1 + exp(-g))
 //   gelu       P = erfc(-g / sqrt(2)) / 2
 //   gelu_tanh  P = (1 + tanh(y)) / 2 = 1 / (1 + exp(-2 y)),  2 y = kTanhScale (g + kTanhCube g^3)
 template <int ACT>
-__device__ __forceinline__ float share_of(float g) {
-    if constexpr (ACT == ZERO_ACT_SILU) return sigmoid(g);
-    if constexpr (ACT == ZERO_ACT_GELU) return 0.5f * erfcf(g * -0.70710678118654752f);
-    return sigmoid(kTanhScale * __fmaf_rn(kTanhCube * g, g * g, g));
-}
-
-// P' by P
-template <int ACT>
-__device__ __forceinline__ float share_slope(float g, float p) {
-    if constexpr (ACT == ZERO_ACT_SILU) return p * (1.0f - p);
-    if constexpr (ACT == ZERO_ACT_GELU) return 0.3989422804014327f * exp2_approx(g * g * (-0.5f * kLog2e));
-    return p * (1.0f - p) * (kTanhScale * __fmaf_rn(3.0f * kTanhCube * g, g, 1.0f));
+__device__ __forceinline__ float share_of(float g, float &derivative) {
+    if constexpr (ACT == ZERO_ACT_GELU) {
+        const float bell = exp2_approx(g * g * (-0.5f * kLog2e));
+        derivative = 0.3989422804014327f * bell;
+        return normal_share(g, bell);
+    } else if constexpr (ACT == ZERO_ACT_SILU) {
+        const float p = sigmoid(g);
+        derivative = p * (1.0f - p);
+        return p;
+    } else {
+        const float p = sigmoid(kTanhScale * __fmaf_rn(kTanhCube * g, g * g, g));
+        derivative = p * (1.0f - p) * (kTanhScale * __fmaf_rn(3.0f * kTanhCube * g, g, 1.0f));
+        return p;
+    }
 }
 
 // out of n columns, g and u in place
 template <int ACT, int N>
 __device__ __forceinline__ void outs_of(const float (&g)[N], float (&u)[N]) {
+    float unused;
 #pragma unroll
-    for (int i = 0; i < N; ++i) u[i] = g[i] * share_of<ACT>(g[i]) * u[i];
+    for (int i = 0; i < N; ++i) u[i] = g[i] * share_of<ACT>(g[i], unused) * u[i];
 }
 
 // dg and du of n columns, in g's and u's place
@@ -104,8 +129,9 @@ template <int ACT, int N>
 __device__ __forceinline__ void slopes_of(const float (&go)[N], float (&g)[N], float (&u)[N]) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const float p = share_of<ACT>(g[i]);
-        const float slope = __fmaf_rn(g[i], share_slope<ACT>(g[i], p), p);
+        float derivative;
+        const float p = share_of<ACT>(g[i], derivative);
+        const float slope = __fmaf_rn(g[i], derivative, p);
         const float du = go[i] * (g[i] * p);
         g[i] = go[i] * u[i] * slope;
         u[i] = du;
@@ -123,8 +149,8 @@ struct GatedParams {
     CUtensorMap dg_out, du_out;  // slopes: 32 of F x 32 tokens
     CUtensorMap dg_k, du_k;      // slopes: 64 of F x 128 tokens
     CUtensorMap dg_mn, du_mn;    // slopes: 64 of F x 64 tokens
-    CUtensorMap gx_out;          // grad_x: 64 of D x 32 tokens, or the partial sums: 32 of D x 32 rows, float
-    CUtensorMap ggate_out, gup_out;  // 64 of D x 32 of F
+    CUtensorMap gx_out;          // grad_x: 32 of D x 32 tokens, or the partial sums: 16 of D x 32 rows, float
+    CUtensorMap ggate_out, gup_out;  // 32 of D x 32 of F
     long long tokens, rows;
     int wide, dim, splits;
     int step;  // columns of a tile of both projections
@@ -136,19 +162,35 @@ struct GatedParams {
     long long wait_cycles;
 };
 
-// 32 rows of 64 bytes, one a lane, to a box of `map`: put_rows with half the columns and two
-// buffers a warp, which stores in turn.
-__device__ __forceinline__ void put_half_rows(const uint32_t (&w)[16], uint32_t buffer, int lane, const CUtensorMap *map, int x, int y, bool skip) {
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-    __syncwarp();
+// A warp's results leave through two buffers of 32 rows of 64 bytes, a row a lane, with the
+// 64-byte swizzle: a store reads one while the other is filled.  (With one of 128 bytes a row
+// every store waited for the one before, 1600 cycles each: most of what a tile whose sums
+// are short takes.)
+
+// 32 bytes of this lane's row, the first or second half
+__device__ __forceinline__ void fill_half(const uint32_t (&w)[8], uint32_t buffer, int lane, int half) {
     const uint32_t row = buffer + lane * 64;
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + ((c ^ (lane >> 1 & 3)) << 4)), "r"(w[4 * c]),
+    for (int c = 0; c < 2; ++c)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + (((2 * half + c) ^ (lane >> 1 & 3)) << 4)), "r"(w[4 * c]),
                      "r"(w[4 * c + 1]), "r"(w[4 * c + 2]), "r"(w[4 * c + 3])
                      : "memory");
+}
+
+// until at most PENDING of the last stores still read their buffers
+template <int PENDING>
+__device__ __forceinline__ void buffer_free(int lane) {
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(PENDING) : "memory");
+    __syncwarp();
+}
+
+// what the lanes have filled, visible to the stores
+__device__ __forceinline__ void buffer_filled() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
+}
+
+__device__ __forceinline__ void store_half(uint32_t buffer, int lane, const CUtensorMap *map, int x, int y, bool skip) {
     if (lane == 0) {
         if (!skip) tma_store(map, x, y, buffer);
         store_commit();
@@ -415,90 +457,104 @@ gated_products(const __grid_constant__ GatedParams p) {
         uint32_t acc_phase = 0;
         for (int j = 0; work.at(j, t); ++j) {
             const int row0 = t.m0 + (int)rank * kHalf + quad * 32;  // this warp's first row of M
-            uint4 grad[MODE == kSlopes ? 2 : 1][4];
-            if constexpr (MODE == kSlopes) {  // while the sums are under way
+            // grad_out of the next 16 elements of this lane's row
+            uint4 grad[2];
+            const auto ask = [&](int c) {
                 const long long row = row0 + lane;
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int c = group * 64 + 32 * h, f = t.n0 / 2 + c + 8 * i;
-                        grad[h][i] = row < p.tokens && c < t.width / 2 && f < p.wide ? __ldg(p.grad_out + row * p.grad_stride + f / 8)
-                                                                                    : make_uint4(0u, 0u, 0u, 0u);
-                    }
-            }
+                for (int i = 0; i < 2; ++i) {
+                    const int f = t.n0 / 2 + c + 8 * i;
+                    grad[i] = row < p.tokens && f < p.wide ? __ldg(p.grad_out + row * p.grad_stride + f / 8) : make_uint4(0u, 0u, 0u, 0u);
+                }
+            };
+            if constexpr (MODE == kSlopes) ask(group * 64);
             const bool got = wait_for(&sh.acc_full[buf], acc_phase, dead, limit, p.status);
             if (!__all_sync(0xffffffffu, got)) break;
             tc_fence_after();
             const uint32_t acc = tmem + buf * kTileN + ((uint32_t)(quad * 32) << 16);
-            if constexpr (MODE == kForward) {
+            if constexpr (MODE != kGradients) {
+                // 16 elements at a time: short code, which a kernel of one tile a pair reads for the first time
 #pragma unroll 1
-                for (int c = group * 64; c < group * 64 + 64 && c < t.width / 2; c += 32) {
-                    const int f = t.n0 / 2 + c;
-                    float g[32], u[32];
-                    uint32_t w[16];
-                    tmem_load32(acc + c, g);
-                    tmem_load32(acc + t.width / 2 + c, u);
-                    if (p.act == ZERO_ACT_SILU) outs_of<ZERO_ACT_SILU>(g, u);
-                    else if (p.act == ZERO_ACT_GELU) outs_of<ZERO_ACT_GELU>(g, u);
-                    else outs_of<ZERO_ACT_GELU_TANH>(g, u);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) w[i] = pack_lp<BF16>(u[2 * i], u[2 * i + 1]);
-                    put_half_rows(w, buffer + turn * (kStoreBytes / 2), lane, &p.out, f, row0, row0 >= p.tokens || f >= p.wide);
-                    turn ^= 1;
-                }
-            } else if constexpr (MODE == kSlopes) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int c = group * 64 + 32 * h, f = t.n0 / 2 + c;
-                    if (c >= t.width / 2) break;
-                    float g[32], u[32], go[32];
-                    uint32_t w[16];
-                    tmem_load32(acc + c, g);
-                    tmem_load32(acc + t.width / 2 + c, u);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float x[8];
-                        widen8<BF16>(grad[h][i], x);
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) go[8 * i + k] = BF16 ? x[k] : x[k] * scale;
-                    }
-                    if (p.act == ZERO_ACT_SILU) slopes_of<ZERO_ACT_SILU>(go, g, u);
-                    else if (p.act == ZERO_ACT_GELU) slopes_of<ZERO_ACT_GELU>(go, g, u);
-                    else slopes_of<ZERO_ACT_GELU_TANH>(go, g, u);
+                for (int c = group * 64; c < group * 64 + 64 && c < (t.width / 2 + 31 & ~31); c += 16) {
+                    const int f = t.n0 / 2 + (c & ~31);
                     const bool skip = row0 >= p.tokens || f >= p.wide;
+                    float g[16], u[16];
+                    uint32_t w[8];
+                    tmem_load16(acc + c, g);
+                    tmem_load16(acc + t.width / 2 + c, u);
+                    if constexpr (MODE == kForward) {
+                        if (p.act == ZERO_ACT_SILU) outs_of<ZERO_ACT_SILU>(g, u);
+                        else if (p.act == ZERO_ACT_GELU) outs_of<ZERO_ACT_GELU>(g, u);
+                        else outs_of<ZERO_ACT_GELU_TANH>(g, u);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) w[i] = pack_lp<BF16>(g[2 * i], g[2 * i + 1]);
-                    put_half_rows(w, buffer, lane, &p.dg_out, f, row0, skip);
+                        for (int i = 0; i < 8; ++i) w[i] = pack_lp<BF16>(u[2 * i], u[2 * i + 1]);
+                        const uint32_t to = buffer + turn * (kStoreBytes / 2);
+                        if (!(c & 16)) buffer_free<1>(lane);
+                        fill_half(w, to, lane, c >> 4 & 1);
+                        if (c & 16) {
+                            buffer_filled();
+                            store_half(to, lane, &p.out, f, row0, skip);
+                            turn ^= 1;
+                        }
+                    } else {
+                        float go[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) w[i] = pack_lp<BF16>(u[2 * i], u[2 * i + 1]);
-                    put_half_rows(w, buffer + kStoreBytes / 2, lane, &p.du_out, f, row0, skip);
+                        for (int i = 0; i < 2; ++i) {
+                            float x[8];
+                            widen8<BF16>(grad[i], x);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) go[8 * i + k] = BF16 ? x[k] : x[k] * scale;
+                        }
+                        ask(c + 16);
+                        if (p.act == ZERO_ACT_SILU) slopes_of<ZERO_ACT_SILU>(go, g, u);
+                        else if (p.act == ZERO_ACT_GELU) slopes_of<ZERO_ACT_GELU>(go, g, u);
+                        else slopes_of<ZERO_ACT_GELU_TANH>(go, g, u);
+                        if (!(c & 16)) buffer_free<0>(lane);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) w[i] = pack_lp<BF16>(g[2 * i], g[2 * i + 1]);
+                        fill_half(w, buffer, lane, c >> 4 & 1);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) w[i] = pack_lp<BF16>(u[2 * i], u[2 * i + 1]);
+                        fill_half(w, buffer + kStoreBytes / 2, lane, c >> 4 & 1);
+                        if (c & 16) {
+                            buffer_filled();
+                            store_half(buffer, lane, &p.dg_out, f, row0, skip);
+                            store_half(buffer + kStoreBytes / 2, lane, &p.du_out, f, row0, skip);
+                        }
+                    }
                 }
             } else {
-                const int first = group * kResultColumns;
-                if (t.kind == kGradX && p.splits > 1) {
-                    for (int c = first; c < first + kResultColumns; c += 32) {
+                const bool sums = t.kind == kGradX && p.splits > 1;  // floats: 16 columns in 64 bytes, else 32
+                const CUtensorMap *to = t.kind == kGradX ? &p.gx_out : t.kind == kGradGate ? &p.ggate_out : &p.gup_out;
+                const bool skip = !sums && row0 >= (t.kind == kGradX ? p.tokens : (long long)p.wide);
+                const int y = sums ? (int)(t.split * p.rows) + row0 : row0;
+#pragma unroll 1
+                for (int c = group * kResultColumns; c < group * kResultColumns + kResultColumns && c < t.width; c += sums ? 16 : 32) {
+                    uint32_t lo[8], hi[8];
+                    if (sums) {
+                        float z[16];
+                        tmem_load16(acc + c, z);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            lo[i] = __float_as_uint(z[i] * factor);
+                            hi[i] = __float_as_uint(z[8 + i] * factor);
+                        }
+                    } else {
                         float z[32];
                         tmem_load32(acc + c, z);
-                        uint32_t w[32];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(z[i] * factor);
-                        put_rows(w, buffer, lane, &p.gx_out, t.n0 + c, (int)(t.split * p.rows) + row0, false, t.n0 + c >= p.dim);
-                    }
-                } else {
-                    const CUtensorMap *to = t.kind == kGradX ? &p.gx_out : t.kind == kGradGate ? &p.ggate_out : &p.gup_out;
-                    const bool skip = row0 >= (t.kind == kGradX ? p.tokens : (long long)p.wide);
-                    for (int c = first; c < first + kResultColumns; c += 64) {
-                        uint32_t w[32];
-#pragma unroll
-                        for (int h = 0; h < 64; h += 32) {
-                            float z[32];
-                            tmem_load32(acc + c + h, z);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) w[h / 2 + i] = pack_lp<BF16>(z[2 * i] * factor, z[2 * i + 1] * factor);
+                        for (int i = 0; i < 8; ++i) {
+                            lo[i] = pack_lp<BF16>(z[2 * i] * factor, z[2 * i + 1] * factor);
+                            hi[i] = pack_lp<BF16>(z[16 + 2 * i] * factor, z[16 + 2 * i + 1] * factor);
                         }
-                        put_rows(w, buffer, lane, to, t.n0 + c, row0, false, skip || t.n0 + c >= p.dim);
                     }
+                    const uint32_t at = buffer + turn * (kStoreBytes / 2);
+                    buffer_free<1>(lane);
+                    fill_half(lo, at, lane, 0);
+                    fill_half(hi, at, lane, 1);
+                    buffer_filled();
+                    store_half(at, lane, to, t.n0 + c, y, skip || t.n0 + c >= p.dim);
+                    turn ^= 1;
                 }
             }
             tc_fence_before();
@@ -995,10 +1051,10 @@ cudaError_t backward_impl(const GatedArgs &a, cudaStream_t stream) {
         !make_map(&p.du_out, du, a.tokens, a.wide, a.wide, a.lp, false, 32, true) ||
         !map(&p.dg_k, dg, a.tokens, a.wide, a.wide, kHalf) || !map(&p.du_k, du, a.tokens, a.wide, a.wide, kHalf) ||
         !map(&p.dg_mn, dg, a.tokens, a.wide, a.wide, kTileK) || !map(&p.du_mn, du, a.tokens, a.wide, a.wide, kTileK) ||
-        !map(&p.ggate_out, a.grad_gate, a.wide, a.dim, a.grad_gate_stride, 32) ||
-        !map(&p.gup_out, a.grad_up, a.wide, a.dim, a.grad_up_stride, 32) ||
-        !(l.splits > 1 ? make_map(&p.gx_out, sums, l.splits * l.rows, a.dim, a.dim, a.lp, true, 32)
-                       : map(&p.gx_out, a.grad_x, a.tokens, a.dim, a.grad_x_stride, 32)))
+        !make_map(&p.ggate_out, a.grad_gate, a.wide, a.dim, a.grad_gate_stride, a.lp, false, 32, true) ||
+        !make_map(&p.gup_out, a.grad_up, a.wide, a.dim, a.grad_up_stride, a.lp, false, 32, true) ||
+        !(l.splits > 1 ? make_map(&p.gx_out, sums, l.splits * l.rows, a.dim, a.dim, a.lp, true, 32, true)
+                       : make_map(&p.gx_out, a.grad_x, a.tokens, a.dim, a.grad_x_stride, a.lp, false, 32, true)))
         return cudaErrorNotSupported;
     p.tokens = a.tokens;
     p.rows = l.rows;
