@@ -16,6 +16,7 @@ devices raise ZeroError (ZERO_EINVAL) before any device work.
 from operator import attrgetter
 from typing import NamedTuple, Optional
 
+import numpy as np
 import torch
 
 from . import _abi as A
@@ -59,22 +60,33 @@ def adamw_state(params, bits=32, stream=None):
 
 
 def _one(where, name, t, dtype, device):
-    if t is not None and (t.dtype != dtype or t.numel() != 1 or t.get_device() != device):
+    """The address of one element, or None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.numel() != 1 or t.get_device() != device:
         _refuse(where, "%s must be one %s on the current CUDA device" % (name, dtype))
+    return t.data_ptr()
+
+
+def _vector_at(where, name, t, dtype, n, device):
+    """The address of one of the state's tensors."""
+    if (not isinstance(t, _T) or t.dtype != dtype or t.ndim != 1 or t.numel() != n or t.get_device() != device
+            or not t.is_contiguous()):
+        _refuse(where, "the state's %s must be %d contiguous %s on the current CUDA device" % (name, n, dtype))
+    return t.data_ptr()
 
 
 def _moments(where, state, total, device):
-    """Whether the state holds 8 bits, having looked it over."""
+    """(format, addresses of m, v, their scales and the record) of a state, looked over."""
     m, v, m_scales, v_scales, record = state
-    eight = m.dtype == torch.int8
-    want = [("m", m, torch.int8 if eight else torch.float32, total), ("v", v, torch.uint8 if eight else torch.float32, total),
-            ("record", record, torch.int64, 2)]
-    if eight:
-        want += [("m_scales", m_scales, torch.float32, total // _BLOCK), ("v_scales", v_scales, torch.float32, total // _BLOCK)]
-    for name, t, dtype, n in want:
-        if not isinstance(t, _T) or t.dtype != dtype or t.shape != (n,) or t.get_device() != device or not t.is_contiguous():
-            _refuse(where, "the state's %s must be %d contiguous %s on the current CUDA device" % (name, n, dtype))
-    return eight
+    at_record = _vector_at(where, "record", record, torch.int64, 2, device)
+    if m.dtype != torch.int8:
+        return (A.ZERO_MOMENTS_FP32, _vector_at(where, "m", m, torch.float32, total, device),
+                _vector_at(where, "v", v, torch.float32, total, device), None, None, at_record)
+    return (A.ZERO_MOMENTS_8BIT, _vector_at(where, "m", m, torch.int8, total, device),
+            _vector_at(where, "v", v, torch.uint8, total, device),
+            _vector_at(where, "m_scales", m_scales, torch.float32, total // _BLOCK, device),
+            _vector_at(where, "v_scales", v_scales, torch.float32, total // _BLOCK, device), at_record)
 
 
 def adamw_step(params, grads, state, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, copies=None, loss_scale=1.0,
@@ -105,19 +117,18 @@ def adamw_step(params, grads, state, lr, beta1=0.9, beta2=0.999, eps=1e-8, weigh
         copy_lens, at_copies = _gather(where, "copies", copies, copies[0].dtype, device)
     if grad_lens != lens or (at_copies is not None and copy_lens != lens):
         _refuse(where, "a gradient or copy has another length than its parameter")
-    total = sum([-(-n // _BLOCK) for n in lens]) * _BLOCK
-    eight = _moments(where, state, total, device)
-    _one(where, "coef", coef, torch.float32, device)
-    _one(where, "skip", skip, torch.int32, device)
+    if len(lens) <= 64:   # a short list costs less than numpy's calls
+        blocks = sum([(n + _BLOCK - 1) // _BLOCK for n in lens])
+    else:
+        blocks = int(((np.frombuffer(lens, np.int64) + (_BLOCK - 1)) // _BLOCK).sum())
+    moments = _moments(where, state, blocks * _BLOCK, device)
+    at_coef = _one(where, "coef", coef, torch.float32, device)
+    at_skip = _one(where, "skip", skip, torch.int32, device)
     if not -2 ** 31 <= seed < 2 ** 31:
         _refuse(where, "seed outside 32 bits")
-    m, v, m_scales, v_scales, record = state
-    addr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-    table = lambda a: None if a is None else a.buffer_info()[0]  # noqa: E731
-    _call("zero_adamw_step", len(lens), table(at_params), table(at_grads), _CLIP[grads[0].dtype], table(at_copies), copy_type,
-          table(lens), A.ZERO_MOMENTS_8BIT if eight else A.ZERO_MOMENTS_FP32, m.data_ptr(), v.data_ptr(),
-          addr(m_scales), addr(v_scales), record.data_ptr(), lr, beta1, beta2, eps, weight_decay, loss_scale, addr(coef),
-          addr(skip), seed, A._stream(stream))
+    _call("zero_adamw_step", len(lens), at_params.buffer_info()[0], at_grads.buffer_info()[0], _CLIP[grads[0].dtype],
+          at_copies and at_copies.buffer_info()[0], copy_type, lens.buffer_info()[0], *moments, lr, beta1, beta2, eps,
+          weight_decay, loss_scale, at_coef, at_skip, seed, A._stream(stream))
 
 
 def adamw_moments(state, dtype=torch.float32, stream=None):
@@ -126,14 +137,13 @@ def adamw_moments(state, dtype=torch.float32, stream=None):
     where = "adamw_moments"
     if dtype not in _CLIP:
         _refuse(where, "dtype must be float16, bfloat16 or float32")
-    m, v, m_scales, v_scales, record = state
-    device = torch._C._cuda_getDevice()
+    m, v = state[:2]
     if m.numel() % _BLOCK:
         _refuse(where, "a state's length is a multiple of %d" % _BLOCK)
+    fmt, *at, _ = _moments(where, state, m.numel(), torch._C._cuda_getDevice())
     with _on(stream):
-        if not _moments(where, state, m.numel(), device):
+        if fmt == A.ZERO_MOMENTS_FP32:
             return m.to(dtype), v.to(dtype)
         m_out, v_out = (torch.empty(m.shape, dtype=dtype, device=m.device) for _ in range(2))
-        _call("zero_adamw_values", m.data_ptr(), v.data_ptr(), m_scales.data_ptr(), v_scales.data_ptr(), m.numel(), _CLIP[dtype],
-              m_out.data_ptr(), v_out.data_ptr(), A._stream(stream))
+        _call("zero_adamw_values", *at, m.numel(), _CLIP[dtype], m_out.data_ptr(), v_out.data_ptr(), A._stream(stream))
     return m_out, v_out
