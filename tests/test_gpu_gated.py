@@ -197,17 +197,32 @@ def test_rows_do_not_touch_each_other(t, bad):
     assert not torch.isfinite(gg2[7]).any() and not torch.isfinite(gu2[7]).any()
 
 
-@pytest.mark.parametrize("t", [1, 3, 40, 300])
-def test_outputs_stay_in_their_rows(t):
-    """Output rows that are parts of wider ones, and what stands behind the last row."""
-    x, gate, up, grad = case(t, 72, 136, BF)
+@pytest.mark.parametrize("left", [0, 8, 16])
+@pytest.mark.parametrize("t,d,f", [(1, 72, 136), (3, 264, 72), (40, 72, 136), (300, 520, 264), (300, 8, 8)])
+def test_outputs_stay_in_their_rows(t, d, f, left):
+    """Output rows that are parts of wider ones, some of them off the sectors of 32 bytes, and what stands around them."""
+    x, gate, up, grad = case(t, d, f, BF)
     want = Z.gated_linear_backward(x, gate, up, grad)
-    wide = [torch.full((n + 5, 72 + 24), 7.0, device="cuda", dtype=BF) for n in (t, 136, 136)]
-    into = [w[:n, :72] for w, n in zip(wide, (t, 136, 136))]
+    wide = [torch.full((n + 5, d + 24), 7.0, device="cuda", dtype=BF) for n in (t, f, f)]
+    into = [w[:n, left:left + d] for w, n in zip(wide, (t, f, f))]
     got = Z.gated_linear_backward(x, gate, up, grad, grad_x=into[0], grad_gate=into[1], grad_up=into[2])
-    for g, i, w, r, n in zip(got, into, wide, want, (t, 136, 136)):
+    for g, i, w, r, n in zip(got, into, wide, want, (t, f, f)):
         assert g.data_ptr() == i.data_ptr() and torch.equal(i, r)
-        assert (w[:, 72:] == 7).all() and (w[n:] == 7).all()
+        assert (w[:, :left] == 7).all() and (w[:, left + d:] == 7).all() and (w[n:] == 7).all()
+
+
+@pytest.mark.parametrize("left", [0, 8])
+@pytest.mark.parametrize("t,d,f", [(3, 64, 136), (70, 64, 136), (300, 64, 1000)])
+def test_forward_output_stays_in_its_rows(t, d, f, left):
+    """The C call's output among wider rows."""
+    x, gate, up, _ = case(t, d, f, BF)
+    want = Z.gated_linear(x, gate, up)
+    wide = torch.full((t + 5, f + 24), 7.0, device="cuda", dtype=BF)
+    status = torch.zeros(1, device="cuda", dtype=torch.int32)
+    into = wide[:t, left:left + f]
+    Z.zero_gated_forward(x, d, gate, d, up, d, Z.ZERO_ACT_SILU, t, f, d, Z.ZERO_BF16, into, f + 24, status, None, 0)
+    assert torch.equal(into, want) and int(status) == 0
+    assert (wide[:, :left] == 7).all() and (wide[:, left + f:] == 7).all() and (wide[t:] == 7).all()
 
 
 def test_no_tokens():

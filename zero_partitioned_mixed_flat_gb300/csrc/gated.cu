@@ -22,6 +22,7 @@
 namespace zk {
 namespace {
 
+constexpr int kGatedSmem = 1024 + kStages * kStageBytes;
 constexpr int kTileCost = 4;  // blocks of K that starting and storing a tile cost, about
 
 enum Mode { kForward = 0, kSlopes = 1, kGradients = 2 };
@@ -32,6 +33,7 @@ constexpr int kTopBlocks = 304, kTopThreads = 256;
 
 struct GatedLayout {
     int64_t rows;   // tokens rounded up to whole tiles
+    int64_t stride; // of the slopes' rows: whole sectors
     int splits;     // partial sums of grad_x
     int64_t slope_gate, slope_up, sums, bytes;  // byte offsets
 };
@@ -52,8 +54,9 @@ GatedLayout gated_layout(int64_t tokens, int64_t wide, int dim) {
         at = up(at + bytes, 1024);
         return here;
     };
-    l.slope_gate = take(tokens * wide * 2);
-    l.slope_up = take(tokens * wide * 2);
+    l.stride = up(wide, 16);
+    l.slope_gate = take(tokens * l.stride * 2);
+    l.slope_up = take(tokens * l.stride * 2);
     l.sums = take(l.splits > 1 ? l.splits * l.rows * dim * 4 : 0);
     l.bytes = at;
     return l;
@@ -140,62 +143,85 @@ __device__ __forceinline__ void slopes_of(const float (&go)[N], float (&g)[N], f
 
 // --------------------------------------------------------------------- products
 
+// Results go from registers to memory, 32 bytes of its row a lane: a whole sector, where the
+// rows begin at one.  (Through shared memory and TMA a warp took 540 cycles for 32 rows of 64
+// bytes, most of them waiting to fill, fence and start the store: as long as the sums of a
+// tile with a K of 512, and the products read shared memory meanwhile.)
+__device__ __forceinline__ void store_sector(void *to, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// A matrix of lp results.
+struct Rows {
+    uint16_t *at;
+    long long stride;
+    int cols;
+};
+
+// Writes a stretch of one row, 16 elements at a time, in whole sectors: where the row lies 16
+// bytes off one, the last eight elements wait for the next eight, and only the stretch's two
+// ends are half sectors.  (With halves everywhere 129 x 4088 x 10920's gradients took 198 us
+// and not 163.)
+struct RowWriter {
+    uint16_t *at;     // of column 0
+    int cols;
+    bool odd, first;
+    uint32_t carry[4];
+
+    __device__ __forceinline__ RowWriter(const Rows &m, long long row, int col) {
+        at = m.at + row * m.stride;
+        cols = m.cols;
+        odd = reinterpret_cast<uintptr_t>(at + col) & 16u;
+        first = true;
+    }
+    static __device__ __forceinline__ void store_four(uint16_t *to, const uint32_t *w) {
+        *reinterpret_cast<uint4 *>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    // columns col to col + 15, or as many of them as there are (a multiple of 8)
+    __device__ __forceinline__ void put(int col, const uint32_t (&w)[8]) {
+        uint32_t s[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            s[i] = odd ? carry[i] : w[i];
+            s[4 + i] = odd ? w[i] : w[4 + i];
+            carry[i] = w[4 + i];
+        }
+        const int from = odd ? col - 8 : col;  // eight and eight elements from here
+        const bool lo = !(odd && first) && from < cols, hi = from + 8 < cols;
+        if (lo && hi) store_sector(at + from, s);
+        else if (lo) store_four(at + from, s);
+        else if (hi) store_four(at + from + 8, s + 4);
+        first = false;
+    }
+    // after the last column before `end`
+    __device__ __forceinline__ void finish(int end) const {
+        if (odd && !first && end - 8 < cols) store_four(at + end - 8, carry);
+    }
+};
+
 struct GatedParams {
     CUtensorMap x_k;             // x: boxes 64 of D x 128 tokens
     CUtensorMap gate_k, up_k;    // matrices: 64 of D x half a tile's columns
-    CUtensorMap out;             // out: 32 of F x 32 tokens
     CUtensorMap x_mn;            // x: 64 of D x 64 tokens
     CUtensorMap gate_mn, up_mn;  // matrices: 64 of D x 64 of F
-    CUtensorMap dg_out, du_out;  // slopes: 32 of F x 32 tokens
     CUtensorMap dg_k, du_k;      // slopes: 64 of F x 128 tokens
     CUtensorMap dg_mn, du_mn;    // slopes: 64 of F x 64 tokens
-    CUtensorMap gx_out;          // grad_x: 32 of D x 32 tokens, or the partial sums: 16 of D x 32 rows, float
-    CUtensorMap ggate_out, gup_out;  // 32 of D x 32 of F
     long long tokens, rows;
     int wide, dim, splits;
     int step;  // columns of a tile of both projections
     int act;
+    Rows out;                // forward
+    Rows dg, du;             // slopes
+    Rows gx, ggate, gup;     // gradients
+    float *sums;             // of gx, where splits > 1: [split][rows][dim]
     const uint4 *grad_out;
     long long grad_stride;  // vectors
     const float *tops;      // NULL: the slopes are not scaled
     int *status;
     long long wait_cycles;
 };
-
-// A warp's results leave through two buffers of 32 rows of 64 bytes, a row a lane, with the
-// 64-byte swizzle: a store reads one while the other is filled.  (With one of 128 bytes a row
-// every store waited for the one before, 1600 cycles each: most of what a tile whose sums
-// are short takes.)
-
-// 32 bytes of this lane's row, the first or second half
-__device__ __forceinline__ void fill_half(const uint32_t (&w)[8], uint32_t buffer, int lane, int half) {
-    const uint32_t row = buffer + lane * 64;
-#pragma unroll
-    for (int c = 0; c < 2; ++c)
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + (((2 * half + c) ^ (lane >> 1 & 3)) << 4)), "r"(w[4 * c]),
-                     "r"(w[4 * c + 1]), "r"(w[4 * c + 2]), "r"(w[4 * c + 3])
-                     : "memory");
-}
-
-// until at most PENDING of the last stores still read their buffers
-template <int PENDING>
-__device__ __forceinline__ void buffer_free(int lane) {
-    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(PENDING) : "memory");
-    __syncwarp();
-}
-
-// what the lanes have filled, visible to the stores
-__device__ __forceinline__ void buffer_filled() {
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    __syncwarp();
-}
-
-__device__ __forceinline__ void store_half(uint32_t buffer, int lane, const CUtensorMap *map, int x, int y, bool skip) {
-    if (lane == 0) {
-        if (!skip) tma_store(map, x, y, buffer);
-        store_commit();
-    }
-}
 
 // The work of one launch, and which of it each pair does, in order: every pair-th tile,
 // gradients first the tiles of grad_x, few and long; the pairs that get one fewer of
@@ -450,17 +476,16 @@ gated_products(const __grid_constant__ GatedParams p) {
     } else {  // ------------------------------------------------------ results
         const int quad = warp & 3;              // the quarter of the lanes this warp may read
         const int group = (warp - 2) >> 2;      // which half of the columns it takes
-        const uint32_t buffer = stage0 + kStages * kStageBytes + (warp - 2) * kStoreBytes;
         const float scale = MODE == kForward ? 1.0f : scale_of(p.tops);
         const float factor = 1.0f / scale;      // powers of two
-        int buf = 0, turn = 0;
+        int buf = 0;
         uint32_t acc_phase = 0;
         for (int j = 0; work.at(j, t); ++j) {
             const int row0 = t.m0 + (int)rank * kHalf + quad * 32;  // this warp's first row of M
+            const long long row = row0 + lane;
             // grad_out of the next 16 elements of this lane's row
             uint4 grad[2];
             const auto ask = [&](int c) {
-                const long long row = row0 + lane;
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int f = t.n0 / 2 + c + 8 * i;
@@ -474,10 +499,12 @@ gated_products(const __grid_constant__ GatedParams p) {
             const uint32_t acc = tmem + buf * kTileN + ((uint32_t)(quad * 32) << 16);
             if constexpr (MODE != kGradients) {
                 // 16 elements at a time: short code, which a kernel of one tile a pair reads for the first time
+                const int f0 = t.n0 / 2 + group * 64;
+                RowWriter first(MODE == kForward ? p.out : p.dg, row, f0), second(p.du, row, f0);
+                int c = group * 64;
 #pragma unroll 1
-                for (int c = group * 64; c < group * 64 + 64 && c < (t.width / 2 + 31 & ~31); c += 16) {
-                    const int f = t.n0 / 2 + (c & ~31);
-                    const bool skip = row0 >= p.tokens || f >= p.wide;
+                for (; c < group * 64 + 64 && c < t.width / 2; c += 16) {
+                    const int f = t.n0 / 2 + c;
                     float g[16], u[16];
                     uint32_t w[8];
                     tmem_load16(acc + c, g);
@@ -488,14 +515,7 @@ gated_products(const __grid_constant__ GatedParams p) {
                         else outs_of<ZERO_ACT_GELU_TANH>(g, u);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) w[i] = pack_lp<BF16>(u[2 * i], u[2 * i + 1]);
-                        const uint32_t to = buffer + turn * (kStoreBytes / 2);
-                        if (!(c & 16)) buffer_free<1>(lane);
-                        fill_half(w, to, lane, c >> 4 & 1);
-                        if (c & 16) {
-                            buffer_filled();
-                            store_half(to, lane, &p.out, f, row0, skip);
-                            turn ^= 1;
-                        }
+                        if (row < p.tokens) first.put(f, w);
                     } else {
                         float go[16];
 #pragma unroll
@@ -509,53 +529,45 @@ gated_products(const __grid_constant__ GatedParams p) {
                         if (p.act == ZERO_ACT_SILU) slopes_of<ZERO_ACT_SILU>(go, g, u);
                         else if (p.act == ZERO_ACT_GELU) slopes_of<ZERO_ACT_GELU>(go, g, u);
                         else slopes_of<ZERO_ACT_GELU_TANH>(go, g, u);
-                        if (!(c & 16)) buffer_free<0>(lane);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) w[i] = pack_lp<BF16>(g[2 * i], g[2 * i + 1]);
-                        fill_half(w, buffer, lane, c >> 4 & 1);
+                        if (row < p.tokens) first.put(f, w);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) w[i] = pack_lp<BF16>(u[2 * i], u[2 * i + 1]);
-                        fill_half(w, buffer + kStoreBytes / 2, lane, c >> 4 & 1);
-                        if (c & 16) {
-                            buffer_filled();
-                            store_half(buffer, lane, &p.dg_out, f, row0, skip);
-                            store_half(buffer + kStoreBytes / 2, lane, &p.du_out, f, row0, skip);
-                        }
+                        if (row < p.tokens) second.put(f, w);
                     }
                 }
+                if (MODE == kForward && row < p.tokens) first.finish(t.n0 / 2 + c);  // the slopes' rows begin at sectors
             } else {
-                const bool sums = t.kind == kGradX && p.splits > 1;  // floats: 16 columns in 64 bytes, else 32
-                const CUtensorMap *to = t.kind == kGradX ? &p.gx_out : t.kind == kGradGate ? &p.ggate_out : &p.gup_out;
-                const bool skip = !sums && row0 >= (t.kind == kGradX ? p.tokens : (long long)p.wide);
-                const int y = sums ? (int)(t.split * p.rows) + row0 : row0;
+                const bool sums = t.kind == kGradX && p.splits > 1;
+                const Rows to = t.kind == kGradX ? p.gx : t.kind == kGradGate ? p.ggate : p.gup;
+                const bool mine = row < (t.kind == kGradX ? p.tokens : (long long)p.wide);
+                float *const part = p.sums + (t.split * p.rows + row) * p.dim;
+                RowWriter writer(to, row, t.n0 + group * kResultColumns);
+                int c = group * kResultColumns;
 #pragma unroll 1
-                for (int c = group * kResultColumns; c < group * kResultColumns + kResultColumns && c < t.width; c += sums ? 16 : 32) {
-                    uint32_t lo[8], hi[8];
+                for (; c < group * kResultColumns + kResultColumns && c < t.width; c += 32) {
+                    float z[32];
+                    tmem_load32(acc + c, z);
+                    const int col = t.n0 + c;
+                    uint32_t w[8];
                     if (sums) {
-                        float z[16];
-                        tmem_load16(acc + c, z);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            lo[i] = __float_as_uint(z[i] * factor);
-                            hi[i] = __float_as_uint(z[8 + i] * factor);
+                        for (int h = 0; h < 4; ++h) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(z[8 * h + i] * factor);
+                            if (mine && col + 8 * h < p.dim) store_sector(part + col + 8 * h, w);
                         }
                     } else {
-                        float z[32];
-                        tmem_load32(acc + c, z);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            lo[i] = pack_lp<BF16>(z[2 * i] * factor, z[2 * i + 1] * factor);
-                            hi[i] = pack_lp<BF16>(z[16 + 2 * i] * factor, z[16 + 2 * i + 1] * factor);
+                        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) w[i] = pack_lp<BF16>(z[16 * h + 2 * i] * factor, z[16 * h + 2 * i + 1] * factor);
+                            if (mine) writer.put(col + 16 * h, w);
                         }
                     }
-                    const uint32_t at = buffer + turn * (kStoreBytes / 2);
-                    buffer_free<1>(lane);
-                    fill_half(lo, at, lane, 0);
-                    fill_half(hi, at, lane, 1);
-                    buffer_filled();
-                    store_half(at, lane, to, t.n0 + c, y, skip || t.n0 + c >= p.dim);
-                    turn ^= 1;
                 }
+                if (mine && !sums) writer.finish(t.n0 + c);
             }
             tc_fence_before();
             __syncwarp();
@@ -563,7 +575,6 @@ gated_products(const __grid_constant__ GatedParams p) {
             buf ^= 1;
             if (buf == 0) acc_phase ^= 1;
         }
-        if (lane == 0) store_wait_all();
     }
     __syncwarp();
     __syncthreads();
@@ -628,7 +639,8 @@ struct NarrowParams {
     long long out_stride;
     const uint16_t *grad_out;  // slopes
     long long grad_stride;
-    uint16_t *dg, *du;         // rows of `wide`
+    uint16_t *dg, *du;
+    long long slope_stride;
     const float *tops;
     int *status;
     long long wait_cycles;
@@ -691,8 +703,8 @@ __device__ __forceinline__ void narrow_results(const NarrowParams &p, long long 
         if (p.act == ZERO_ACT_SILU) slopes_of<ZERO_ACT_SILU>(go, g, u);
         else if (p.act == ZERO_ACT_GELU) slopes_of<ZERO_ACT_GELU>(go, g, u);
         else slopes_of<ZERO_ACT_GELU_TANH>(go, g, u);
-        *reinterpret_cast<uint2 *>(p.dg + t * p.wide + f) = make_uint2(pack_lp<BF16>(g[0], g[1]), pack_lp<BF16>(g[2], g[3]));
-        *reinterpret_cast<uint2 *>(p.du + t * p.wide + f) = make_uint2(pack_lp<BF16>(u[0], u[1]), pack_lp<BF16>(u[2], u[3]));
+        *reinterpret_cast<uint2 *>(p.dg + t * p.slope_stride + f) = make_uint2(pack_lp<BF16>(g[0], g[1]), pack_lp<BF16>(g[2], g[3]));
+        *reinterpret_cast<uint2 *>(p.du + t * p.slope_stride + f) = make_uint2(pack_lp<BF16>(u[0], u[1]), pack_lp<BF16>(u[2], u[3]));
     }
 }
 
@@ -914,12 +926,12 @@ int pairs_at_once() {
     static PerDevice kept;
     return kept.get([] {
         const int set = done_or_error(
-            cudaFuncSetAttribute(gated_products<BF16, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes));
+            cudaFuncSetAttribute(gated_products<BF16, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kGatedSmem));
         if (set < 0) return set;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2);
         cfg.blockDim = dim3(kProductThreads);
-        cfg.dynamicSmemBytes = kSmemBytes;
+        cfg.dynamicSmemBytes = kGatedSmem;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = 2;
@@ -959,7 +971,7 @@ cudaError_t launch_products(const GatedParams &p, int64_t tiles, cudaStream_t st
     if (pairs < 0) return (cudaError_t)-pairs;
     if (tiles > 0x3fffffff) return cudaErrorInvalidValue;
     const int64_t use = std::max<int64_t>(1, std::min<int64_t>(pairs, tiles));
-    return launch_pdl(gated_products<BF16, MODE>, dim3((unsigned)(2 * use)), dim3(kProductThreads), kSmemBytes, stream, p);
+    return launch_pdl(gated_products<BF16, MODE>, dim3((unsigned)(2 * use)), dim3(kProductThreads), kGatedSmem, stream, p);
 }
 
 template <bool BF16, int MODE>
@@ -990,6 +1002,7 @@ cudaError_t launch_narrow(const GatedArgs &a, uint16_t *dg, uint16_t *du, const 
     p.grad_stride = a.grad_out_stride;
     p.dg = dg;
     p.du = du;
+    p.slope_stride = up(a.wide, 16);
     p.tops = tops;
     p.status = a.status;
     p.wait_cycles = loss_wait();
@@ -1018,9 +1031,9 @@ cudaError_t forward_impl(const GatedArgs &a, cudaStream_t stream) {
     p.step = step_of(a.tokens, a.wide, a.dim, pairs);
     if (!encoder() || !make_map(&p.x_k, a.x, a.tokens, a.dim, a.x_stride, a.lp, false, kHalf) ||
         !make_map(&p.gate_k, a.gate, a.wide, a.dim, a.gate_stride, a.lp, false, p.step / 2) ||
-        !make_map(&p.up_k, a.up, a.wide, a.dim, a.up_stride, a.lp, false, p.step / 2) ||
-        !make_map(&p.out, a.out, a.tokens, a.wide, a.out_stride, a.lp, false, 32, true))
+        !make_map(&p.up_k, a.up, a.wide, a.dim, a.up_stride, a.lp, false, p.step / 2))
         return cudaErrorNotSupported;
+    p.out = {static_cast<uint16_t *>(a.out), a.out_stride, a.wide};
     p.tokens = a.tokens;
     p.wide = a.wide;
     p.dim = a.dim;
@@ -1047,14 +1060,8 @@ cudaError_t backward_impl(const GatedArgs &a, cudaStream_t stream) {
     if (!encoder() || !map(&p.x_k, a.x, a.tokens, a.dim, a.x_stride, kHalf) || !map(&p.gate_k, a.gate, a.wide, a.dim, a.gate_stride, p.step / 2) ||
         !map(&p.up_k, a.up, a.wide, a.dim, a.up_stride, p.step / 2) || !map(&p.x_mn, a.x, a.tokens, a.dim, a.x_stride, kTileK) ||
         !map(&p.gate_mn, a.gate, a.wide, a.dim, a.gate_stride, kTileK) || !map(&p.up_mn, a.up, a.wide, a.dim, a.up_stride, kTileK) ||
-        !make_map(&p.dg_out, dg, a.tokens, a.wide, a.wide, a.lp, false, 32, true) ||
-        !make_map(&p.du_out, du, a.tokens, a.wide, a.wide, a.lp, false, 32, true) ||
-        !map(&p.dg_k, dg, a.tokens, a.wide, a.wide, kHalf) || !map(&p.du_k, du, a.tokens, a.wide, a.wide, kHalf) ||
-        !map(&p.dg_mn, dg, a.tokens, a.wide, a.wide, kTileK) || !map(&p.du_mn, du, a.tokens, a.wide, a.wide, kTileK) ||
-        !make_map(&p.ggate_out, a.grad_gate, a.wide, a.dim, a.grad_gate_stride, a.lp, false, 32, true) ||
-        !make_map(&p.gup_out, a.grad_up, a.wide, a.dim, a.grad_up_stride, a.lp, false, 32, true) ||
-        !(l.splits > 1 ? make_map(&p.gx_out, sums, l.splits * l.rows, a.dim, a.dim, a.lp, true, 32, true)
-                       : make_map(&p.gx_out, a.grad_x, a.tokens, a.dim, a.grad_x_stride, a.lp, false, 32, true)))
+        !map(&p.dg_k, dg, a.tokens, a.wide, l.stride, kHalf) || !map(&p.du_k, du, a.tokens, a.wide, l.stride, kHalf) ||
+        !map(&p.dg_mn, dg, a.tokens, a.wide, l.stride, kTileK) || !map(&p.du_mn, du, a.tokens, a.wide, l.stride, kTileK))
         return cudaErrorNotSupported;
     p.tokens = a.tokens;
     p.rows = l.rows;
@@ -1062,6 +1069,12 @@ cudaError_t backward_impl(const GatedArgs &a, cudaStream_t stream) {
     p.dim = a.dim;
     p.splits = l.splits;
     p.act = a.act;
+    p.dg = {static_cast<uint16_t *>(dg), l.stride, a.wide};
+    p.du = {static_cast<uint16_t *>(du), l.stride, a.wide};
+    p.gx = {static_cast<uint16_t *>(a.grad_x), a.grad_x_stride, a.dim};
+    p.ggate = {static_cast<uint16_t *>(a.grad_gate), a.grad_gate_stride, a.dim};
+    p.gup = {static_cast<uint16_t *>(a.grad_up), a.grad_up_stride, a.dim};
+    p.sums = sums;
     p.grad_out = static_cast<const uint4 *>(a.grad_out);
     p.grad_stride = a.grad_out_stride / 8;
     p.tops = BF16 ? nullptr : tops;

@@ -298,12 +298,7 @@ def gated_linear_backward(x, gate, up, grad_out, activation="silu", grad_x=None,
     gus = dim if grad_up is None else _matrix(where, "grad_up", grad_up, dtype, (wide, dim))[2]
     status = _status(device)
     with _on(stream):
-        if grad_x is None:
-            grad_x = torch.empty((tokens, dim), dtype=dtype, device=device)
-        if grad_gate is None:
-            grad_gate = torch.empty((wide, dim), dtype=dtype, device=device)
-        if grad_up is None:
-            grad_up = torch.empty((wide, dim), dtype=dtype, device=device)
+        grad_x, grad_gate, grad_up = (_like(t) if g is None else g for g, t in ((grad_x, x), (grad_gate, gate), (grad_up, up)))
         need = A.zero_gated_workspace(tokens, wide, dim)[1]
         space = _scratch(need, device)
         _call("zero_gated_backward", x.data_ptr(), xs, gate.data_ptr(), gs, up.data_ptr(), us, act, grad_out.data_ptr(), gos,
