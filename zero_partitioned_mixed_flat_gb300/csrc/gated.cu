@@ -38,16 +38,32 @@ struct GatedLayout {
     int64_t slope_gate, slope_up, sums, bytes;  // byte offsets
 };
 
+// What a tile costs, in blocks of K of 256 columns; starting and storing it take about kTileCost.
+// Fewer columns take (columns + 128) / 384 of a block, as measured (see step_of).
+double tile_cost(double blocks, int64_t columns) { return blocks * (double)(std::min<int64_t>(columns, kTileN) + 128) / 384 + kTileCost; }
+
+// In how many partial sums grad_x comes: it has few tiles and long sums.  As many as leave no
+// part longer than a pair's share of all three gradients (at most 16, 8 blocks of K each); or
+// fewer, so that every tile has a pair of its own, where the longest then ends before a
+// pair that has one of each kind would.
+int splits_of(int64_t tokens, int64_t wide, int dim) {
+    const int64_t dim_tiles = up(dim, kTileN) / kTileN, row_tiles = up(std::max<int64_t>(tokens, 1), kTileM) / kTileM;
+    const int64_t long_sum = 2 * (up(wide, kTileK) / kTileK), short_sum = up(tokens, kTileK) / kTileK;
+    const int64_t n_x = row_tiles * dim_tiles, n_weight = 2 * (up(wide, kTileM) / kTileM) * dim_tiles;
+    const int64_t share = (n_x * long_sum + n_weight * short_sum) / kPairs;
+    int splits = 1;
+    while (splits < 16 && long_sum / splits > share && long_sum / (splits + 1) >= 8) ++splits;
+    const int64_t alone = (kPairs - n_weight) / n_x;
+    if (alone >= 1 && alone < splits &&
+        tile_cost((double)long_sum / alone, kTileN) < tile_cost((double)long_sum / splits, kTileN) + tile_cost((double)short_sum, kTileN))
+        splits = (int)alone;  // 1023 x 768 x 2048: two parts and 72 tiles, and not four and 96
+    return splits;
+}
+
 GatedLayout gated_layout(int64_t tokens, int64_t wide, int dim) {
     GatedLayout l;
     l.rows = up(std::max<int64_t>(tokens, 1), kTileM);
-    // grad_x has few tiles and long sums: cut its sums until no part is longer than a
-    // pair's share of all three gradients (at most 16 ways, 8 blocks of K each)
-    const int64_t dim_tiles = up(dim, kTileN) / kTileN, row_tiles = l.rows / kTileM;
-    const int64_t long_sum = 2 * (up(wide, kTileK) / kTileK), short_sum = up(tokens, kTileK) / kTileK;
-    const int64_t share = (row_tiles * dim_tiles * long_sum + 2 * (up(wide, kTileM) / kTileM) * dim_tiles * short_sum) / kPairs;
-    l.splits = 1;
-    while (l.splits < 16 && long_sum / l.splits > share && long_sum / (l.splits + 1) >= 8) ++l.splits;
+    l.splits = splits_of(tokens, wide, dim);
     int64_t at = up(kTopBlocks * 4, 1024);
     auto take = [&](int64_t bytes) {
         const int64_t here = at;
@@ -211,6 +227,7 @@ struct GatedParams {
     long long tokens, rows;
     int wide, dim, splits;
     int step;  // columns of a tile of both projections
+    int catch_up, start;  // see GatedWork
     int act;
     Rows out;                // forward
     Rows dg, du;             // slopes
@@ -225,14 +242,17 @@ struct GatedParams {
 
 // The work of one launch, and which of it each pair does, in order: every pair-th tile,
 // gradients first the tiles of grad_x, few and long; the pairs that get one fewer of
-// them then take `catch_up` tiles of the matrices' gradients each, about as long
-// together as one of the others; the rest of those goes round all pairs.
+// them then take `catch_up` tiles of the matrices' gradients each; the rest of those goes round
+// all pairs from `start` on.  Of either kind the tiles of 256 columns come first and those of
+// the last, fewer columns after them, as what is left over is best made of short ones.
+// plan_gradients chooses catch_up and start.
 template <int MODE>
 struct GatedWork {
-    Tiles gates, x, weight;
-    int step;
-    int pair, pairs, n_x, n_weight, weight_m;
-    int fuller, catch_up, mine;
+    Tiles whole, edge;           // both projections (whole alone); grad_x
+    Tiles weight, weight_edge;   // gradients of the matrices, gate's rows before up's
+    int step, edge_column;
+    int pair, pairs, n_whole, n_weight, n_weights, weight_m;
+    int fuller, catch_up, from, mine;
 
     __device__ __forceinline__ explicit GatedWork(const GatedParams &p) {
         const int row_tiles = (int)((p.tokens + kTileM - 1) / kTileM);
@@ -241,19 +261,23 @@ struct GatedWork {
         step = p.step;
         if constexpr (MODE != kGradients) {
             const int wide_tiles = (2 * p.wide + p.step - 1) / p.step;
-            gates.set(row_tiles, wide_tiles, 2 * p.wide, (p.dim + kTileK - 1) / kTileK, 1);
+            whole.set(row_tiles, wide_tiles, 2 * p.wide, (p.dim + kTileK - 1) / kTileK, 1);
         } else {
-            const int dim_tiles = (p.dim + kTileN - 1) / kTileN;
+            const int columns = p.dim / kTileN, last = p.dim % kTileN, some = last ? 1 : 0;
+            const int x_blocks = 2 * ((p.wide + kTileK - 1) / kTileK), weight_blocks = (int)((p.tokens + kTileK - 1) / kTileK);
             weight_m = (p.wide + kTileM - 1) / kTileM;
-            x.set(row_tiles, dim_tiles, p.dim, 2 * ((p.wide + kTileK - 1) / kTileK), p.splits);
-            weight.set(2 * weight_m, dim_tiles, p.dim, (int)((p.tokens + kTileK - 1) / kTileK), 1);
-            n_x = x.size();
+            edge_column = columns * kTileN;
+            whole.set(row_tiles, columns, edge_column, x_blocks, p.splits);
+            edge.set(row_tiles, some, last, x_blocks, p.splits);
+            weight.set(2 * weight_m, columns, edge_column, weight_blocks, 1);
+            weight_edge.set(2 * weight_m, some, last, weight_blocks, 1);
+            n_whole = whole.size();
             n_weight = weight.size();
+            n_weights = n_weight + weight_edge.size();
+            const int n_x = n_whole + edge.size();
             fuller = n_x % pairs;
-            const int long_tile = x.k_blocks / x.splits + kTileCost, short_tile = weight.k_blocks + kTileCost;
-            catch_up = fuller ? (long_tile + short_tile / 2) / short_tile : 0;
-            const int most = fuller ? n_weight / (pairs - fuller) : 0;
-            if (catch_up > most) catch_up = most;
+            catch_up = p.catch_up;
+            from = pair >= p.start ? pair - p.start : pair - p.start + pairs;
             mine = n_x > pair ? (n_x - pair + pairs - 1) / pairs : 0;
         }
     }
@@ -261,32 +285,37 @@ struct GatedWork {
     __device__ __forceinline__ bool at(int j, Tile &t) const {
         if constexpr (MODE != kGradients) {
             const int i = pair + j * pairs;
-            if (i >= gates.size()) return false;
-            t = gates.at(i, kGates);
+            if (i >= whole.size()) return false;
+            t = whole.at(i, kGates);
             t.n0 = t.n * step;
-            const int left = (gates.columns - t.n0 + 31) / 32 * 32;
+            const int left = (whole.columns - t.n0 + 31) / 32 * 32;
             t.width = left < step ? left : step;
             return true;
         }
+        bool last;
         if (j < mine) {
-            t = x.at(pair + j * pairs, kGradX);
-            return true;
-        }
-        j -= mine;
-        const int others = pairs - fuller;
-        int i;
-        if (catch_up && pair >= fuller && j < catch_up) {
-            i = pair - fuller + j * others;
+            const int i = pair + j * pairs;
+            last = i >= n_whole;
+            t = last ? edge.at(i - n_whole, kGradX) : whole.at(i, kGradX);
         } else {
-            if (catch_up && pair >= fuller) j -= catch_up;
-            i = catch_up * others + pair + j * pairs;
+            j -= mine;
+            const int others = pairs - fuller;
+            int i;
+            if (catch_up && pair >= fuller && j < catch_up) {
+                i = pair - fuller + j * others;
+            } else {
+                if (catch_up && pair >= fuller) j -= catch_up;
+                i = catch_up * others + from + j * pairs;
+            }
+            if (i >= n_weights) return false;
+            last = i >= n_weight;
+            t = last ? weight_edge.at(i - n_weight, kGradGate) : weight.at(i, kGradGate);
+            if (t.m0 >= weight_m * kTileM) {
+                t.m0 -= weight_m * kTileM;
+                t.kind = kGradUp;
+            }
         }
-        if (i >= n_weight) return false;
-        t = weight.at(i, kGradGate);
-        if (t.m0 >= weight_m * kTileM) {
-            t.m0 -= weight_m * kTileM;
-            t.kind = kGradUp;
-        }
+        if (last) t.n0 = edge_column;
         return true;
     }
 };
@@ -357,7 +386,10 @@ gated_products(const __grid_constant__ GatedParams p) {
             ask_for(&p.du_mn);
         }
     }
-    pdl_enter();
+    // fp16 slopes follow gated_top, whose result only the results' warps read.  The others need
+    // not wait for it: every block of it has waited for all that came before, x and the
+    // matrices among it, or this kernel would not have started.
+    if (MODE != kSlopes || BF16 || warp >= 2) pdl_enter();
 
     volatile int *dead = &sh.dead;
     const long long limit = p.wait_cycles;
@@ -945,6 +977,55 @@ int pairs_at_once() {
     });
 }
 
+// GatedWork's catch_up and start: of a few near what evens out the pairs' shares, those with
+// which the last pair ends first.  (Without, and with the edge tiles among the others,
+// 2048 x 1600 x 4264 took 246 blocks of K and not 210, 5000 x 776 x 3000 279 and not 213.)
+void plan_gradients(GatedParams &p, int pairs) {
+    constexpr int kMost = 256;
+    p.catch_up = p.start = 0;
+    if (pairs > kMost) return;
+    const int64_t rows = up(p.tokens, kTileM) / kTileM, columns = p.dim / kTileN, last = p.dim % kTileN;
+    const double blocks = 2.0 * (double)(up(p.wide, kTileK) / kTileK) / p.splits;
+    const int64_t short_blocks = up(p.tokens, kTileK) / kTileK, weight_m = 2 * (up(p.wide, kTileM) / kTileM);
+    const int64_t n_whole = rows * columns * p.splits, n_x = n_whole + (last ? rows * p.splits : 0);
+    const int64_t n_weight = weight_m * columns, n_weights = n_weight + (last ? weight_m : 0);
+    const double x = tile_cost(blocks, kTileN), x_last = tile_cost(blocks, last);
+    const double w = tile_cost((double)short_blocks, kTileN), w_last = tile_cost((double)short_blocks, last);
+    // tiles i, i + by, ... below n
+    const auto count = [](int64_t n, int64_t i, int64_t by) { return n > i ? (n - i + by - 1) / by : 0; };
+    const int64_t fuller = n_x % pairs, others = pairs - fuller;
+    double first[kMost];
+    for (int q = 0; q < pairs; ++q) {
+        const int64_t whole = count(n_whole, q, pairs);
+        first[q] = (double)whole * x + (double)(count(n_x, q, pairs) - whole) * x_last;
+    }
+    const int64_t even = fuller ? (int64_t)(x / w + 0.5) : 0;
+    const int64_t starts[3] = {0, fuller, n_whole % pairs};
+    double best = -1.0;
+    for (int64_t c = std::max<int64_t>(0, even - 2); c <= even + 1; ++c) {
+        if (c > 0 && (fuller == 0 || c * others > n_weights)) break;
+        const int64_t taken = c * others, whole_left = std::max<int64_t>(0, n_weight - taken), left = n_weights - taken;
+        for (const int64_t start : starts) {
+            double end = 0.0;
+            for (int q = 0; q < pairs; ++q) {
+                double mine = first[q];
+                if (q >= fuller && c > 0) {
+                    const int64_t whole = std::min(c, count(n_weight, q - fuller, others));
+                    mine += (double)whole * w + (double)(c - whole) * w_last;
+                }
+                const int64_t i = q >= start ? q - start : q - start + pairs, whole = count(whole_left, i, pairs);
+                mine += (double)whole * w + (double)(count(left, i, pairs) - whole) * w_last;
+                end = std::max(end, mine);
+            }
+            if (best < 0.0 || end < best) {
+                best = end;
+                p.catch_up = (int)c;
+                p.start = (int)start;
+            }
+        }
+    }
+}
+
 // Columns of a tile of both projections: those for which the pairs' rounds take the least time.
 // A block of K takes (step + 128) / 384 of what it takes with 256 columns, as measured: 19
 // rounds of 256 and 24 of 192 (4096 x 4096 x 10928) 400 and 432 us, 15 and 19 (8184 x 1600 x
@@ -1088,8 +1169,12 @@ cudaError_t backward_impl(const GatedArgs &a, cudaStream_t stream) {
         e = launch_narrow<BF16, kSlopes>(a, static_cast<uint16_t *>(dg), static_cast<uint16_t *>(du), p.tops, stream);
     else if (e == cudaSuccess)
         e = launch_products<BF16, kSlopes>(p, row_tiles * (up(2 * a.wide, p.step) / p.step), stream);
-    if (e == cudaSuccess)
-        e = launch_products<BF16, kGradients>(p, row_tiles * dim_tiles * l.splits + 2 * (up(a.wide, kTileM) / kTileM) * dim_tiles, stream);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = row_tiles * dim_tiles * l.splits + 2 * (up(a.wide, kTileM) / kTileM) * dim_tiles;
+    const int gradient_pairs = pairs_at_once<BF16, kGradients>();
+    if (gradient_pairs < 0) return (cudaError_t)-gradient_pairs;
+    plan_gradients(p, (int)std::min<int64_t>(gradient_pairs, tiles));
+    e = launch_products<BF16, kGradients>(p, tiles, stream);
     if (e == cudaSuccess && l.splits > 1)
         e = launch_pdl(gated_finish<BF16>, dim3((unsigned)std::min<int64_t>(a.tokens, 8 * sm_count())), dim3(kFinishThreads), 0, stream,
                        reinterpret_cast<const float4 *>(sums), (long long)a.tokens, (long long)l.rows, l.splits, a.dim / 8,
