@@ -240,6 +240,17 @@ __device__ __forceinline__ Piece piece_of(const AdamwParams<TABLE> &t, int chunk
     return q;
 }
 
+// b^n by squaring: b^n is off by at most about n 2^-53 of itself, which 1 - b^n in float does
+// not show.  (pow took 1.1 us more of a short list's 8.2.)
+__device__ __forceinline__ double power(double b, long long n) {
+    double r = 1.0;
+    for (; n > 0; n >>= 1) {
+        if (n & 1) r = __dmul_rn(r, b);
+        b = __dmul_rn(b, b);
+    }
+    return r;
+}
+
 // What one step needs of its number and the device's decisions.
 struct StepScalars {
     float factor, bc1, bc2;
@@ -424,12 +435,12 @@ adamw_step(const __grid_constant__ AdamwParams<TABLE> t) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long step = c.record[0] + 1;
     if (threadIdx.x == 0) {
-        shared.bc1 = (float)(1.0 - pow(c.b1, (double)step));
+        shared.bc1 = (float)(1.0 - power(c.b1, step));
         shared.factor = __fmul_rn(c.coef ? *c.coef : 1.0f, c.inv_scale);
         shared.skip = c.skip ? *c.skip : 0;
         shared.key = mix(mix(c.seed) + (uint32_t)step);
     }
-    if (threadIdx.x == 32) shared.bc2 = (float)(1.0 - pow(c.b2, (double)step));
+    if (threadIdx.x == 32) shared.bc2 = (float)(1.0 - power(c.b2, step));
     const int chunks = t.chunk0[t.n];
     constexpr int N = kDepth<BITS>;
     bool first = true;

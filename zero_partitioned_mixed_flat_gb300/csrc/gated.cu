@@ -169,6 +169,8 @@ __device__ __forceinline__ void store_sector(void *to, const uint32_t (&w)[8]) {
                  : "memory");
 }
 
+__device__ __forceinline__ void ask_page(const void *at) { asm volatile("prefetch.global.L2 [%0];" ::"l"(at)); }
+
 // A matrix of lp results.
 struct Rows {
     uint16_t *at;
@@ -386,6 +388,7 @@ gated_products(const __grid_constant__ GatedParams p) {
             ask_for(&p.du_mn);
         }
     }
+    const GatedWork<MODE> work(p);
     // fp16 slopes follow gated_top, whose result only the results' warps read.  The others need
     // not wait for it: every block of it has waited for all that came before, x and the
     // matrices among it, or this kernel would not have started.
@@ -393,7 +396,6 @@ gated_products(const __grid_constant__ GatedParams p) {
 
     volatile int *dead = &sh.dead;
     const long long limit = p.wait_cycles;
-    const GatedWork<MODE> work(p);
     Tile t;
 
     if (warp == 0) {
@@ -525,6 +527,23 @@ gated_products(const __grid_constant__ GatedParams p) {
                 }
             };
             if constexpr (MODE == kSlopes) ask(group * 64);
+            if (j == 0) {  // the first results' pages (1023 x 768 x 2048 forward 9.15 -> 8.96 us)
+                if constexpr (MODE != kGradients) {
+                    const int f = t.n0 / 2 + group * 64;
+                    if (row < p.tokens && f < p.wide) {
+                        ask_page((MODE == kForward ? p.out : p.dg).at + row * (MODE == kForward ? p.out : p.dg).stride + f);
+                        if (MODE == kSlopes) ask_page(p.du.at + row * p.du.stride + f);
+                    }
+                } else {
+                    const Rows &to = t.kind == kGradX ? p.gx : t.kind == kGradGate ? p.ggate : p.gup;
+                    const int col = t.n0 + group * kResultColumns;
+                    if (t.kind == kGradX && p.splits > 1) {
+                        if (col < p.dim) ask_page(p.sums + (t.split * p.rows + row) * p.dim + col);
+                    } else if (row < (t.kind == kGradX ? p.tokens : (long long)p.wide) && col < p.dim) {
+                        ask_page(to.at + row * to.stride + col);
+                    }
+                }
+            }
             const bool got = wait_for(&sh.acc_full[buf], acc_phase, dead, limit, p.status);
             if (!__all_sync(0xffffffffu, got)) break;
             tc_fence_after();
