@@ -683,8 +683,9 @@ zero_status zero_clip_gradients(int32_t n_tensors, const void *const *grads, con
  *    ZERO_QUANT_BLOCK elements.  m[i] is an E4M3 code, m its value times the scale, which is the
  *    block's largest |m| / 448.  v[i] is an unsigned code, the bits 5 to 12 of a binary16
  *    number, whose value times the scale is the root of v; the scale is the block's largest root /
- *    (1.96875 / 256).  The step itself uses the new m and root before they are rounded.  Each is
- *    then rounded to one of its two neighbours at random, in proportion: by
+ *    (1.96875 / 256).  The step itself uses the new m and root before they are rounded, which
+ *    are those of ZERO_MOMENTS_FP32 for the old ones' values (root: the square root, rounded
+ *    to float).  Each is then divided by its scale (times the scale's rounded reciprocal) and rounded to one of its two neighbours at random, in proportion: by
  *    h(i) = mix((i mod 2^32) ^ mix(mix(mix(seed) + t) + i / 2^32)), where i is the element's
  *    place in m and mix takes x to x ^ x >> 16, that times 0x9E3779B1, then x ^ x >> 15, that
  *    times 0xB504F333, then x ^ x >> 16 (all modulo 2^32): up where the fraction that is cut
