@@ -279,6 +279,38 @@ def test_moments_of_every_code():
     assert got[0].dtype == BF and got[0].numel() == 384
 
 
+def codes_of(x, top, bits, mantissa, low, most):
+    """Codes and scales of float x >= 0 by torch's float operations, in the order that the definition gives."""
+    rows = x.view(-1, BLOCK)
+    scale = rows.amax(1, keepdim=True) * (1.0 / top)
+    y = torch.where(scale > 0, rows * (1.0 / scale), 0.0).flatten()
+    drop = 23 - mantissa
+    z = y * 2.0 ** (-126 - low)       # float's subnormal numbers where the code has its
+    code = (z.view(torch.int32) + (bits.int() << drop - 16) + (1 << drop - 17)) >> drop
+    return code.clamp(max=most), scale.flatten()
+
+
+@pytest.mark.parametrize("grad", [BF, F32])
+def test_codes_to_the_bit(grad):
+    """The definition's operations, each rounded on its own, give the kernel's codes and scales without an exception."""
+    n = 1 << 21
+    c = Case([n], 8, grad)
+    coef = torch.tensor([0.37], device="cuda")
+    for step in range(1, 5):
+        c.new_grads()
+        m0, r0, _, _ = (x.float() for x in values(c.state))
+        f = c.grads[0].float() * (coef * torch.tensor(1 / 3.0, device="cuda"))
+        m = m0 * 0.9 + f * (1 - 0.9)
+        r = ((r0 * r0) * 0.999 + (f * f) * (1 - 0.999)).sqrt()
+        c.step(check=False, seed=7, coef=coef, loss_scale=3.0)
+        bits_m, bits_r = random16(0, n, step, 7)
+        code_m, scale_m = codes_of(m.abs(), 448.0, bits_m, 3, -6, 126)
+        code_r, scale_r = codes_of(r, 1.96875 / 256, bits_r, 5, -14, 255)
+        _, _, got_m, got_r = values(c.state)
+        assert torch.equal(c.state.m_scales, scale_m) and torch.equal(c.state.v_scales, scale_r)
+        assert torch.equal(got_m, code_m.long()) and torch.equal(got_r, torch.where(r > 0, code_r.clamp(min=1), code_r).long())
+
+
 def test_rounding_is_unbiased_and_depends_on_seed_step_and_place():
     """Means of codes over many elements of one value, to within five standard deviations."""
     n = 1 << 20

@@ -35,15 +35,15 @@ constexpr int kBlock = ZERO_QUANT_BLOCK;  // a warp's 32 lanes x 4
 // Blocks of 128 that a warp has in flight, 16 or 12 elements a lane, in one block of 16 warps on an
 // SM.  More warps with less in flight each are slower: 117M elements with 32-bit moments 525 us
 // so, 541 and 617 us with two and three blocks of 256 that take 2 at a time, 982 us with
-// eight that take 1; 124M with 8-bit moments and their values 451 us, 465 with two
-// blocks of 256, 481 and 532 where they take 3 and 2 at a time.
+// eight that take 1; 124M with 8-bit moments and their values 479 us, 499 with two
+// blocks of 256, 528 with 3 at a time, 531 with 24 warps that take 2.
 template <int BITS>
 constexpr int kDepth = BITS == 8 ? 4 : 3;
 template <int BITS>
 constexpr int kChunkBlocks = kWarps * kDepth<BITS>;  // blocks of 128 of a chunk
 // Whether a chunk's lines are asked for while the one before is at work: 8-bit moments, whose
-// arithmetic takes about as long as their copies (124M elements 520 us without it; with
-// 32-bit moments 4 % slower with it).
+// arithmetic takes about as long as their copies (124M elements 551 us without it and 512
+// with it; with 32-bit moments 4 % slower with it).
 template <int BITS>
 constexpr bool kAhead = BITS == 8;
 // Tensors of one launch: the table is a kernel parameter, 44 bytes a tensor.
@@ -110,16 +110,37 @@ __device__ __forceinline__ uint32_t pack_bytes(uint32_t a, uint32_t b, uint32_t 
     return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
+// two floats at once, each operation rounded to nearest
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+// (add.rn.f32x2 of two products came out as if they were fused into it)
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y)); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;"
+        : "=l"(reinterpret_cast<uint64_t &>(r))
+        : "l"(reinterpret_cast<const uint64_t &>(a)), "l"(reinterpret_cast<const uint64_t &>(b)));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t &>(r))
+        : "l"(reinterpret_cast<const uint64_t &>(a)), "l"(reinterpret_cast<const uint64_t &>(b)),
+          "l"(reinterpret_cast<const uint64_t &>(c)));
+    return r;
+}
+
 // The square root and the reciprocal of normal numbers, rounded to nearest: the hardware's
 // approximation and one step with an exact remainder (P. Markstein, "Computation of elementary
-// functions on the IBM RISC System/6000 processor", IBM J. Res. Dev. 34(1), 1990); tested
-// against the IEEE operations.  (Those intrinsics, with their branches for all other numbers,
-// made 124M elements 512 us and not 470.)  The root of 0 is 0; below 2^-126 it is only near.
-__device__ __forceinline__ float root_of(float x) {
-    float y;
-    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaxf(x, 0x1p-126f)));
-    const float s = __fmul_rn(x, y);
-    return __fmaf_rn(__fmaf_rn(-s, s, x), 0.5f * y, s);
+// functions on the IBM RISC System/6000 processor", IBM J. Res. Dev. 34(1), 1990); equal to the
+// IEEE operations for every mantissa.  (Those intrinsics, with their branches for all other
+// numbers, made 124M elements 512 us and not 479; two numbers an operation 456.)  The root of 0 is 0; below 2^-126 it is only near.
+__device__ __forceinline__ float2 roots_of(float2 x) {
+    float2 y;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(fmaxf(x.x, 0x1p-126f)));
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(fmaxf(x.y, 0x1p-126f)));
+    const float2 s = mul2(x, y), minus = mul2(x, make_float2(-y.x, -y.y));
+    return fma2(fma2(minus, s, x), mul2(y, both(0.5f)), s);
 }
 __device__ __forceinline__ float reciprocal_of(float x) {
     const float r = rcp_approx(x);
@@ -377,16 +398,26 @@ struct Span {
                 float m[4], r[4], top_m = 0.0f, top_r = 0.0f;
                 m_values(mc[i], m);
                 root_values(vc[i], r);
+                const float2 old_m = both(ms[i]), old_r = both(vs[i]);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
+                for (int k = 0; k < 4; k += 2) {
                     // The new moments as with 32 bits, every operation rounded on its own: codes beside a
                     // border are anybody's guess otherwise.  The update need not be.
-                    const float f = __fmul_rn(grad[k], s.factor), root = __fmul_rn(r[k], vs[i]);
-                    m[k] = __fadd_rn(__fmul_rn(c.beta1, __fmul_rn(m[k], ms[i])), __fmul_rn(c.omb1, f));
-                    r[k] = root_of(__fadd_rn(__fmul_rn(c.beta2, __fmul_rn(root, root)), __fmul_rn(c.omb2, __fmul_rn(f, f))));
-                    w[k] = __fmaf_rn(w[k], c.decay, -(lr1 * m[k] * rcp_approx(__fmaf_rn(r[k], rs2, c.eps))));
-                    top_m = larger(top_m, m[k]);
-                    top_r = larger(top_r, r[k]);
+                    const float2 f = mul2(make_float2(grad[k], grad[k + 1]), both(s.factor));
+                    const float2 root = mul2(make_float2(r[k], r[k + 1]), old_r);
+                    const float2 m2 = add2(mul2(both(c.beta1), mul2(make_float2(m[k], m[k + 1]), old_m)), mul2(both(c.omb1), f));
+                    const float2 r2 = roots_of(add2(mul2(both(c.beta2), mul2(root, root)), mul2(both(c.omb2), mul2(f, f))));
+                    const float2 denominator = fma2(r2, both(rs2), both(c.eps));
+                    const float2 part = mul2(mul2(both(-lr1), m2), make_float2(rcp_approx(denominator.x), rcp_approx(denominator.y)));
+                    const float2 p2 = fma2(make_float2(w[k], w[k + 1]), both(c.decay), part);
+                    w[k] = p2.x;
+                    w[k + 1] = p2.y;
+                    m[k] = m2.x;
+                    m[k + 1] = m2.y;
+                    r[k] = r2.x;
+                    r[k + 1] = r2.y;
+                    top_m = larger(larger(top_m, m2.x), m2.y);
+                    top_r = larger(larger(top_r, r2.x), r2.y);
                 }
                 put(i, w);
                 const uint32_t bits_m = __reduce_max_sync(0xffffffffu, __float_as_uint(top_m));
