@@ -75,3 +75,21 @@ def test_layout():
         Z.zero_adamw_layout([5, -1])
     with pytest.raises(Z.ZeroError):
         Z.zero_adamw_layout([1 << 40] * 17)
+
+
+def test_the_tensor_call_refuses_what_is_no_cuda_tensor():
+    """Before any CUDA call: the module that takes torch tensors."""
+    import torch
+    call = Z._abi.tensors().adamw_step
+    p = torch.zeros(5)
+    numbers = (1e-3, 0.9, 0.999, 1e-8, 0.0, 1.0, None, None)
+    for params in ([p], [3], [p.half()], [None], []):
+        with pytest.raises(Z.ZeroError) as e:
+            call(params, [], None, (None,) * 5, *numbers, 0, 0, 0)
+        assert e.value.code == INVALID
+    with pytest.raises(TypeError):
+        call(p)
+    with pytest.raises(TypeError):
+        call(5, [p], None, (None,) * 5, *numbers, 0, 0, 0)
+    with pytest.raises(Z.ZeroError):
+        call([p], [p], None, (None,) * 5, *numbers, 1 << 40, 0, 0)

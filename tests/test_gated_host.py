@@ -73,3 +73,18 @@ def test_workspace_sizes():
             assert forward >= 0 and backward >= 2 * t * wide * 2
     # both slopes, and at most 16 float sums of the tiles' rows
     assert Z.zero_gated_workspace(4096, 10928, 4096)[1] <= 2 * 4096 * 10928 * 2 + 4 * 4096 * 4096 * 4 + 8192
+
+
+def test_the_tensor_call_refuses_what_is_no_cuda_matrix():
+    """Before any CUDA call: the module that takes torch tensors."""
+    import torch
+    call = Z._abi.tensors().gated_forward
+    x = torch.zeros(2, 8, dtype=torch.bfloat16)
+    for bad in (x, x.float(), x[0], None, 3, x.to_sparse()):
+        with pytest.raises(Z.ZeroError) as e:
+            call(bad, x, x, 0, 0, P, 0)
+        assert e.value.code == INVALID
+    with pytest.raises(Z.ZeroError, match="requires grad"):
+        call(torch.zeros(2, 8, requires_grad=True), x, x, 0, 0, P, 0)
+    with pytest.raises(TypeError):
+        call(x, x)

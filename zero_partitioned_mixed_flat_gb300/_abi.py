@@ -117,6 +117,29 @@ def load():
     return _LIB
 
 
+_TENSORS = None
+
+
+def tensors():
+    """The module of calls on torch tensors (_lib/_tensors.so, built with libzero).  Raises if it is missing."""
+    global _TENSORS
+    if _TENSORS is None:
+        import importlib.util
+
+        import torch  # noqa: F401  (the module's own libraries)
+        load()
+        path = os.path.join(os.path.dirname(LIB_PATH), "_tensors.so")
+        if not os.path.exists(path):
+            raise ImportError("_tensors.so is not built (%s): run "
+                              "`python -m zero_partitioned_mixed_flat_gb300.build`" % path)
+        spec = importlib.util.spec_from_file_location("_tensors", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.bind(ZeroError)
+        _TENSORS = module
+    return _TENSORS
+
+
 def _check(code: int, where: str):
     if code != ZERO_OK:
         msg = load().zero_last_error()

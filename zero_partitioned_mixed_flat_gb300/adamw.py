@@ -13,17 +13,14 @@ loaded like any other; steps of one state follow each other on a stream.  The ca
 captured into a graph, whose replays are the following steps.  Wrong types, lengths or
 devices raise ZeroError (ZERO_EINVAL) before any device work.
 """
-from operator import attrgetter
 from typing import NamedTuple, Optional
 
-import numpy as np
 import torch
 
 from . import _abi as A
-from .head import _CLIP, _LP, _call, _gather, _on, _refuse
+from .head import _CLIP, _call, _on, _refuse
 
 _T = torch.Tensor
-_DTYPE = attrgetter("dtype")
 _BLOCK = A.ZERO_QUANT_BLOCK
 
 
@@ -59,34 +56,12 @@ def adamw_state(params, bits=32, stream=None):
                           zeros(total // _BLOCK, torch.float32), record)
 
 
-def _one(where, name, t, dtype, device):
-    """The address of one element, or None."""
-    if t is None:
-        return None
-    if t.dtype != dtype or t.numel() != 1 or t.get_device() != device:
-        _refuse(where, "%s must be one %s on the current CUDA device" % (name, dtype))
-    return t.data_ptr()
-
-
 def _vector_at(where, name, t, dtype, n, device):
     """The address of one of the state's tensors."""
     if (not isinstance(t, _T) or t.dtype != dtype or t.ndim != 1 or t.numel() != n or t.get_device() != device
             or not t.is_contiguous()):
         _refuse(where, "the state's %s must be %d contiguous %s on the current CUDA device" % (name, n, dtype))
     return t.data_ptr()
-
-
-def _moments(where, state, total, device):
-    """(format, addresses of m, v, their scales and the record) of a state, looked over."""
-    m, v, m_scales, v_scales, record = state
-    at_record = _vector_at(where, "record", record, torch.int64, 2, device)
-    if m.dtype != torch.int8:
-        return (A.ZERO_MOMENTS_FP32, _vector_at(where, "m", m, torch.float32, total, device),
-                _vector_at(where, "v", v, torch.float32, total, device), None, None, at_record)
-    return (A.ZERO_MOMENTS_8BIT, _vector_at(where, "m", m, torch.int8, total, device),
-            _vector_at(where, "v", v, torch.uint8, total, device),
-            _vector_at(where, "m_scales", m_scales, torch.float32, total // _BLOCK, device),
-            _vector_at(where, "v_scales", v_scales, torch.float32, total // _BLOCK, device), at_record)
 
 
 def adamw_step(params, grads, state, lr, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.0, copies=None, loss_scale=1.0,
@@ -97,38 +72,8 @@ def adamw_step(params, grads, state, lr, beta1=0.9, beta2=0.999, eps=1e-8, weigh
     t counts the state's steps, on the device.  coef (one float32) and skip (one int32: not 0 leaves
     everything as it was, the count too) are device tensors such as gradient_norm gives; None: 1 and
     never.  seed: of the random rounding of 8-bit moments, which also depends on t and the element."""
-    where = "adamw_step"
-    if not params:
-        _refuse(where, "no parameters")
-    if len(grads) != len(params) or (copies is not None and len(copies) != len(params)):
-        _refuse(where, "one gradient, and one copy if any, per parameter")
-    device = torch._C._cuda_getDevice()
-    lens, at_params = _gather(where, "params", params, torch.float32, device)
-    if len(set(at_params)) < len(lens) and len({p for p, n in zip(at_params, lens) if n}) < sum(map(bool, lens)):
-        _refuse(where, "a parameter is listed twice")
-    if grads[0].dtype not in _CLIP:
-        _refuse(where, "grads must be float16, bfloat16 or float32")
-    grad_lens, at_grads = _gather(where, "grads", grads, grads[0].dtype, device)
-    at_copies, copy_type = None, A.ZERO_BF16
-    if copies is not None:
-        if copies[0].dtype not in _LP:
-            _refuse(where, "copies must be float16 or bfloat16")
-        copy_type = _LP[copies[0].dtype]
-        copy_lens, at_copies = _gather(where, "copies", copies, copies[0].dtype, device)
-    if grad_lens != lens or (at_copies is not None and copy_lens != lens):
-        _refuse(where, "a gradient or copy has another length than its parameter")
-    if len(lens) <= 64:   # a short list costs less than numpy's calls
-        blocks = sum([(n + _BLOCK - 1) // _BLOCK for n in lens])
-    else:
-        blocks = int(((np.frombuffer(lens, np.int64) + (_BLOCK - 1)) // _BLOCK).sum())
-    moments = _moments(where, state, blocks * _BLOCK, device)
-    at_coef = _one(where, "coef", coef, torch.float32, device)
-    at_skip = _one(where, "skip", skip, torch.int32, device)
-    if not -2 ** 31 <= seed < 2 ** 31:
-        _refuse(where, "seed outside 32 bits")
-    _call("zero_adamw_step", len(lens), at_params.buffer_info()[0], at_grads.buffer_info()[0], _CLIP[grads[0].dtype],
-          at_copies and at_copies.buffer_info()[0], copy_type, lens.buffer_info()[0], *moments, lr, beta1, beta2, eps,
-          weight_decay, loss_scale, at_coef, at_skip, seed, A._stream(stream))
+    A.tensors().adamw_step(params, grads, copies, state, lr, beta1, beta2, eps, weight_decay, loss_scale, coef, skip, seed,
+                           torch._C._cuda_getDevice(), A._stream(stream))
 
 
 def adamw_moments(state, dtype=torch.float32, stream=None):
@@ -137,13 +82,17 @@ def adamw_moments(state, dtype=torch.float32, stream=None):
     where = "adamw_moments"
     if dtype not in _CLIP:
         _refuse(where, "dtype must be float16, bfloat16 or float32")
-    m, v = state[:2]
-    if m.numel() % _BLOCK:
+    m, v, m_scales, v_scales, _ = state
+    total, device = m.numel(), torch._C._cuda_getDevice()
+    if total % _BLOCK:
         _refuse(where, "a state's length is a multiple of %d" % _BLOCK)
-    fmt, *at, _ = _moments(where, state, m.numel(), torch._C._cuda_getDevice())
+    eight = m.dtype == torch.int8
+    at = [_vector_at(where, "m", m, torch.int8 if eight else torch.float32, total, device),
+          _vector_at(where, "v", v, torch.uint8 if eight else torch.float32, total, device)]
     with _on(stream):
-        if fmt == A.ZERO_MOMENTS_FP32:
+        if not eight:
             return m.to(dtype), v.to(dtype)
+        at += [_vector_at(where, n, t, torch.float32, total // _BLOCK, device) for n, t in (("m_scales", m_scales), ("v_scales", v_scales))]
         m_out, v_out = (torch.empty(m.shape, dtype=dtype, device=m.device) for _ in range(2))
-        _call("zero_adamw_values", *at, m.numel(), _CLIP[dtype], m_out.data_ptr(), v_out.data_ptr(), A._stream(stream))
+        _call("zero_adamw_values", *at, total, _CLIP[dtype], m_out.data_ptr(), v_out.data_ptr(), A._stream(stream))
     return m_out, v_out

@@ -260,16 +260,14 @@ def linear_loss_backward(hidden, weight, targets, lse, grad_loss, ignore=-100, g
 
 # ---- gated projections --------------------------------------------------------------
 
-def _gated_inputs(where, x, gate, up, activation):
+def _gated(where, activation):
+    """(activation's number, current device, status address)"""
     act = _ACTS.get(activation)
     if act is None:
         _refuse(where, "activation is %r, expected one of %s" % (activation, ", ".join(_ACTS)))
-    tokens, dim, xs = _matrix(where, "x", x)
-    dtype = x.dtype
-    wide, across, gs = _matrix(where, "gate", gate, dtype)
-    if across != dim:
-        _refuse(where, "gate has rows of %d, x of %d" % (across, dim))
-    return tokens, dim, wide, xs, gs, _matrix(where, "up", up, dtype, (wide, dim))[2], act, dtype, x.device
+    device = torch._C._cuda_getDevice()
+    status = _STATUS.get(device)
+    return act, device, (_status(torch.device("cuda", device)) if status is None else status).data_ptr()
 
 
 def gated_linear(x, gate, up, activation="silu", stream=None):
@@ -277,34 +275,17 @@ def gated_linear(x, gate, up, activation="silu", stream=None):
     gated feed-forward block (gate, up: [wide, dim]; they may be halves of one matrix).
     activation: "silu", "gelu" or "gelu_tanh".  Neither projection is stored; the backward
     call takes x again.  check_losses also reports a wait that gave up here."""
-    tokens, dim, wide, xs, gs, us, act, dtype, device = _gated_inputs("gated_linear", x, gate, up, activation)
-    status = _status(device)
+    act, device, status = _gated("gated_linear", activation)
     with _on(stream):
-        out = torch.empty((tokens, wide), dtype=dtype, device=device)
-        # the forward call needs no workspace
-        _call("zero_gated_forward", x.data_ptr(), xs, gate.data_ptr(), gs, up.data_ptr(), us, act, tokens, wide, dim,
-              _LP[dtype], out.data_ptr(), wide, status.data_ptr(), None, 0, A._stream(stream))
-    return out
+        return A.tensors().gated_forward(x, gate, up, act, device, status, A._stream(stream))
 
 
 def gated_linear_backward(x, gate, up, grad_out, activation="silu", grad_x=None, grad_gate=None, grad_up=None, stream=None):
     """(grad_x, grad_gate, grad_up) of gated_linear for the gradient of its output,
     written into the given tensors if there are any (with rows like every matrix's)."""
-    where = "gated_linear_backward"
-    tokens, dim, wide, xs, gs, us, act, dtype, device = _gated_inputs(where, x, gate, up, activation)
-    gos = _matrix(where, "grad_out", grad_out, dtype, (tokens, wide))[2]
-    gxs = dim if grad_x is None else _matrix(where, "grad_x", grad_x, dtype, (tokens, dim))[2]
-    ggs = dim if grad_gate is None else _matrix(where, "grad_gate", grad_gate, dtype, (wide, dim))[2]
-    gus = dim if grad_up is None else _matrix(where, "grad_up", grad_up, dtype, (wide, dim))[2]
-    status = _status(device)
+    act, device, status = _gated("gated_linear_backward", activation)
     with _on(stream):
-        grad_x, grad_gate, grad_up = (_like(t) if g is None else g for g, t in ((grad_x, x), (grad_gate, gate), (grad_up, up)))
-        need = A.zero_gated_workspace(tokens, wide, dim)[1]
-        space = _scratch(need, device)
-        _call("zero_gated_backward", x.data_ptr(), xs, gate.data_ptr(), gs, up.data_ptr(), us, act, grad_out.data_ptr(), gos,
-              tokens, wide, dim, _LP[dtype], grad_x.data_ptr(), gxs, grad_gate.data_ptr(), ggs, grad_up.data_ptr(), gus,
-              status.data_ptr(), space.data_ptr(), need, A._stream(stream))
-    return grad_x, grad_gate, grad_up
+        return A.tensors().gated_backward(x, gate, up, act, device, status, A._stream(stream), grad_out, grad_x, grad_gate, grad_up)
 
 
 # ---- global norm, clipping, packing ----------------------------------------------
