@@ -86,8 +86,15 @@ __device__ __forceinline__ float rcp_approx(float x) {
     return r;
 }
 
+// Two elements at a time, which halves the instructions: the thread that feeds the tensor core
+// needs its turns too.
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 rcp2(float2 x) { return make_float2(rcp_approx(x.x), rcp_approx(x.y)); }
+__device__ __forceinline__ float2 exp2_2(float2 x) { return make_float2(exp2_approx(x.x), exp2_approx(x.y)); }
+__device__ __forceinline__ float2 one_minus(float2 x) { return fma2(x, both(-1.0f), both(1.0f)); }
+
 // 1 / (1 + exp(-x)); 0 and 1 far out
-__device__ __forceinline__ float sigmoid(float x) { return rcp_approx(1.0f + exp2_approx(-x * kLog2e)); }
+__device__ __forceinline__ float2 sigmoid(float2 x) { return rcp2(add2(exp2_2(mul2(x, both(-kLog2e))), both(1.0f))); }
 
 constexpr float kTanhScale = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kTanhCube = 0.044715f;
@@ -97,21 +104,20 @@ constexpr float kTanhCube = 0.044715f;
 // "Chebyshev approximation of (1 + 2x) exp(x^2) erfc x in 0 <= x < infinity", Math. Comp. 36,
 // 1981); the coefficients are a Chebyshev fit of degree 9 of half of it, 1.5e-7 off.  With the
 // exponential rounded as it is here q is off by at most 0.4 (g^2 / 2 + 16) 2^-22 of itself.
-// (erfcf took 120 cycles an element, which showed: 8184 x 1600 x 4264 forward 138 us.)
-__device__ __forceinline__ float normal_share(float g, float bell) {
-    const float x = fminf(fabsf(g) * 0.70710678118654752f, 16.0f);
-    const float t = (x - 2.5f) * rcp_approx(x + 2.5f);
-    float h = __fmaf_rn(2.022946865e-04f, t, 1.512481249e-04f);
-    h = __fmaf_rn(h, t, -2.088966779e-03f);
-    h = __fmaf_rn(h, t, 5.443191039e-04f);
-    h = __fmaf_rn(h, t, 1.633777283e-02f);
-    h = __fmaf_rn(h, t, -5.151086301e-02f);
-    h = __fmaf_rn(h, t, 7.882248610e-02f);
-    h = __fmaf_rn(h, t, -4.950888082e-02f);
-    h = __fmaf_rn(h, t, -6.117876619e-02f);
-    h = __fmaf_rn(h, t, 6.324190497e-01f);
-    const float q = bell * (h * rcp_approx(__fmaf_rn(2.0f, x, 1.0f)));
-    return g < 0.0f ? q : 1.0f - q;
+// bell: exp(-g^2 / 2).  (erfcf took 120 cycles an element.)
+__device__ __forceinline__ float2 normal_share(float2 g, float2 bell) {
+    constexpr float kFit[10] = {2.022946865e-04f, 1.512481249e-04f,  -2.088966779e-03f, 5.443191039e-04f,  1.633777283e-02f,
+                                -5.151086301e-02f, 7.882248610e-02f, -4.950888082e-02f, -6.117876619e-02f, 6.324190497e-01f};
+    const float2 y = mul2(g, both(0.70710678118654752f));
+    const float2 x = make_float2(fminf(fabsf(y.x), 16.0f), fminf(fabsf(y.y), 16.0f));
+    const float2 above = add2(x, both(2.5f)), twice = fma2(x, both(2.0f), both(1.0f));
+    const float2 r = rcp2(mul2(above, twice));  // at most 18.5 * 33
+    const float2 t = mul2(mul2(add2(x, both(-2.5f)), twice), r);
+    float2 h = both(kFit[0]);
+#pragma unroll
+    for (int i = 1; i < 10; ++i) h = fma2(h, t, both(kFit[i]));
+    const float2 q = mul2(bell, mul2(h, mul2(above, r))), rest = one_minus(q);
+    return make_float2(g.x < 0.0f ? q.x : rest.x, g.y < 0.0f ? q.y : rest.y);
 }
 
 // Each activation is g P(g), its derivative P + g P'.
@@ -119,18 +125,19 @@ __device__ __forceinline__ float normal_share(float g, float bell) {
 //   gelu       P = erfc(-g / sqrt(2)) / 2
 //   gelu_tanh  P = (1 + tanh(y)) / 2 = 1 / (1 + exp(-2 y)),  2 y = kTanhScale (g + kTanhCube g^3)
 template <int ACT>
-__device__ __forceinline__ float share_of(float g, float &derivative) {
+__device__ __forceinline__ float2 share_of(float2 g, float2 &derivative) {
+    const float2 square = mul2(g, g);
     if constexpr (ACT == ZERO_ACT_GELU) {
-        const float bell = exp2_approx(g * g * (-0.5f * kLog2e));
-        derivative = 0.3989422804014327f * bell;
+        const float2 bell = exp2_2(mul2(square, both(-0.5f * kLog2e)));
+        derivative = mul2(bell, both(0.3989422804014327f));
         return normal_share(g, bell);
     } else if constexpr (ACT == ZERO_ACT_SILU) {
-        const float p = sigmoid(g);
-        derivative = p * (1.0f - p);
+        const float2 p = sigmoid(g);
+        derivative = mul2(p, one_minus(p));
         return p;
     } else {
-        const float p = sigmoid(kTanhScale * __fmaf_rn(kTanhCube * g, g * g, g));
-        derivative = p * (1.0f - p) * (kTanhScale * __fmaf_rn(3.0f * kTanhCube * g, g, 1.0f));
+        const float2 p = sigmoid(mul2(fma2(mul2(g, both(kTanhCube)), square, g), both(kTanhScale)));
+        derivative = mul2(mul2(p, one_minus(p)), fma2(square, both(3.0f * kTanhCube * kTanhScale), both(kTanhScale)));
         return p;
     }
 }
@@ -138,26 +145,32 @@ __device__ __forceinline__ float share_of(float g, float &derivative) {
 // out of n columns, g and u in place
 template <int ACT, int N>
 __device__ __forceinline__ void outs_of(const float (&g)[N], float (&u)[N]) {
-    float unused;
 #pragma unroll
-    for (int i = 0; i < N; ++i) u[i] = g[i] * share_of<ACT>(g[i], unused) * u[i];
+    for (int i = 0; i < N; i += 2) {
+        const float2 a = make_float2(g[i], g[i + 1]);
+        float2 unused;
+        const float2 out = mul2(mul2(a, share_of<ACT>(a, unused)), make_float2(u[i], u[i + 1]));
+        u[i] = out.x;
+        u[i + 1] = out.y;
+    }
 }
 
 // dg and du of n columns, in g's and u's place
 template <int ACT, int N>
 __device__ __forceinline__ void slopes_of(const float (&go)[N], float (&g)[N], float (&u)[N]) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        float derivative;
-        const float p = share_of<ACT>(g[i], derivative);
-        const float slope = __fmaf_rn(g[i], derivative, p);
-        const float du = go[i] * (g[i] * p);
-        g[i] = go[i] * u[i] * slope;
-        u[i] = du;
+    for (int i = 0; i < N; i += 2) {
+        const float2 a = make_float2(g[i], g[i + 1]), grad = make_float2(go[i], go[i + 1]);
+        float2 derivative;
+        const float2 p = share_of<ACT>(a, derivative);
+        const float2 slope = fma2(a, derivative, p), du = mul2(grad, mul2(a, p));
+        const float2 dg = mul2(mul2(grad, make_float2(u[i], u[i + 1])), slope);
+        g[i] = dg.x;
+        g[i + 1] = dg.y;
+        u[i] = du.x;
+        u[i + 1] = du.y;
     }
 }
-
-// --------------------------------------------------------------------- products
 
 // Results go from registers to memory, 32 bytes of its row a lane: a whole sector, where the
 // rows begin at one.  (Through shared memory and TMA a warp took 540 cycles for 32 rows of 64
