@@ -962,23 +962,35 @@ gated_top(const uint4 *__restrict__ grad, long long stride, long long tokens, in
 
 constexpr int kFinishThreads = 128;
 
-// grad_x of a token: its partial sums in order, rounded once
+// grad_x: the partial sums in order, rounded once.  A thread takes eight elements and asks for
+// four parts at a time.
 template <bool BF16>
 __global__ void __launch_bounds__(kFinishThreads)
 gated_finish(const float4 *__restrict__ sums, long long tokens, long long rows, int splits, int vecs, uint4 *out, long long stride) {
     pdl_enter();
-    for (long long t = blockIdx.x; t < tokens; t += gridDim.x)
-        for (int v = threadIdx.x; v < vecs; v += kFinishThreads) {
-            float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
-            for (int s = 0; s < splits; ++s) {
-                const float4 *src = sums + ((s * rows + t) * vecs + v) * 2;
-                const float4 a = src[0], b = src[1];
-                lo.x += a.x; lo.y += a.y; lo.z += a.z; lo.w += a.w;
-                hi.x += b.x; hi.y += b.y; hi.z += b.z; hi.w += b.w;
+    const long long all = tokens * vecs;
+    for (long long i = (long long)blockIdx.x * kFinishThreads + threadIdx.x; i < all; i += (long long)gridDim.x * kFinishThreads) {
+        const long long t = i / vecs, v = i - t * vecs;
+        float4 lo = make_float4(0.f, 0.f, 0.f, 0.f), hi = lo;
+        for (int s0 = 0; s0 < splits; s0 += 4) {
+            float4 a[4], b[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (s0 + k >= splits) break;
+                const float4 *src = sums + (((s0 + k) * rows + t) * vecs + v) * 2;
+                a[k] = src[0];
+                b[k] = src[1];
             }
-            out[t * stride + v] = make_uint4(pack_lp<BF16>(lo.x, lo.y), pack_lp<BF16>(lo.z, lo.w), pack_lp<BF16>(hi.x, hi.y),
-                                             pack_lp<BF16>(hi.z, hi.w));
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (s0 + k >= splits) break;
+                lo.x += a[k].x; lo.y += a[k].y; lo.z += a[k].z; lo.w += a[k].w;
+                hi.x += b[k].x; hi.y += b[k].y; hi.z += b[k].z; hi.w += b[k].w;
+            }
         }
+        out[t * stride + v] = make_uint4(pack_lp<BF16>(lo.x, lo.y), pack_lp<BF16>(lo.z, lo.w), pack_lp<BF16>(hi.x, hi.y),
+                                         pack_lp<BF16>(hi.z, hi.w));
+    }
 }
 
 // ------------------------------------------------------------------------ host
@@ -1208,7 +1220,7 @@ cudaError_t backward_impl(const GatedArgs &a, cudaStream_t stream) {
     plan_gradients(p, (int)std::min<int64_t>(gradient_pairs, tiles));
     e = launch_products<BF16, kGradients>(p, tiles, stream);
     if (e == cudaSuccess && l.splits > 1)
-        e = launch_pdl(gated_finish<BF16>, dim3((unsigned)std::min<int64_t>(a.tokens, 8 * sm_count())), dim3(kFinishThreads), 0, stream,
+        e = launch_pdl(gated_finish<BF16>, dim3((unsigned)std::min<int64_t>(up(a.tokens * (a.dim / 8), kFinishThreads) / kFinishThreads, 16 * sm_count())), dim3(kFinishThreads), 0, stream,
                        reinterpret_cast<const float4 *>(sums), (long long)a.tokens, (long long)l.rows, l.splits, a.dim / 8,
                        static_cast<uint4 *>(a.grad_x), (long long)(a.grad_x_stride / 8));
     return e;
