@@ -666,7 +666,7 @@ gated_products(const __grid_constant__ GatedParams p) {
 // and a row of tensor memory holds one f's sums for every token, g's columns before u's.
 // A cluster of CTAs shares a tile's K between them, so that as many CTAs as run at once
 // load at the same time; each then adds up its share of the elements from all of them.
-constexpr int kNarrow = 64;
+constexpr int kNarrow = 128;
 constexpr int kNarrowThreads = 192;          // loads, products, and a warp for each quarter of the lanes
 constexpr int kNarrowSmem = 220 * 1024, kNarrowHalf = 112 * 1024;  // one CTA on an SM, or two
 constexpr int kNarrowWays = 8;               // CTAs of a cluster, at most
@@ -677,9 +677,20 @@ struct NarrowPlan {
     int stages, stage_bytes, ways, tmem, smem;
 };
 
-// Two CTAs on an SM, unless there is more than 16 tokens' worth of sums to exchange and one on
-// each has a way of its own: 48 tokens, 1600 x 4264 12.6 us with two and 10.7 with one, one
-// token 8.6 and 9.2, and 4096 x 10928, whose 86 tiles one on an SM leaves whole, 33.5 and 37.4.
+// Clusters of 1 to 8 CTAs that run at once with one CTA on an SM (cudaOccupancyMaxActiveClusters:
+// what the SMs of a GPC leave room for); with two on each, twice as many.
+constexpr int kClusters[kNarrowWays] = {152, 76, 46, 36, 28, 23, 15, 15};
+
+int ways_of(int64_t tiles, int64_t blocks, int on_each) {
+    int ways = (int)std::max<int64_t>(1, std::min<int64_t>(kNarrowWays, blocks / 2));
+    while (ways > 1 && tiles > on_each * kClusters[ways - 1]) --ways;
+    return ways;
+}
+
+// One CTA on an SM, with a long ring, if that leaves each tile two of them; else two.  As many ways
+// as run at once: 34 tiles of 25 blocks (1600 x 4264, 24 tokens) 14.4, 10.9, 10.2, 9.9 us
+// with 1 to 4 ways and one CTA on an SM, 15.4 and 21 with 5 and 8, which are two rounds; 86 tiles
+// of 64 (4096 x 10928) 35.7 us whole and 32.2 three ways with two on an SM.
 NarrowPlan narrow_plan(int64_t tokens, int64_t wide, int dim) {
     NarrowPlan n;
     n.columns = (int)up(tokens, 16);
@@ -687,11 +698,24 @@ NarrowPlan narrow_plan(int64_t tokens, int64_t wide, int dim) {
     n.tmem = 32;
     while (n.tmem < 2 * n.columns) n.tmem *= 2;
     const int64_t tiles = up(wide, kHalf) / kHalf, blocks = up(dim, kTileK) / kTileK;
-    const bool one = n.columns > 16 && tiles <= kPairs;
-    n.smem = one ? kNarrowSmem : kNarrowHalf;
+    n.ways = ways_of(tiles, blocks, 1);
+    // (the sums of more than 64 tokens take more than half an SM's shared memory)
+    n.smem = n.ways > 1 || blocks < 4 || n.columns > 64 ? kNarrowSmem : kNarrowHalf;
+    if (n.smem == kNarrowHalf) n.ways = ways_of(tiles, blocks, 2);
     n.stages = std::min(kNarrowStages, (n.smem - 1024) / n.stage_bytes);
-    n.ways = (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(kNarrowWays, (one ? 2 : 4) * kPairs / tiles), blocks / 2));
     return n;
+}
+
+// Whether so few tokens are better off here than in tiles of 256, by what either takes beyond a
+// launch, in us as measured: here the matrices at 6 TB/s and 0.045 for a token's sums, there 0.3
+// for a block of K in each round of tiles, or the matrices at 4.2 TB/s.  (768 x 2048: 5.8 us here
+// and 7.4 there with 8 tokens, 7.5 and 7.3 with 48; 4088 x 400: 8.6 and 20.3 with 32; 200 x 400:
+// 4.6 and 4.8 with 8, 5.3 and 4.9 with 24.)
+bool few(int64_t tokens, int64_t wide, int dim) {
+    if (tokens > kNarrow) return false;
+    const double bytes = 4.0 * (double)wide * dim, blocks = (double)(up(dim, kTileK) / kTileK);
+    const double rounds = (double)(up(up(2 * wide, kTileN) / kTileN, kPairs) / kPairs);
+    return 0.045 * (double)tokens + bytes / 6.0e6 < std::max(0.3 * blocks * rounds, bytes / 4.2e6);
 }
 
 struct NarrowParams {
@@ -1149,7 +1173,7 @@ cudaError_t launch_narrow(const GatedArgs &a, uint16_t *dg, uint16_t *du, const 
 
 template <bool BF16>
 cudaError_t forward_impl(const GatedArgs &a, cudaStream_t stream) {
-    if (a.tokens <= kNarrow) return launch_narrow<BF16, kForward>(a, nullptr, nullptr, nullptr, stream);
+    if (few(a.tokens, a.wide, a.dim)) return launch_narrow<BF16, kForward>(a, nullptr, nullptr, nullptr, stream);
     const int pairs = pairs_at_once<BF16, kForward>();
     if (pairs < 0) return (cudaError_t)-pairs;
     GatedParams p = {};
@@ -1209,7 +1233,7 @@ cudaError_t backward_impl(const GatedArgs &a, cudaStream_t stream) {
     cudaError_t e = cudaSuccess;
     if (!BF16)
         e = launch_pdl(gated_top, dim3(kTopBlocks), dim3(kTopThreads), 0, stream, p.grad_out, p.grad_stride, (long long)a.tokens, a.wide / 8, tops);
-    if (e == cudaSuccess && a.tokens <= kNarrow)
+    if (e == cudaSuccess && few(a.tokens, a.wide, a.dim))
         e = launch_narrow<BF16, kSlopes>(a, static_cast<uint16_t *>(dg), static_cast<uint16_t *>(du), p.tops, stream);
     else if (e == cudaSuccess)
         e = launch_products<BF16, kSlopes>(p, row_tiles * (up(2 * a.wide, p.step) / p.step), stream);
