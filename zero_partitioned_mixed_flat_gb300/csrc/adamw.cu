@@ -6,7 +6,9 @@
 // Bound by memory: 24 bytes an element and the gradient and copy with 32-bit moments, 12
 // with 8-bit ones.  Everything is read once and written once: a warp takes blocks of 128
 // elements, each lane four of them, holds a whole block in registers and finds the new
-// scales there, so 8-bit moments need no second pass.
+// scales there, so 8-bit moments need no second pass.  On GB300: 124M elements with bf16 gradients
+// and copies 0.526 ms with 32-bit moments (99 % of the measured copy rate), 0.340 ms with 8-bit ones
+// (85 %: issue slots 60 % busy beside the copies); a list of 12 small tensors 5.7 us.
 //
 // 8 bits.  Of a block of 128: m as E4M3 times the block's scale (the largest |m| / 448), the
 // root of v as an unsigned number of three exponent and five mantissa bits times its own (the

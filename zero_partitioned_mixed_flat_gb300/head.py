@@ -1,7 +1,7 @@
 """The head of a training step on torch tensors: residual addition and RMS norm,
-the softmax cross entropy against the vocabulary matrix, their gradients, and
-the clipped, packed gradients (the zero_norm_*, zero_loss_* and zero_clip_* calls
-of include/zero.h).
+the softmax cross entropy against the vocabulary matrix, the gated projections of a
+feed-forward block, their gradients, and the clipped, packed gradients (the zero_norm_*,
+zero_loss_*, zero_gated_* and zero_clip_* calls of include/zero.h).
 
 These functions only allocate outputs and scratch, read strides off the tensors
 and marshal them; the arithmetic runs in libzero.  Matrices are 2-D float16 or
@@ -13,7 +13,7 @@ them and nothing else.  No graph is recorded: the *_backward functions are the
 gradients, to be called by hand or from a torch.autograd.Function, and a matrix
 or vector that requires grad is refused while gradients are enabled (clip_gradients
 takes its tensors as numbers).  Wrong shapes, types or devices raise ZeroError
-(ZERO_EINVAL) before any device work.  A process's first loss call on a device
+(ZERO_EINVAL) before any device work.  A process's first loss or gated call on a device
 allocates its status word and waits for the device, so it belongs before a graph
 capture; everything else can be captured.
 """
