@@ -32,7 +32,7 @@ constexpr int kGatedSmem = 1024 + kStages * kStageBytes;
 constexpr int kTileCost = 4;  // blocks of K that starting and storing a tile cost, about
 
 enum Mode { kForward = 0, kSlopes = 1, kGradients = 2 };
-enum Kind { kGates = 0, kGradX = 1, kGradGate = 2, kGradUp = 3 };
+enum Kind { kGates = 0, kGatesEdge = 1, kGradX = 2, kGradGate = 3, kGradUp = 4 };
 
 // Blocks that look for the largest |grad_out|, two on each SM.
 constexpr int kTopBlocks = 304, kTopThreads = 256;
@@ -45,7 +45,7 @@ struct GatedLayout {
 };
 
 // What a tile costs, in blocks of K of 256 columns; starting and storing it take about kTileCost.
-// Fewer columns take (columns + 128) / 384 of a block, as measured (see step_of).
+// Fewer columns take (columns + 128) / 384 of a block, as measured (see plan_gates).
 double tile_cost(double blocks, int64_t columns) { return blocks * (double)(std::min<int64_t>(columns, kTileN) + 128) / 384 + kTileCost; }
 
 // In how many partial sums grad_x comes: it has few tiles and long sums.  As many as leave no
@@ -240,15 +240,15 @@ struct RowWriter {
 
 struct GatedParams {
     CUtensorMap x_k;             // x: boxes 64 of D x 128 tokens
-    CUtensorMap gate_k, up_k;    // matrices: 64 of D x half a tile's columns
+    CUtensorMap gate_k, up_k, gate_k_edge, up_k_edge;  // matrices: 64 of D x half a tile's columns
     CUtensorMap x_mn;            // x: 64 of D x 64 tokens
     CUtensorMap gate_mn, up_mn;  // matrices: 64 of D x 64 of F
     CUtensorMap dg_k, du_k;      // slopes: 64 of F x 128 tokens
     CUtensorMap dg_mn, du_mn;    // slopes: 64 of F x 64 tokens
     long long tokens, rows;
     int wide, dim, splits;
-    int step;  // columns of a tile of both projections
-    int catch_up, start;  // see GatedWork
+    int step, whole, step_edge;  // columns of a tile of both projections, tiles of them, and columns of the others'
+    int catch_up, start;         // see GatedWork
     int act;
     Rows out;                // forward
     Rows dg, du;             // slopes
@@ -264,14 +264,14 @@ struct GatedParams {
 // The work of one launch, and which of it each pair does, in order: every pair-th tile,
 // gradients first the tiles of grad_x, few and long; the pairs that get one fewer of
 // them then take `catch_up` tiles of the matrices' gradients each; the rest of those goes round
-// all pairs from `start` on.  Of either kind the tiles of 256 columns come first and those of
-// the last, fewer columns after them, as what is left over is best made of short ones.
-// plan_gradients chooses catch_up and start.
+// all pairs from `start` on.  Of every kind the tiles of many columns come first and those of
+// fewer after them, as what is left over is best made of short ones.  plan_gates chooses
+// the columns, plan_gradients catch_up and start.
 template <int MODE>
 struct GatedWork {
-    Tiles whole, edge;           // both projections (whole alone); grad_x
+    Tiles whole, edge;           // both projections; grad_x
     Tiles weight, weight_edge;   // gradients of the matrices, gate's rows before up's
-    int step, edge_column;
+    int step, step_edge, edge_column;
     int pair, pairs, n_whole, n_weight, n_weights, weight_m;
     int fuller, catch_up, from, mine;
 
@@ -280,9 +280,14 @@ struct GatedWork {
         pair = blockIdx.x >> 1;
         pairs = gridDim.x >> 1;
         step = p.step;
+        step_edge = p.step_edge;
         if constexpr (MODE != kGradients) {
-            const int wide_tiles = (2 * p.wide + p.step - 1) / p.step;
-            whole.set(row_tiles, wide_tiles, 2 * p.wide, (p.dim + kTileK - 1) / kTileK, 1);
+            const int blocks = (p.dim + kTileK - 1) / kTileK;
+            edge_column = p.whole * p.step;
+            const int left = 2 * p.wide - edge_column;
+            whole.set(row_tiles, p.whole, edge_column, blocks, 1);
+            edge.set(row_tiles, (left + p.step_edge - 1) / p.step_edge, left, blocks, 1);
+            n_whole = whole.size();
         } else {
             const int columns = p.dim / kTileN, last = p.dim % kTileN, some = last ? 1 : 0;
             const int x_blocks = 2 * ((p.wide + kTileK - 1) / kTileK), weight_blocks = (int)((p.tokens + kTileK - 1) / kTileK);
@@ -306,11 +311,18 @@ struct GatedWork {
     __device__ __forceinline__ bool at(int j, Tile &t) const {
         if constexpr (MODE != kGradients) {
             const int i = pair + j * pairs;
-            if (i >= whole.size()) return false;
-            t = whole.at(i, kGates);
-            t.n0 = t.n * step;
-            const int left = (whole.columns - t.n0 + 31) / 32 * 32;
-            t.width = left < step ? left : step;
+            if (i >= n_whole + edge.size()) return false;
+            if (i < n_whole) {
+                t = whole.at(i, kGates);
+                t.n0 = t.n * step;
+                t.width = step;
+            } else {
+                t = edge.at(i - n_whole, kGatesEdge);
+                t.n0 = t.n * step_edge;
+                const int left = (edge.columns - t.n0 + 31) / 32 * 32;
+                t.width = left < step_edge ? left : step_edge;
+                t.n0 += edge_column;
+            }
             return true;
         }
         bool last;
@@ -429,7 +441,8 @@ gated_products(const __grid_constant__ GatedParams p) {
                 // this CTA's rows of A, and its half of the columns of B
                 const int m0 = t.m0 + (int)rank * kHalf, n0 = t.n0 + (int)rank * (t.width / 2);
                 const bool two = MODE != kGradients || t.width > kTileN / 2;  // boxes of 64 columns that hold its half
-                const uint32_t bytes = MODE != kGradients ? 2 * kOperandBytes + work.step * kTileK * 2
+                const bool last = MODE != kGradients && t.kind == kGatesEdge;
+                const uint32_t bytes = MODE != kGradients ? 2 * kOperandBytes + (last ? p.step_edge : p.step) * kTileK * 2
                                                           : 2 * (two ? kBlockBytes : kBlockBytes - kBoxBytes);
                 const int half_k = MODE == kGradients ? (p.wide + kTileK - 1) / kTileK : 0;
                 for (int k = t.k0; k < t.k1; k += kStageBlocks) {
@@ -444,7 +457,7 @@ gated_products(const __grid_constant__ GatedParams p) {
                         if constexpr (MODE != kGradients) {
                             const int kk = (k + i) * kTileK;
                             tma_load(a, &p.x_k, kk, m0, bar);
-                            tma_load(b, rank == 0 ? &p.gate_k : &p.up_k, kk, t.n0 / 2, bar);
+                            tma_load(b, rank == 0 ? (last ? &p.gate_k_edge : &p.gate_k) : (last ? &p.up_k_edge : &p.up_k), kk, t.n0 / 2, bar);
                         } else if (t.kind == kGradX) {
                             const bool second = k + i >= half_k;
                             const int kk = (k + i - (second ? half_k : 0)) * kTileK;
@@ -1100,24 +1113,41 @@ void plan_gradients(GatedParams &p, int pairs) {
     }
 }
 
-// Columns of a tile of both projections: those for which the pairs' rounds take the least time.
-// A block of K takes (step + 128) / 384 of what it takes with 256 columns, as measured: 19
-// rounds of 256 and 24 of 192 (4096 x 4096 x 10928) 400 and 432 us, 15 and 19 (8184 x 1600 x
-// 4264) 134.6 and 140.6, but one round of 128 columns and not of 256 (300 x 1000 x 2000) 9.3
+// Tiles of both projections: `whole` of `step` columns each, then the others of step_edge, so that
+// the last pair ends first.  A block of K takes (columns + 128) / 384 of what it takes with 256, as
+// measured: 19 rounds of 256 and 24 of 192 (4096 x 4096 x 10928) 400 and 432 us, 15 and 19 (8184 x 1600
+// x 4264) 134.6 and 140.6, but one round of 128 columns and not of 256 (300 x 1000 x 2000) 9.3
 // and 11.4, two of 192 and not of 256 (129 x 4088 x 10920) 53.3 and 58.5.
-int step_of(int64_t tokens, int64_t wide, int dim, int pairs) {
-    const int64_t rows = up(tokens, kTileM) / kTileM, blocks = up(dim, kTileK) / kTileK;
-    int best = kTileN;
-    int64_t least = 0;
-    for (int step = kTileN; step >= kTileN / 2; step -= 64) {
-        const int64_t rounds = up(rows * (up(2 * wide, step) / step), pairs) / pairs;
-        const int64_t cost = rounds * (blocks * (step + 128) + kTileCost * 384);
-        if (least == 0 || cost < least) {
-            least = cost;
-            best = step;
+int64_t plan_gates(GatedParams &p, int64_t tokens, int pairs) {
+    const int64_t rows = up(tokens, kTileM) / kTileM, columns = 2 * (int64_t)p.wide;
+    const double blocks = (double)(up(p.dim, kTileK) / kTileK);
+    double best = -1.0;
+    int64_t tiles = 0;
+    const auto look = [&](int64_t step, int64_t whole, int64_t step_edge) {
+        const int64_t left = columns - whole * step, first = whole * rows, others = up(left, step_edge) / step_edge * rows;
+        const double c = tile_cost(blocks, step), c_edge = tile_cost(blocks, std::min(step_edge, up(left, 32)));
+        // pairs with one tile more of the first than the rest; the others' go on behind the last of them
+        const int64_t more = first % pairs, more_edge = others % pairs;
+        const double even = (double)(first / pairs) * c + (double)(others / pairs) * c_edge;
+        double end = even + (more_edge > 0 ? c_edge : 0.0);
+        if (more > 0) end = std::max(end, even + c + (more + more_edge > pairs ? c_edge : 0.0));
+        if (best >= 0.0 && end >= best * 0.995) return;  // nearly the same: as few tiles as that takes
+        best = end;
+        tiles = first + others;
+        p.step = (int)step;
+        p.whole = (int)whole;
+        p.step_edge = (int)step_edge;
+    };
+    for (int64_t step = kTileN; step >= kTileN / 2; step -= 64) {
+        const int64_t all = columns / step, rounds = all * rows / pairs;
+        look(step, all, std::max<int64_t>(64, up(columns - all * step, 32)));
+        for (int64_t less = 0; less < 2 && rounds - less > 0; ++less) {
+            const int64_t whole = (rounds - less) * pairs / rows;
+            if (whole >= all) continue;
+            for (int64_t edge = step - 32; edge >= 96; edge -= 32) look(step, whole, edge);
         }
     }
-    return best;
+    return tiles;
 }
 
 template <bool BF16, int MODE>
@@ -1183,20 +1213,22 @@ cudaError_t forward_impl(const GatedArgs &a, cudaStream_t stream) {
     const int pairs = pairs_at_once<BF16, kForward>();
     if (pairs < 0) return (cudaError_t)-pairs;
     GatedParams p = {};
-    p.step = step_of(a.tokens, a.wide, a.dim, pairs);
+    p.wide = a.wide;
+    p.dim = a.dim;
+    const int64_t tiles = plan_gates(p, a.tokens, pairs);
     if (!encoder() || !make_map(&p.x_k, a.x, a.tokens, a.dim, a.x_stride, a.lp, false, kHalf) ||
         !make_map(&p.gate_k, a.gate, a.wide, a.dim, a.gate_stride, a.lp, false, p.step / 2) ||
-        !make_map(&p.up_k, a.up, a.wide, a.dim, a.up_stride, a.lp, false, p.step / 2))
+        !make_map(&p.up_k, a.up, a.wide, a.dim, a.up_stride, a.lp, false, p.step / 2) ||
+        !make_map(&p.gate_k_edge, a.gate, a.wide, a.dim, a.gate_stride, a.lp, false, p.step_edge / 2) ||
+        !make_map(&p.up_k_edge, a.up, a.wide, a.dim, a.up_stride, a.lp, false, p.step_edge / 2))
         return cudaErrorNotSupported;
     p.out = {static_cast<uint16_t *>(a.out), a.out_stride, a.wide};
     p.tokens = a.tokens;
-    p.wide = a.wide;
-    p.dim = a.dim;
     p.act = a.act;
     p.splits = 1;
     p.status = a.status;
     p.wait_cycles = loss_wait();
-    return launch_products<BF16, kForward>(p, up(a.tokens, kTileM) / kTileM * (up(2 * a.wide, p.step) / p.step), stream);
+    return launch_products<BF16, kForward>(p, tiles, stream);
 }
 
 template <bool BF16>
@@ -1208,20 +1240,22 @@ cudaError_t backward_impl(const GatedArgs &a, cudaStream_t stream) {
     const int pairs = pairs_at_once<BF16, kSlopes>();
     if (pairs < 0) return (cudaError_t)-pairs;
     GatedParams p = {};
-    p.step = step_of(a.tokens, a.wide, a.dim, pairs);
+    p.wide = a.wide;
+    p.dim = a.dim;
+    const int64_t gate_tiles = plan_gates(p, a.tokens, pairs);
     const auto map = [&](CUtensorMap *m, const void *at, int64_t rows, int64_t cols, int64_t stride, int box) {
         return make_map(m, at, rows, cols, stride, a.lp, false, box);
     };
     if (!encoder() || !map(&p.x_k, a.x, a.tokens, a.dim, a.x_stride, kHalf) || !map(&p.gate_k, a.gate, a.wide, a.dim, a.gate_stride, p.step / 2) ||
-        !map(&p.up_k, a.up, a.wide, a.dim, a.up_stride, p.step / 2) || !map(&p.x_mn, a.x, a.tokens, a.dim, a.x_stride, kTileK) ||
+        !map(&p.up_k, a.up, a.wide, a.dim, a.up_stride, p.step / 2) ||
+        !map(&p.gate_k_edge, a.gate, a.wide, a.dim, a.gate_stride, p.step_edge / 2) ||
+        !map(&p.up_k_edge, a.up, a.wide, a.dim, a.up_stride, p.step_edge / 2) || !map(&p.x_mn, a.x, a.tokens, a.dim, a.x_stride, kTileK) ||
         !map(&p.gate_mn, a.gate, a.wide, a.dim, a.gate_stride, kTileK) || !map(&p.up_mn, a.up, a.wide, a.dim, a.up_stride, kTileK) ||
         !map(&p.dg_k, dg, a.tokens, a.wide, l.stride, kHalf) || !map(&p.du_k, du, a.tokens, a.wide, l.stride, kHalf) ||
         !map(&p.dg_mn, dg, a.tokens, a.wide, l.stride, kTileK) || !map(&p.du_mn, du, a.tokens, a.wide, l.stride, kTileK))
         return cudaErrorNotSupported;
     p.tokens = a.tokens;
     p.rows = l.rows;
-    p.wide = a.wide;
-    p.dim = a.dim;
     p.splits = l.splits;
     p.act = a.act;
     p.dg = {static_cast<uint16_t *>(dg), l.stride, a.wide};
@@ -1242,7 +1276,7 @@ cudaError_t backward_impl(const GatedArgs &a, cudaStream_t stream) {
     if (e == cudaSuccess && few(a.tokens, a.wide, a.dim))
         e = launch_narrow<BF16, kSlopes>(a, static_cast<uint16_t *>(dg), static_cast<uint16_t *>(du), p.tops, stream);
     else if (e == cudaSuccess)
-        e = launch_products<BF16, kSlopes>(p, row_tiles * (up(2 * a.wide, p.step) / p.step), stream);
+        e = launch_products<BF16, kSlopes>(p, gate_tiles, stream);
     if (e != cudaSuccess) return e;
     const int64_t tiles = row_tiles * dim_tiles * l.splits + 2 * (up(a.wide, kTileM) / kTileM) * dim_tiles;
     const int gradient_pairs = pairs_at_once<BF16, kGradients>();
