@@ -685,7 +685,8 @@ zero_status zero_clip_gradients(int32_t n_tensors, const void *const *grads, con
  *    number, whose value times the scale is the root of v; the scale is the block's largest root /
  *    (1.96875 / 256).  The step itself uses the new m and root before they are rounded, which
  *    are those of ZERO_MOMENTS_FP32 for the old ones' values (root: the square root, rounded
- *    to float).  Each is then divided by its scale (times the scale's rounded reciprocal) and rounded to one of its two neighbours at random, in proportion: by
+ *    to float).  Each is then divided by its scale (times the scale's rounded reciprocal) and
+ *    rounded to one of its two neighbours at random, in proportion: by
  *    h(i) = mix((i mod 2^32) ^ mix(mix(mix(seed) + t) + i / 2^32)), where i is the element's
  *    place in m and mix takes x to x ^ x >> 16, that times 0x9E3779B1, then x ^ x >> 15, that
  *    times 0xB504F333, then x ^ x >> 16 (all modulo 2^32): up where the fraction that is cut
@@ -698,10 +699,10 @@ zero_status zero_clip_gradients(int32_t n_tensors, const void *const *grads, con
  * coef: a device float (zero_clip_gradients' coef where the gradients are not clipped yet),
  * NULL: 1.  skip: a device int32 (zero_clip_gradients' nonfinite); where it is not 0
  * nothing changes, and the step does not count.  NULL: never.
- * beta1 and beta2 in [0, 1), lr, wd and eps finite, eps >= 0.  1 - beta, 1 - lr wd and the
- * corrections are computed in double and rounded once.  Asynchronous, capturable (a
- * replay is the next step), the same bits from run to run; steps of one state follow
- * each other on a stream. */
+ * beta1 and beta2 in [0, 1); lr, wd, 1 - lr wd and eps finite as floats, eps >= 0, with 8-bit
+ * moments 0 or at least 2^-126.  1 - beta, 1 - lr wd and the corrections are computed in
+ * double and rounded once.  Asynchronous, capturable (a replay is the next step), the same
+ * bits from run to run; steps of one state follow each other on a stream. */
 #define ZERO_MOMENTS_FP32 0
 #define ZERO_MOMENTS_8BIT 1
 zero_status zero_adamw_layout(int32_t n_tensors, const int64_t *lens, int64_t *offsets);

@@ -46,6 +46,13 @@ def test_step_refuses(code, changed):
     refused(code, Z.zero_adamw_step, STEP, changed)
 
 
+@pytest.mark.parametrize("changed", [dict(lr=1e39), dict(lr=-1e39), dict(eps=1e39), dict(lr=1e30, wd=-1e30),
+                                     dict(eps=1e-39), dict(eps=2.0 ** -126 * 0.999)])
+def test_step_refuses_numbers_outside_a_float(changed):
+    """What is infinite as a float, and an eps whose reciprocal is: a moment of 0 times that is NaN, and not 0."""
+    refused(INVALID, Z.zero_adamw_step, STEP, changed)
+
+
 def test_step_refuses_lists_that_do_not_match():
     with pytest.raises(ValueError):
         Z.zero_adamw_step(*{**STEP, "grads": [P]}.values(), stream=0)

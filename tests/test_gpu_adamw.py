@@ -486,3 +486,12 @@ def test_refuses():
     grown = [torch.nn.Parameter(x.clone()) for x in p]
     Z.adamw_step(grown, g, s, 1e-3)      # parameters that require grad are what an optimizer steps
     assert int(s.record[0]) == 1
+
+
+def test_the_smallest_eps():
+    """2^-126 with moments of 0: the elements only decay."""
+    p = [torch.full((300,), 2.0, device="cuda")]
+    for bits in (32, 8):
+        Z.adamw_step(p, [torch.zeros(300, device="cuda")], Z.adamw_state(p, bits), 1e-2, eps=2.0 ** -126, weight_decay=0.5)
+    decay = torch.tensor(1 - 1e-2 * 0.5, dtype=torch.float64).float()
+    assert (p[0].cpu() == decay * (decay * 2.0)).all()

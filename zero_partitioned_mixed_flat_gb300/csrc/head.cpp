@@ -6,6 +6,7 @@
 
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -367,8 +368,11 @@ zero_status zero_adamw_step(int32_t n_tensors, float *const *params, const void 
     if (!record) return refuse(ZERO_EINVAL, "record is NULL");
     if (!aligned(record, 8)) return refuse(ZERO_EALIGN, "record is not 8-byte aligned");
     if (!aligned(coef, 4) || !aligned(skip, 4)) return refuse(ZERO_EALIGN, "coef or skip is not 4-byte aligned");
-    if (!std::isfinite(lr) || !std::isfinite(wd) || !(eps >= 0.0) || !std::isfinite(eps))
-        return refuse(ZERO_EINVAL, "lr, wd and eps must be finite and eps >= 0");
+    // (a float's range: beyond it an element whose moments are 0 would become 0 * infinity)
+    if (!(std::fabs(lr) <= FLT_MAX) || !std::isfinite(wd) || !(std::fabs(1.0 - lr * wd) <= FLT_MAX) || !(eps >= 0.0 && eps <= FLT_MAX))
+        return refuse(ZERO_EINVAL, "lr, wd, 1 - lr wd and eps must be finite floats and eps >= 0");
+    if (moments == ZERO_MOMENTS_8BIT && eps > 0.0 && eps < FLT_MIN)
+        return refuse(ZERO_EINVAL, "eps must be 0 or at least 2^-126 with 8-bit moments");
     if (!(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0)) return refuse(ZERO_EINVAL, "beta1 and beta2 must lie in [0, 1)");
     if (!(loss_scale > 0.0f) || !std::isfinite(loss_scale)) return refuse(ZERO_EINVAL, "loss_scale must be finite and > 0");
     const zk::AdamwArgs a = {n_tensors, params, grads, grad_dtype, copies, int(copy_type), lens, moments == ZERO_MOMENTS_8BIT,
