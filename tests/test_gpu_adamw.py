@@ -488,6 +488,20 @@ def test_refuses():
     assert int(s.record[0]) == 1
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_what_an_iterator_gives(bits):
+    """Tensors that nobody else holds, the same step as of a list of them."""
+    a, b = Case([300, 40, 5000], bits, BF, BF), Case([300, 40, 5000], bits, BF, BF)
+    for x, y in zip(a.params + a.grads, b.params + b.grads):
+        y.copy_(x)
+    Z.adamw_step(a.params, [g.float() for g in a.grads], a.state, 1e-3, copies=a.copies)
+    Z.adamw_step((p.view(-1) for p in b.params), (g.float() for g in b.grads), b.state, 1e-3, copies=tuple(b.copies))
+    for x, y in zip(a.params + a.copies, b.params + b.copies):
+        assert torch.equal(x, y)
+    for x, y in zip(a.state, b.state):
+        assert x is None or torch.equal(x, y)
+
+
 def test_the_smallest_eps():
     """2^-126 with moments of 0: the elements only decay."""
     p = [torch.full((300,), 2.0, device="cuda")]

@@ -170,22 +170,28 @@ PyObject *gated_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
     END_HANDLE_TH_ERRORS
 }
 
-// A list of contiguous tensors of one type on the device.
+// A list of contiguous tensors of one type on the device, which it holds until the call ends: an
+// iterator's may be the last there are, and a list may be another thread's, too.
 struct List {
     std::vector<int64_t> lens;
     std::vector<void *> at;
     at::ScalarType type = at::kFloat;
+    PyObject *held = nullptr;
+
+    List() = default;
+    List(const List &) = delete;
+    List &operator=(const List &) = delete;
+    ~List() { Py_XDECREF(held); }
 
     bool take(const char *where, const char *name, PyObject *list, const char *types, bool floats, bool lps, long device) {
-        PyObject *fast = PySequence_Fast(list, "a list of tensors is expected");
-        if (!fast) return false;
-        const Py_ssize_t n = PySequence_Fast_GET_SIZE(fast);
-        PyObject **items = PySequence_Fast_ITEMS(fast);
+        held = PySequence_Tuple(list);
+        if (!held) return false;
+        const Py_ssize_t n = PyTuple_GET_SIZE(held);
         lens.resize(n);
         at.resize(n);
         bool ok = true;
         for (Py_ssize_t i = 0; ok && i < n; ++i) {
-            const at::Tensor *t = tensor(items[i]);
+            const at::Tensor *t = tensor(PyTuple_GET_ITEM(held, i));
             ok = t && here(*t, device) && t->is_contiguous() &&
                  (i == 0 ? (floats && t->scalar_type() == at::kFloat) || (lps && lp_of(t->scalar_type()) >= 0) : t->scalar_type() == type);
             if (!ok) break;
@@ -193,7 +199,6 @@ struct List {
             lens[i] = t->numel();
             at[i] = t->data_ptr();
         }
-        Py_DECREF(fast);
         return ok || refuse(where, "%s must be contiguous tensors of one type (%s) on the current CUDA device", name, types);
     }
 };
