@@ -461,19 +461,18 @@ EncodeTiled encoder() {
 
 // rows x cols elements (lp, or float) at p, read or written in boxes of 128
 // bytes x box_rows with the 128-byte swizzle; what lies outside reads as zero.
-// (half: boxes of 64 bytes with the 64-byte swizzle)
-bool make_map(CUtensorMap *m, const void *p, int64_t rows, int64_t cols, int64_t stride, int lp, bool f32, int box_rows, bool half = false) {
+bool make_map(CUtensorMap *m, const void *p, int64_t rows, int64_t cols, int64_t stride, int lp, bool f32, int box_rows) {
     const int size = f32 ? 4 : 2;
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     const cuuint64_t strides[1] = {(cuuint64_t)(stride * size)};
-    const cuuint32_t box[2] = {(cuuint32_t)((half ? 64 : 128) / size), (cuuint32_t)box_rows};
+    const cuuint32_t box[2] = {(cuuint32_t)(128 / size), (cuuint32_t)box_rows};
     const cuuint32_t ones[2] = {1, 1};
     const CUtensorMapDataType type = f32  ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                      : lp ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                           : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
     const auto encode = [&] {
         return encoder()(m, type, 2, const_cast<void *>(p), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                         half ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
     };
     if (encode()) return true;
