@@ -1140,7 +1140,9 @@ void plan_gradients(GatedParams &p, int pairs) {
 // the last pair ends first.  A block of K takes (columns + 128) / 384 of what it takes with 256, as
 // measured: 19 rounds of 256 and 24 of 192 (4096 x 4096 x 10928) 400 and 432 us, 15 and 19 (8184 x 1600
 // x 4264) 134.6 and 140.6, but one round of 128 columns and not of 256 (300 x 1000 x 2000) 9.3
-// and 11.4, two of 192 and not of 256 (129 x 4088 x 10920) 53.3 and 58.5.
+// and 11.4, two of 192 and not of 256 (129 x 4088 x 10920) 53.3 and 58.5.  With narrower ones for what
+// whole rounds leave: 129 x 4088 x 10920 52.4 -> 48.8, 2048 x 1600 x 4264 36.6 -> 35.2, 700 x 2000 x
+// 5000 26.8 -> 24.8.
 int64_t plan_gates(GatedParams &p, int64_t tokens, int pairs) {
     const int64_t rows = up(tokens, kTileM) / kTileM, columns = 2 * (int64_t)p.wide;
     const double blocks = (double)(up(p.dim, kTileK) / kTileK);
