@@ -34,6 +34,11 @@ constexpr int kTileCost = 4;  // blocks of K that starting and storing a tile co
 enum Mode { kForward = 0, kSlopes = 1, kGradients = 2 };
 enum Kind { kGates = 0, kGatesEdge = 1, kGradX = 2, kGradGate = 3, kGradUp = 4 };
 
+// Where the workspace's regions begin: slopes and partial sums leave in sectors of 32 bytes, each
+// written by one store that asks for that alignment, and a warp's rows in lines.  A workspace
+// is any 16-byte boundary, so the calls round it up to this and ask for that much more.
+constexpr int64_t kBase = 128, kBaseSlack = kBase - 16;
+
 // Blocks that look for the largest |grad_out|, two on each SM.
 constexpr int kTopBlocks = 304, kTopThreads = 256;
 
@@ -41,7 +46,8 @@ struct GatedLayout {
     int64_t rows;   // tokens rounded up to whole tiles
     int64_t stride; // of the slopes' rows: whole sectors
     int splits;     // partial sums of grad_x
-    int64_t slope_gate, slope_up, sums, bytes;  // byte offsets
+    int64_t slope_gate, slope_up, sums;  // byte offsets from the rounded-up workspace
+    int64_t bytes;                       // that a workspace needs wherever it begins
 };
 
 // What a tile costs, in blocks of K of 256 columns; starting and storing it take about kTileCost.
@@ -80,7 +86,7 @@ GatedLayout gated_layout(int64_t tokens, int64_t wide, int dim) {
     l.slope_gate = take(tokens * l.stride * 2);
     l.slope_up = take(tokens * l.stride * 2);
     l.sums = take(l.splits > 1 ? l.splits * l.rows * dim * 4 : 0);
-    l.bytes = at;
+    l.bytes = at + kBaseSlack;
     return l;
 }
 
@@ -1259,7 +1265,7 @@ cudaError_t forward_impl(const GatedArgs &a, cudaStream_t stream) {
 template <bool BF16>
 cudaError_t backward_impl(const GatedArgs &a, cudaStream_t stream) {
     const GatedLayout l = gated_layout(a.tokens, a.wide, a.dim);
-    char *ws = static_cast<char *>(a.workspace);
+    char *ws = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(a.workspace) + (kBase - 1)) & ~uintptr_t(kBase - 1));
     float *tops = reinterpret_cast<float *>(ws), *sums = reinterpret_cast<float *>(ws + l.sums);
     void *dg = ws + l.slope_gate, *du = ws + l.slope_up;
     const int pairs = pairs_at_once<BF16, kSlopes>();
