@@ -693,7 +693,9 @@ zero_status zero_clip_gradients(int32_t n_tensors, const void *const *grads, con
  *    off and ((h mod 2^16) + 1/2) / 2^16 (m) or (h / 2^16 + 1/2) / 2^16 (the root) make
  *    one together.  A root above 0 has a code of at least 1, 2^-12 of the block's largest root.
  *    A scale below 2^-126 is 0, and so are its codes.  A
- *    block with a value that is not finite has a NaN scale and codes 0.
+ *    block with a value that is not finite has a NaN scale and codes 0: also where only v is,
+ *    after a finite g' beyond 2^64, whose own step is that of ZERO_MOMENTS_FP32 (an update of 0)
+ *    while all of the block's parameters are NaN from the next one on.
  * record: two int64 of device memory (8-byte aligned), zero at first: record[0] is the
  * number of steps taken, which the call counts up; record[1] belongs to the call.
  * coef: a device float (zero_clip_gradients' coef where the gradients are not clipped yet),

@@ -136,13 +136,19 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 // approximation and one step with an exact remainder (P. Markstein, "Computation of elementary
 // functions on the IBM RISC System/6000 processor", IBM J. Res. Dev. 34(1), 1990); equal to the
 // IEEE operations for every mantissa.  (Those intrinsics, with their branches for all other
-// numbers, made 124M elements 512 us and not 479; two numbers an operation 456.)  The root of 0 is 0; below 2^-126 it is only near.
+// numbers, made 124M elements 512 us and not 479; two numbers an operation 456.)  The root of 0 is 0, that of infinity NaN;
+// below 2^-126 it is only near.
 __device__ __forceinline__ float2 roots_of(float2 x) {
     float2 y;
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(fmaxf(x.x, 0x1p-126f)));
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(fmaxf(x.y, 0x1p-126f)));
     const float2 s = mul2(x, y), minus = mul2(x, make_float2(-y.x, -y.y));
     return fma2(fma2(minus, s, x), mul2(y, both(0.5f)), s);
+}
+// Such roots with infinity's own: x / 2^64 is below the root of everything finite.
+__device__ __forceinline__ float2 any_roots_of(float2 x) {
+    const float2 r = roots_of(x), least = mul2(x, both(0x1p-64f));
+    return make_float2(fmaxf(r.x, least.x), fmaxf(r.y, least.y));
 }
 __device__ __forceinline__ float reciprocal_of(float x) {
     const float r = rcp_approx(x);
@@ -154,6 +160,11 @@ __device__ __forceinline__ float larger(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
     return r;
+}
+
+// the bits of a block's largest root, of the lanes' four each
+__device__ __forceinline__ uint32_t largest_root(const float (&r)[4]) {
+    return __reduce_max_sync(0xffffffffu, __float_as_uint(larger(larger(larger(r[0], r[1]), r[2]), r[3])));
 }
 
 // the scale of a block whose largest magnitude has these bits, and its reciprocal
@@ -397,7 +408,7 @@ struct Span {
                 put(i, w);
             } else {
                 // What lies behind a tensor's end has gradient and codes 0, and keeps them.
-                float m[4], r[4], top_m = 0.0f, top_r = 0.0f;
+                float m[4], r[4], v[4];
                 m_values(mc[i], m);
                 root_values(vc[i], r);
                 const float2 old_m = both(ms[i]), old_r = both(vs[i]);
@@ -408,22 +419,36 @@ struct Span {
                     const float2 f = mul2(make_float2(grad[k], grad[k + 1]), both(s.factor));
                     const float2 root = mul2(make_float2(r[k], r[k + 1]), old_r);
                     const float2 m2 = add2(mul2(both(c.beta1), mul2(make_float2(m[k], m[k + 1]), old_m)), mul2(both(c.omb1), f));
-                    const float2 r2 = roots_of(add2(mul2(both(c.beta2), mul2(root, root)), mul2(both(c.omb2), mul2(f, f))));
-                    const float2 denominator = fma2(r2, both(rs2), both(c.eps));
-                    const float2 part = mul2(mul2(both(-lr1), m2), make_float2(rcp_approx(denominator.x), rcp_approx(denominator.y)));
+                    const float2 v2 = add2(mul2(both(c.beta2), mul2(root, root)), mul2(both(c.omb2), mul2(f, f)));
+                    const float2 r2 = roots_of(v2);
+                    m[k] = m2.x;
+                    m[k + 1] = m2.y;
+                    v[k] = v2.x;
+                    v[k + 1] = v2.y;
+                    r[k] = r2.x;
+                    r[k + 1] = r2.y;
+                }
+                const float top_m = larger(larger(larger(larger(0.0f, m[0]), m[1]), m[2]), m[3]);
+                const uint32_t bits_m = __reduce_max_sync(0xffffffffu, __float_as_uint(top_m));
+                uint32_t bits_r = largest_root(r);
+                if (bits_r >= 0x7f800000u) {  // some v is infinite, or NaN
+#pragma unroll
+                    for (int k = 0; k < 4; k += 2) {
+                        const float2 r2 = any_roots_of(make_float2(v[k], v[k + 1]));
+                        r[k] = r2.x;
+                        r[k + 1] = r2.y;
+                    }
+                    bits_r = largest_root(r);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; k += 2) {
+                    const float2 denominator = fma2(make_float2(r[k], r[k + 1]), both(rs2), both(c.eps));
+                    const float2 part = mul2(mul2(both(-lr1), make_float2(m[k], m[k + 1])), make_float2(rcp_approx(denominator.x), rcp_approx(denominator.y)));
                     const float2 p2 = fma2(make_float2(w[k], w[k + 1]), both(c.decay), part);
                     w[k] = p2.x;
                     w[k + 1] = p2.y;
-                    m[k] = m2.x;
-                    m[k + 1] = m2.y;
-                    r[k] = r2.x;
-                    r[k + 1] = r2.y;
-                    top_m = larger(larger(top_m, m2.x), m2.y);
-                    top_r = larger(larger(top_r, r2.x), r2.y);
                 }
                 put(i, w);
-                const uint32_t bits_m = __reduce_max_sync(0xffffffffu, __float_as_uint(top_m));
-                const uint32_t bits_r = __reduce_max_sync(0xffffffffu, __float_as_uint(top_r));
                 float inv_m, inv_r;
                 const float scale_m = scale_of(bits_m, 1.0f / kTopM, inv_m), scale_r = scale_of(bits_r, 1.0f / kTopR, inv_r);
                 const unsigned long long place = (unsigned long long)(block + i) * kBlock;
