@@ -137,7 +137,7 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 // functions on the IBM RISC System/6000 processor", IBM J. Res. Dev. 34(1), 1990); equal to the
 // IEEE operations for every mantissa.  (Those intrinsics, with their branches for all other
 // numbers, made 124M elements 512 us and not 479; two numbers an operation 456.)  The root of 0 is 0, that of infinity NaN;
-// below 2^-126 it is only near.
+// below 2^-96 the remainder loses bits, and below 2^-126 the result may be far too small.
 __device__ __forceinline__ float2 roots_of(float2 x) {
     float2 y;
     asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y.x) : "f"(fmaxf(x.x, 0x1p-126f)));
@@ -145,10 +145,13 @@ __device__ __forceinline__ float2 roots_of(float2 x) {
     const float2 s = mul2(x, y), minus = mul2(x, make_float2(-y.x, -y.y));
     return fma2(fma2(minus, s, x), mul2(y, both(0.5f)), s);
 }
-// Such roots with infinity's own: x / 2^64 is below the root of everything finite.
+// The same of any numbers: what is below 2^-96 is scaled by 2^64 and its root by 2^-32, both exactly; x / 2^64 is below the
+// root of everything finite, and infinity's own.
 __device__ __forceinline__ float2 any_roots_of(float2 x) {
-    const float2 r = roots_of(x), least = mul2(x, both(0x1p-64f));
-    return make_float2(fmaxf(r.x, least.x), fmaxf(r.y, least.y));
+    const bool small_x = x.x < 0x1p-96f, small_y = x.y < 0x1p-96f;
+    const float2 r = roots_of(mul2(x, make_float2(small_x ? 0x1p64f : 1.0f, small_y ? 0x1p64f : 1.0f)));
+    const float2 root = mul2(r, make_float2(small_x ? 0x1p-32f : 1.0f, small_y ? 0x1p-32f : 1.0f)), least = mul2(x, both(0x1p-64f));
+    return make_float2(fmaxf(root.x, least.x), fmaxf(root.y, least.y));
 }
 __device__ __forceinline__ float reciprocal_of(float x) {
     const float r = rcp_approx(x);
@@ -385,6 +388,12 @@ struct Span {
     }
 
     __device__ __forceinline__ void step(const Moments &st, const AdamwScalars &c, const StepScalars &s, float lr1, float rs2, int lane) {
+        // Blocks whose largest root is NaN, or 0 < root < `least`, take their roots by any_roots_of.  roots_of
+        // is wrong below 2^-48 only, and by less than 2^-63.  Where the block's largest is 2^-34 or more, such a root's code is
+        // 1 whatever it is, and an eps of 2^-38 rs2 or more hides it in the update: with a smaller eps every
+        // block's roots are taken so.  (124M elements 457 -> 456 us, nothing; any_roots_of everywhere 474, a test of every
+        // element 472, the intrinsic in the rare branch 465.)
+        const uint32_t least = c.eps >= rs2 * 0x1p-38f ? 0x2e800000u : 0x7f800000u;
         uint32_t key = BITS == 8 ? mix(s.key + (uint32_t)((unsigned long long)block * kBlock >> 32)) : 0u;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -431,7 +440,7 @@ struct Span {
                 const float top_m = larger(larger(larger(larger(0.0f, m[0]), m[1]), m[2]), m[3]);
                 const uint32_t bits_m = __reduce_max_sync(0xffffffffu, __float_as_uint(top_m));
                 uint32_t bits_r = largest_root(r);
-                if (bits_r >= 0x7f800000u) {  // some v is infinite, or NaN
+                if (bits_r != 0u && bits_r - least >= 0x7f800000u - least) {
 #pragma unroll
                     for (int k = 0; k < 4; k += 2) {
                         const float2 r2 = any_roots_of(make_float2(v[k], v[k + 1]));
