@@ -87,7 +87,10 @@ struct Gated {
     Matrix x, gate, up;
 
     bool take(const char *where, PyObject *const *a, long device) {
-        return x.take(where, "x", a[0], device, nullptr, -1, -1) && gate.take(where, "gate", a[1], device, &x, -1, x.cols) &&
+        if (!x.take(where, "x", a[0], device, nullptr, -1, -1)) return false;
+        // (libzero takes 32 bits of it)
+        if (x.cols > ZERO_HEAD_MAX_DIM) return refuse(where, "x has %lld columns, at most %d are allowed", (long long)x.cols, ZERO_HEAD_MAX_DIM);
+        return gate.take(where, "gate", a[1], device, &x, -1, x.cols) &&
                up.take(where, "up", a[2], device, &x, gate.rows, x.cols);
     }
 };
@@ -244,8 +247,8 @@ PyObject *adamw_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
         !grads.take(where, "grads", a[1], "float16, bfloat16 or float32", true, true, device) ||
         (copied && !copies.take(where, "copies", a[2], "float16 or bfloat16", false, true, device)))
         return nullptr;
-    if (params.lens.empty()) {
-        refuse(where, "no parameters");
+    if (params.lens.empty() || params.lens.size() > INT32_MAX) {
+        refuse(where, params.lens.empty() ? "no parameters" : "more than 2^31 - 1 parameters");
         return nullptr;
     }
     if (grads.lens != params.lens || (copied && copies.lens != params.lens)) {
