@@ -82,6 +82,8 @@ def _matrix(where, name, t, dtype=None, shape=None):
     if dtype is not None and t.dtype != dtype:
         _refuse(where, "%s is %s, expected %s" % (name, t.dtype, dtype))
     rows, cols = t.shape
+    if cols > A.ZERO_HEAD_MAX_DIM:      # libzero takes 32 bits of it
+        _refuse(where, "%s has %d columns, at most %d are allowed" % (name, cols, A.ZERO_HEAD_MAX_DIM))
     if shape is not None and (rows, cols) != shape:
         _refuse(where, "%s is %d x %d, expected %d x %d" % (name, rows, cols, *shape))
     s0, s1 = t.stride()
@@ -173,6 +175,8 @@ def dequantize_rows(codes, scales, fmt, dtype, stream=None):
     if codes.ndim != 2 or codes.dtype != torch.int8 or codes.get_device() != device or not codes.is_contiguous():
         _refuse(where, "codes must be a contiguous 2-D int8 tensor on the current CUDA device")
     rows, dim = codes.shape
+    if dim > A.ZERO_HEAD_MAX_DIM:
+        _refuse(where, "codes has %d columns, at most %d are allowed" % (dim, A.ZERO_HEAD_MAX_DIM))
     if (dtype not in _LP or scales.dtype != torch.float32 or scales.get_device() != device
             or scales.shape != (rows, -(-dim // A.ZERO_QUANT_BLOCK)) or not scales.is_contiguous()):
         _refuse(where, "scales must be one float32 per block of a row, dtype float16 or bfloat16")
