@@ -5,7 +5,8 @@ its moments held in 32 or in 8 bits.
     adamw_step(params, grads, state, lr, weight_decay=0.01, copies=weights)
 
 params: contiguous float32 CUDA tensors of any shape, updated in place (parameters that
-require grad as well: an update is no part of a graph); grads: one contiguous tensor each of
+require grad as well: an update is no part of a graph, but counts as one to a backward pass
+that saved what it writes); grads: one contiguous tensor each of
 the same length, all float16, bfloat16 or float32; copies: one each, all float16 or bfloat16,
 that take the rounded parameters.  Any of them may be parts of flat buffers, at any
 element.  A state is a tuple of tensors that belong to the caller, so it is saved, moved and

@@ -49,6 +49,12 @@ const at::Tensor *tensor(PyObject *o) { return THPVariable_Check(o) ? &THPVariab
 
 bool here(const at::Tensor &t, long device) { return t.layout() == at::kStrided && t.is_cuda() && t.get_device() == device; }
 
+// A call wrote to the tensor: a backward pass that saved it before has to find out.  (Inference
+// tensors have no version.)
+void written(const at::Tensor &t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 struct Matrix {
     const at::Tensor *t = nullptr;
     int64_t rows = 0, cols = 0, stride = 0;
@@ -158,6 +164,8 @@ PyObject *gated_backward(PyObject *, PyObject *const *a, Py_ssize_t n) {
                                stride[1], at[2], stride[2], status, space.data_ptr(), need, stream);
     Py_END_ALLOW_THREADS
     if (!called(code, "zero_gated_backward")) return nullptr;
+    for (const Matrix &m : given)
+        if (m.t) written(*m.t);
     PyObject *out = PyTuple_New(3);
     for (int i = 0; out && i < 3; ++i) {
         PyObject *t = a[8 + i];
@@ -185,6 +193,10 @@ struct List {
     List(const List &) = delete;
     List &operator=(const List &) = delete;
     ~List() { Py_XDECREF(held); }
+
+    void all_written() const {
+        for (Py_ssize_t i = 0; held && i < PyTuple_GET_SIZE(held); ++i) written(*tensor(PyTuple_GET_ITEM(held, i)));
+    }
 
     bool take(const char *where, const char *name, PyObject *list, const char *types, bool floats, bool lps, long device) {
         held = PySequence_Tuple(list);
@@ -290,6 +302,10 @@ PyObject *adamw_step(PyObject *, PyObject *const *a, Py_ssize_t n) {
                            stream);
     Py_END_ALLOW_THREADS
     if (!called(code, "zero_adamw_step")) return nullptr;
+    params.all_written();
+    copies.all_written();
+    for (int i = 0; i < 5; ++i)
+        if (i < 2 || i == 4 || eight) written(*tensor(s[i]));
     Py_RETURN_NONE;
     END_HANDLE_TH_ERRORS
 }
