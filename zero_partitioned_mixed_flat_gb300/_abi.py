@@ -130,8 +130,14 @@ def tensors():
         load()
         path = os.path.join(os.path.dirname(LIB_PATH), "_tensors.so")
         if not os.path.exists(path):
+            why = os.path.splitext(path)[0] + ".error"
+            if os.path.exists(why):
+                with open(why) as f:
+                    why = f.read()
+            else:
+                why = "no build has tried to"
             raise ImportError("_tensors.so is not built (%s): run "
-                              "`python -m zero_partitioned_mixed_flat_gb300.build`" % path)
+                              "`python -m zero_partitioned_mixed_flat_gb300.build`\n%s" % (path, why))
         spec = importlib.util.spec_from_file_location("_tensors", path)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)

@@ -6,7 +6,9 @@ Compiles csrc/*.cu and csrc/*.cpp with nvcc in parallel and links
 zero_partitioned_mixed_flat_gb300/_lib/libzero.so (CUDA runtime linked
 statically, so the library loads without a GPU; device calls need one), and, where
 torch is installed, the Python module _lib/_tensors.so (csrc/tensors.cc, g++)
-that calls it on torch tensors.
+that calls it on torch tensors.  The library does not depend on the module: where
+the module's compiler, Python's headers or torch's are missing, the build says so
+and leaves _lib/_tensors.error, which the calls that need the module raise.
 """
 import hashlib
 import importlib.util
@@ -15,6 +17,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -24,6 +27,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libzero.so")
 TENSORS = os.path.join(OUT_DIR, "_tensors.so")
+TENSORS_ERROR = os.path.join(OUT_DIR, "_tensors.error")   # why there is no module
 TENSORS_SRC = os.path.join(CSRC, "tensors.cc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
@@ -62,69 +66,105 @@ def _tensors_commands(torch_dir, out):
     return compile_it, link
 
 
-def _fingerprint(srcs) -> str:
+def _digest(files, *texts) -> str:
     h = hashlib.sha256()
-    torch_dir = _torch_dir()
-    for f in [TENSORS_SRC] + ([os.path.join(torch_dir, "version.py")] if torch_dir else []):
-        with open(f, "rb") as fh:
-            h.update(fh.read())
-    h.update(sys.version.encode())
-    for f in srcs + sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))) \
-            + [os.path.join(INCLUDE, "zero.h"), os.path.abspath(__file__)]:
+    for f in files:
         h.update(f.encode())
         with open(f, "rb") as fh:
             h.update(fh.read())
-    h.update(" ".join(COMMON + DEVICE).encode())
+    for text in texts:
+        h.update(text.encode())
     return h.hexdigest()
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    srcs = _sources()
-    fp = _fingerprint(srcs)
-    stamp = os.path.join(OUT_DIR, "libzero.stamp")
-    torch_dir = _torch_dir()
-    if not force and os.path.exists(LIB) and (not torch_dir or os.path.exists(TENSORS)) and os.path.exists(stamp):
-        with open(stamp) as f:
-            if f.read().strip() == fp:
-                return LIB
-    os.makedirs(OUT_DIR, exist_ok=True)
+def _fingerprint(srcs) -> str:
+    headers = sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh")))
+    return _digest(srcs + headers + [os.path.join(INCLUDE, "zero.h"), os.path.abspath(__file__)], " ".join(COMMON + DEVICE))
+
+
+def _tensors_fingerprint(torch_dir) -> str:
+    return _digest([TENSORS_SRC, os.path.join(INCLUDE, "zero.h"), os.path.abspath(__file__), os.path.join(torch_dir, "version.py")],
+                   sys.version)
+
+
+def _stamp(target):
+    return os.path.splitext(target)[0] + ".stamp"
+
+
+def _current(target, fp) -> bool:
+    """Whether the target was built from what fp stands for."""
+    if not os.path.exists(target) or not os.path.exists(_stamp(target)):
+        return False
+    with open(_stamp(target)) as f:
+        return f.read().strip() == fp
+
+
+def _done(target, fp):
+    with open(_stamp(target), "w") as f:
+        f.write(fp)
+
+
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("%s:\n%s%s" % (what, r.stdout, r.stderr))
+    return r.stdout + r.stderr
+
+
+def _build_library(srcs, verbose):
     tool = nvcc()
-    objs = []
 
     def compile_one(src):
         obj = os.path.join(OUT_DIR, os.path.basename(src) + ".o")
         cmd = [tool, *COMMON, "-c", src, "-o", obj]
         if src.endswith(".cu"):
             cmd[1:1] = DEVICE
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError("nvcc failed on %s:\n%s%s" % (src, r.stdout, r.stderr))
-        if verbose and (r.stdout or r.stderr):
-            print(r.stdout + r.stderr)
+        said = _run(cmd, "nvcc failed on %s" % src)
+        if verbose and said:
+            print(said)
         return obj
 
-    def run(cmd):
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError("%s failed:\n%s%s" % (" ".join(cmd[:4]), r.stdout, r.stderr))
-
-    compile_tensors, link_tensors = _tensors_commands(torch_dir, TENSORS + ".tmp.%d" % os.getpid()) if torch_dir else (None, None)
-    with ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
-        module = ex.submit(run, compile_tensors) if torch_dir else None
+    with ThreadPoolExecutor(max_workers=len(srcs)) as ex:
         objs = list(ex.map(compile_one, srcs))
-        if module:
-            module.result()
     tmp = LIB + ".tmp.%d" % os.getpid()
-    cmd = [tool, "-shared", *ARCH, "-o", tmp, *objs, "-cudart", "static", "-lrt", "-ldl", "-lpthread"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError("link failed:\n%s%s" % (r.stdout, r.stderr))
+    _run([tool, "-shared", *ARCH, "-o", tmp, *objs, "-cudart", "static", "-lrt", "-ldl", "-lpthread"], "link failed")
     os.replace(tmp, LIB)
-    if torch_dir:
-        run(link_tensors)
-        os.replace(link_tensors[link_tensors.index("-o") + 1], TENSORS)
-    with open(stamp, "w") as f:
-        f.write(fp)
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    srcs = _sources()
+    torch_dir = _torch_dir()
+    fp, tensors_fp = _fingerprint(srcs), _tensors_fingerprint(torch_dir) if torch_dir else None
+    library = force or not _current(LIB, fp)
+    module = torch_dir and (force or not _current(TENSORS, tensors_fp))
+    if not library and not module:
+        return LIB
+    os.makedirs(OUT_DIR, exist_ok=True)
+    with ThreadPoolExecutor(max_workers=1) as ex:
+        if module:
+            tmp = TENSORS + ".tmp.%d" % os.getpid()
+            compile_it, link = _tensors_commands(torch_dir, tmp)
+            compiled = ex.submit(_run, compile_it, "g++ failed on %s" % TENSORS_SRC)
+        if library:
+            _build_library(srcs, verbose)
+            _done(LIB, fp)
+        if module:
+            try:
+                compiled.result()
+                _run(link, "link of _tensors.so failed")
+                os.replace(tmp, TENSORS)
+            except (RuntimeError, OSError) as e:   # OSError: no such compiler
+                for stale in (TENSORS, _stamp(TENSORS)):    # of an earlier source: not to be loaded
+                    if os.path.exists(stale):
+                        os.remove(stale)
+                with open(TENSORS_ERROR, "w") as f:
+                    f.write(str(e))
+                warnings.warn("libzero is built, its module for torch tensors is not (gated_linear, adamw_step): %s" % e,
+                              RuntimeWarning, stacklevel=2)
+            else:
+                if os.path.exists(TENSORS_ERROR):
+                    os.remove(TENSORS_ERROR)
+                _done(TENSORS, tensors_fp)
     return LIB
 
 
