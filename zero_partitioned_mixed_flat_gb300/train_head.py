@@ -153,14 +153,16 @@ def train_whole(steps=60, vocab=64, dim=128, tokens=2048, lr=2e-2, clip=1.0, see
 def main():
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     ap.add_argument("--steps", type=int, default=60)
-    ap.add_argument("--ranks", type=int, default=2)
+    ap.add_argument("--ranks", type=int, help="partitions of the ZeRO step (2)")
     ap.add_argument("--wide", type=int, default=0, help="width of a gated block (a multiple of 8; 0: none)")
     ap.add_argument("--moments", type=int, choices=(8, 32), help="AdamW over whole tensors with moments of so many bits")
     args = ap.parse_args()
+    if args.moments and args.ranks not in (None, 1):
+        ap.error("--moments takes one rank's step over whole tensors: no --ranks")
     if args.moments:
         losses = train_whole(args.steps, wide=args.wide, bits=args.moments)
     else:
-        losses = train(args.steps, args.ranks, wide=args.wide)
+        losses = train(args.steps, 2 if args.ranks is None else args.ranks, wide=args.wide)
     for i in range(0, len(losses), max(1, len(losses) // 10)):
         print("step %4d  loss %.4f" % (i, losses[i]))
     print("step %4d  loss %.4f" % (len(losses) - 1, losses[-1]))
