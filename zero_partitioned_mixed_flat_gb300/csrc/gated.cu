@@ -1302,6 +1302,7 @@ cudaError_t backward_impl(const GatedArgs &a, cudaStream_t stream) {
     p.wait_cycles = loss_wait();
     const int64_t row_tiles = l.rows / kTileM, dim_tiles = up(a.dim, kTileN) / kTileN;
     cudaError_t e = cudaSuccess;
+    // (nothing may come between gated_top and the slopes, whose loads do not wait for it: launch.h)
     if (!BF16)
         e = launch_pdl(gated_top, dim3(kTopBlocks), dim3(kTopThreads), 0, stream, p.grad_out, p.grad_stride, (long long)a.tokens, a.wide / 8, tops);
     if (e == cudaSuccess && few(a.tokens, a.wide, a.dim))

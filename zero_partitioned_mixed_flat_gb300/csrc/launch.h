@@ -6,10 +6,15 @@
 // until the previous kernel in the stream has completed and its writes are
 // visible (griddepcontrol.wait), then lets the next kernel of the stream begin
 // launching (griddepcontrol.launch_dependents).  No global memory is read or
-// written before the wait, so the stream order of the step is kept exactly
-// (loss_join reads what the kernel before it reads too, and says why it may);
+// written before the wait, so the stream order of the step is kept exactly;
 // what overlaps is the next kernel's launch and CTA start-up with the
-// previous kernel's last CTAs.  A dependent grid launches only after every
+// previous kernel's last CTAs.  Two kernels read without it what the kernel
+// before them only reads too: loss_join, and the load and product warps of
+// gated.cu's fp16 slopes, which never wait while the others do.  Either may
+// because one kernel of its own source file always stands directly before it in the
+// stream, writes none of that, and lets dependents start only after its own
+// wait, when all that came earlier has completed: nothing may be launched
+// between the two, and that kernel may not let dependents start any earlier.  A dependent grid launches only after every
 // CTA of the previous grid has started and passed pdl_enter(), so waiting
 // dependents can never keep a CTA of the grid they wait for off the SMs.  A
 // kernel launched without the attribute (or after a non-kernel stream
