@@ -8,7 +8,7 @@
 // elements, each lane four of them, holds a whole block in registers and finds the new
 // scales there, so 8-bit moments need no second pass.  On GB300: 124M elements with bf16 gradients
 // and copies 0.526 ms with 32-bit moments (99 % of the measured copy rate), 0.340 ms with 8-bit ones
-// (85 %: issue slots 60 % busy beside the copies); a list of 12 small tensors 5.7 us.
+// (85 %: issue slots 73 % busy beside the copies); a list of 12 small tensors 5.7 us.
 //
 // 8 bits.  Of a block of 128: m as E4M3 times the block's scale (the largest |m| / 448), the
 // root of v as an unsigned number of three exponent and five mantissa bits times its own (the
@@ -37,7 +37,7 @@ constexpr int kBlock = ZERO_QUANT_BLOCK;  // a warp's 32 lanes x 4
 // Blocks of 128 that a warp has in flight, 16 or 12 elements a lane, in one block of 16 warps on an
 // SM.  More warps with less in flight each are slower: 117M elements with 32-bit moments 525 us
 // so, 541 and 617 us with two and three blocks of 256 that take 2 at a time, 982 us with
-// eight that take 1; 124M with 8-bit moments and their values 479 us, 499 with two
+// eight that take 1; 124M with 8-bit moments and their values 479 us then (454 now), 499 with two
 // blocks of 256, 528 with 3 at a time, 531 with 24 warps that take 2.
 template <int BITS>
 constexpr int kDepth = BITS == 8 ? 4 : 3;

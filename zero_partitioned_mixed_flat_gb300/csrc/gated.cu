@@ -10,6 +10,10 @@
 // nor u is ever stored.  Backward keeps nothing of the forward pass but x: it computes g
 // and u again (4 T D F operations beside the 8 of the gradients), writes dg and du in lp
 // and takes the three products in one launch: gx's sum runs over dg's columns and then du's.
+// dg and du are rounded because the tensor core takes both operands in one type of 16 bits (f16's kind):
+// two parts of each would keep twice the bits for 16 and not 8 T D F operations, which is what bounds
+// the larger sizes.  It leaves the gradients sqrt(2) times as far off as their own rounding (of bf16
+// gradients 0.0023 of their norm, and 0.0017): what a chain of separate products in lp rounds, too.
 //
 // On GB300: forward 8184 x 1600 x 4264 (T x D x F) 0.142 ms (1570 TFLOP/s; 0.127 cold), one token
 // 4096 x 10928 30 us (6.0 TB/s), 48 tokens 1600 x 4264 8.9 us; forward and gradients 4096 x 4096 x
